@@ -26,6 +26,7 @@ FASTOCR_ERR_ALIGN = -6
 FASTOCR_DTYPE_F32 = 0
 FASTOCR_DTYPE_BF16 = 1
 DEV_BAD_PAGE, DEV_BAD_SEQLEN, DEV_BAD_IMG, DEV_BAD_SELECTION, DEV_INTERNAL = 1, 2, 4, 8, 16
+DEV_BAD_GROUP, DEV_BAD_WEIGHTS = 32, 64
 
 
 class fastocr_dims(ctypes.Structure):
@@ -42,6 +43,17 @@ class fastocr_kv(ctypes.Structure):
                 ("num_pages", ctypes.c_int32)]
 
 
+class fastocr_groups(ctypes.Structure):
+    _fields_ = [("start", ctypes.c_void_p), ("prefix_len", ctypes.c_void_p),
+                ("n", ctypes.c_int32), ("max_prefix", ctypes.c_int32)]
+
+
+class fastocr_weights(ctypes.Structure):
+    _fields_ = [("mass", ctypes.c_void_p), ("pos", ctypes.c_void_p),
+                ("protect", ctypes.c_void_p), ("seen", ctypes.c_void_p),
+                ("logits", ctypes.c_void_p), ("stride", ctypes.c_int32)]
+
+
 class FastOCRError(RuntimeError):
     def __init__(self, fn: str, status: int):
         super().__init__(f"{fn}: {status_string(status)} (status {status})")
@@ -54,7 +66,7 @@ def _load() -> ctypes.CDLL:
             f"{LIB_PATH} is not built; run `python dynamic_sparse_kv_gb300/build.py` "
             "(or __graft_entry__.build()) -- there is no CPU fallback")
     lib = ctypes.CDLL(LIB_PATH)
-    P, I32, F64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_double
+    P, I32, I64, F64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_double
     sigs = {
         "fastocr_abi_version": ([], I32),
         "fastocr_status_string": ([I32], ctypes.c_char_p),
@@ -70,6 +82,15 @@ def _load() -> ctypes.CDLL:
         "fastocr_sparse_attend_ex": ([P, P, ctypes.POINTER(fastocr_kv), P, P, I32, P, P,
                                       ctypes.c_uint32, P], I32),
         "fastocr_rswa_attend": ([P, P, ctypes.POINTER(fastocr_kv), I32, I32, P, P], I32),
+        "fastocr_rows_workspace": ([P, I64], I64),
+        "fastocr_shared_attend": ([P, P, ctypes.POINTER(fastocr_kv),
+                                   ctypes.POINTER(fastocr_groups),
+                                   ctypes.POINTER(fastocr_weights), P, P, I64, P], I32),
+        "fastocr_weigh_attend": ([P, P, ctypes.POINTER(fastocr_kv),
+                                  ctypes.POINTER(fastocr_weights), P, P], I32),
+        "fastocr_evict": ([P, ctypes.POINTER(fastocr_kv), ctypes.POINTER(fastocr_weights), I32,
+                           I32, P, P], I32),
+        "fastocr_cross_attend": ([P, P, ctypes.POINTER(fastocr_kv), P, I64, P, P, I64, P], I32),
         "fastocr_profiler_reset": ([P, P], I32),
         "fastocr_profiler_select": ([P, I32, ctypes.POINTER(I32), ctypes.POINTER(F64), P], I32),
         "fastocr_profiler_read": ([P, ctypes.POINTER(F64), P], I32),
@@ -203,6 +224,58 @@ def fastocr_rswa_attend(handle, q, kv: fastocr_kv, prefix_len, window, out, stre
     _check("fastocr_rswa_attend",
            lib.fastocr_rswa_attend(handle, _ptr(q), ctypes.byref(kv), int(prefix_len),
                                    int(window), _ptr(out), _stream(stream)))
+
+
+def fastocr_rows_workspace(handle, rows) -> int:
+    """Workspace bytes of fastocr_shared_attend / fastocr_cross_attend over `rows` query tokens."""
+    n = lib.fastocr_rows_workspace(handle, int(rows))
+    if n < 0:
+        raise FastOCRError("fastocr_rows_workspace", int(n))
+    return n
+
+
+def make_groups(start, prefix_len, max_prefix=0) -> fastocr_groups:
+    """Groups of sequences that share a prefix; keeps no reference to the tensors."""
+    return fastocr_groups(_ptr(start), _ptr(prefix_len), int(start.shape[0]) - 1, int(max_prefix))
+
+
+def make_weights(mass, pos, protect, seen, logits) -> fastocr_weights:
+    """One layer's weights; keeps no reference to the tensors."""
+    return fastocr_weights(_ptr(mass), _ptr(pos), _ptr(protect), _ptr(seen), _ptr(logits),
+                           int(mass.shape[-1]))
+
+
+def fastocr_shared_attend(handle, q, kv: fastocr_kv, groups: fastocr_groups, out, ws, ws_bytes,
+                          weights: fastocr_weights | None = None, stream=None) -> None:
+    """Decode attention with a prefix shared by groups of sequences, read once a group."""
+    w = ctypes.byref(weights) if weights is not None else None
+    _check("fastocr_shared_attend",
+           lib.fastocr_shared_attend(handle, _ptr(q), ctypes.byref(kv), ctypes.byref(groups), w,
+                                     _ptr(out), _ptr(ws), int(ws_bytes), _stream(stream)))
+
+
+def fastocr_weigh_attend(handle, q, kv: fastocr_kv, weights: fastocr_weights, out,
+                         stream=None) -> None:
+    """Full attention that adds every row's attention weight to its accumulator."""
+    _check("fastocr_weigh_attend",
+           lib.fastocr_weigh_attend(handle, _ptr(q), ctypes.byref(kv), ctypes.byref(weights),
+                                    _ptr(out), _stream(stream)))
+
+
+def fastocr_evict(handle, kv: fastocr_kv, weights: fastocr_weights, budget, recent, new_len=None,
+                  stream=None) -> None:
+    """Keep `budget` rows behind protect a KV head: recent ones, then the largest weights."""
+    _check("fastocr_evict",
+           lib.fastocr_evict(handle, ctypes.byref(kv), ctypes.byref(weights), int(budget),
+                             int(recent), _ptr(new_len), _stream(stream)))
+
+
+def fastocr_cross_attend(handle, q, kv: fastocr_kv, q_start, rows, out, ws=None, ws_bytes=0,
+                         stream=None) -> None:
+    """Packed, ragged queries against all states of their sequence."""
+    _check("fastocr_cross_attend",
+           lib.fastocr_cross_attend(handle, _ptr(q), ctypes.byref(kv), _ptr(q_start), int(rows),
+                                    _ptr(out), _ptr(ws), int(ws_bytes), _stream(stream)))
 
 
 def fastocr_profiler_reset(handle, stream=None) -> None:

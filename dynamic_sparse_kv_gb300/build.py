@@ -21,8 +21,9 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfastocr.so")
 
-SOURCES = ["abi.cu", "kernels_bf16.cu", "kernels_f32.cu", "noalloc.cu", "probe.cu"]
-HEADERS = ["attend_kernels.cuh", "attend_impl.cuh"]
+SOURCES = ["abi.cu", "abi_rows.cu", "evict.cu", "kernels_bf16.cu", "kernels_f32.cu", "noalloc.cu",
+           "probe.cu", "rows_f32.cu"]
+HEADERS = ["attend_kernels.cuh", "attend_impl.cuh", "evict.cuh", "handle.cuh", "rows.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

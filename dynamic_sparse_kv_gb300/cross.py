@@ -1,0 +1,73 @@
+"""Cross attention of decoder layers to an encoder's states over the C ABI.
+
+The states' keys and values sit in the same paged layout as a decoder's own
+cache (fastocr_cross_attend): each sequence has a length of its own, 0 included,
+and any number of query tokens, packed without padding.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import _native as N
+
+
+class CrossAttention:
+    """Attention of packed queries to encoder states, for a stack of layers.
+
+    k_cache, v_cache: [layers, num_pages, H_kv, page_size, d] (bf16 or fp32)
+    block_table: [B, pages_per_seq] int32; state_len: int or [B] int32, states a
+    sequence has (a device int32 tensor is taken as it is and may change).
+    max_rows: query tokens of the largest call, for the workspace; a larger
+    call works, with its keys split less.
+    """
+
+    def __init__(self, k_cache, v_cache, block_table, state_len, *, q_heads: int, max_rows: int = 0):
+        assert k_cache.is_cuda and k_cache.shape == v_cache.shape
+        self.k_cache, self.v_cache = k_cache, v_cache
+        self.layers, _, self.kv_heads, self.page_size, self.head_dim = k_cache.shape
+        self.q_heads = q_heads
+        dev = k_cache.device
+        self.block_table = block_table.to(device=dev, dtype=torch.int32).contiguous()
+        self.batch = self.block_table.shape[0]
+        if isinstance(state_len, int):
+            state_len = torch.full((self.batch,), state_len, dtype=torch.int32)
+        self.state_len = state_len.to(device=dev, dtype=torch.int32).contiguous()
+        dtype = N.FASTOCR_DTYPE_BF16 if k_cache.dtype == torch.bfloat16 else N.FASTOCR_DTYPE_F32
+        self.handle = N.fastocr_create(self.batch, q_heads, self.kv_heads, self.head_dim, dtype,
+                                       self.page_size, self.block_table.shape[1], 0, self.layers)
+        self.kv = [N.make_kv(k_cache[l], v_cache[l], self.block_table, self.state_len)
+                   for l in range(self.layers)]
+        n = N.fastocr_rows_workspace(self.handle, max_rows)
+        self.ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+
+    def close(self):
+        if self.handle:
+            N.fastocr_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def attend(self, l, q, q_start, out, stream=None):
+        """Layer l: q, out [rows, H_q, d] contiguous; q_start [B + 1] int32 on the
+        device, query tokens q_start[b] .. q_start[b+1]-1 are sequence b's."""
+        rows = q.shape[0]
+        if tuple(q.shape[1:]) != (self.q_heads, self.head_dim) or out.shape != q.shape:
+            raise ValueError(f"q and out must be [rows, {self.q_heads}, {self.head_dim}]")
+        if not (q.is_contiguous() and out.is_contiguous()):
+            raise ValueError("q and out must be contiguous")
+        if q.dtype != self.k_cache.dtype or out.dtype != q.dtype:
+            raise ValueError(f"q and out must be {self.k_cache.dtype}")
+        if tuple(q_start.shape) != (self.batch + 1,) or q_start.dtype != torch.int32 \
+                or not q_start.is_cuda:
+            raise ValueError(f"q_start must be int32 [{self.batch + 1}] on the device")
+        if rows == 0:
+            return
+        N.fastocr_cross_attend(self.handle, q, self.kv[l], q_start, rows, out, self.ws,
+                               self.ws.numel() if self.ws is not None else 0, stream)
+
+    def device_status(self, stream=None) -> int:
+        return N.fastocr_device_status(self.handle, stream)

@@ -1,0 +1,226 @@
+// C ABI of the shared-prefix, weighing, eviction and cross-attention calls
+// (declared in include/fastocr.h): argument checks, splits and launches.
+#include <stdint.h>
+
+#include "evict.cuh"
+#include "handle.cuh"
+#include "rows.cuh"
+
+using namespace fastocr;
+
+namespace {
+
+fastocr_status check_device(const fastocr_handle* h) {
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return FASTOCR_ERR_NO_DEVICE;
+  return dev == h->device ? FASTOCR_OK : FASTOCR_ERR_INVALID;
+}
+
+fastocr_status check_weights(const fastocr_weights* w, bool attend) {
+  if (!w || !w->mass || !w->pos || !w->protect || !w->seen || (attend && !w->logits))
+    return FASTOCR_ERR_NULL;
+  if (w->stride < 1) return FASTOCR_ERR_INVALID;
+  if (attend && !aligned16(w->logits)) return FASTOCR_ERR_ALIGN;
+  return FASTOCR_OK;
+}
+
+void set_weights(const fastocr_weights* w, Params& p) {
+  p.mass = w->mass;
+  p.row_pos = w->pos;
+  p.protect = w->protect;
+  p.seen = w->seen;
+  p.w_logits = w->logits;
+  p.w_stride = w->stride;
+}
+
+RowsParams rows_params(const fastocr_handle* h, const void* q, const fastocr_kv* kv) {
+  RowsParams p;
+  memset(&p, 0, sizeof(p));
+  const fastocr_dims& d = h->dims;
+  p.q = q;
+  p.k = kv->k;
+  p.v = kv->v;
+  p.block_table = kv->block_table;
+  p.seq_len = kv->seq_len;
+  p.num_pages = kv->num_pages;
+  p.max_pages = d.max_pages_per_seq;
+  p.log2_page = h->log2_page;
+  p.Hq = d.num_q_heads;
+  p.Hkv = d.num_kv_heads;
+  p.g = d.num_q_heads / d.num_kv_heads;
+  p.scale_log2 = (float)(1.4426950408889634 / sqrt((double)d.head_dim));
+  p.status = h->status;
+  return p;
+}
+
+// Bytes of one part's partials of `rows` query tokens.
+int64_t part_bytes(const fastocr_handle* h, int64_t rows) {
+  return rows * h->dims.num_q_heads * (int64_t)(h->dims.head_dim + 2) * (int64_t)sizeof(float);
+}
+
+// Query rows a CTA holds.
+int tile_rows(const fastocr_handle* h) { return kRowsF32; }
+
+// Parts the keys are cut into when about `tiles` row tiles a KV head run at
+// once: enough CTAs for every SM.
+int most_parts(const fastocr_handle* h, int64_t tiles) {
+  const int64_t items = std::max<int64_t>(1, tiles) * h->dims.num_kv_heads;
+  return (int)std::min<int64_t>(kMaxExt, std::max<int64_t>(1, h->num_sms / items));
+}
+
+int choose_parts(const fastocr_handle* h, int64_t tiles, long keys, int64_t ws_bytes, int64_t rows) {
+  const long key_tiles = std::max(1L, (keys + kKeyTile - 1) / kKeyTile);
+  int64_t s = std::min<int64_t>(most_parts(h, tiles), key_tiles);
+  if (rows > 0) s = std::min<int64_t>(s, ws_bytes / part_bytes(h, rows));
+  return (int)std::max<int64_t>(1, s);
+}
+
+fastocr_status launch_rows(const fastocr_handle* h, const RowsParams& p, cudaStream_t s) {
+  const cudaError_t e = h->dims.dtype == FASTOCR_DTYPE_BF16 ? launch_rows_bf16(h->dims.head_dim, p, s)
+                                                            : launch_rows_f32(h->dims.head_dim, p, s);
+  return e == cudaSuccess ? FASTOCR_OK : FASTOCR_ERR_CUDA;
+}
+
+// Places the partials in the caller's workspace: outputs first (16-byte
+// aligned), then the row statistics.
+void place_parts(const fastocr_handle* h, void* ws, RowsParams& p) {
+  p.acc = static_cast<float*>(ws);
+  p.ml = p.acc + (size_t)p.splits * p.rows * p.Hq * h->dims.head_dim;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t fastocr_rows_workspace(const fastocr_handle* h, int64_t rows) {
+  if (!h) return FASTOCR_ERR_NULL;
+  if (rows < 0 || rows * h->dims.num_q_heads >= (1LL << 31)) return FASTOCR_ERR_INVALID;
+  const int bm = tile_rows(h);
+  const int g = h->dims.num_q_heads / h->dims.num_kv_heads;
+  return part_bytes(h, rows) * most_parts(h, (rows * g + bm - 1) / bm);
+}
+
+fastocr_status fastocr_shared_attend(fastocr_handle* h, const void* q, const fastocr_kv* kv,
+                                     const fastocr_groups* groups, const fastocr_weights* weights,
+                                     void* out, void* ws, int64_t ws_bytes, fastocr_stream stream) {
+  if (!h || !q || !out || !groups || !groups->start || !groups->prefix_len || !ws)
+    return FASTOCR_ERR_NULL;
+  fastocr_status st = check_kv(h, kv);
+  if (st != FASTOCR_OK) return st;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(ws)) return FASTOCR_ERR_ALIGN;
+  const int64_t B = h->dims.batch;
+  if (groups->n < 1 || groups->n > B || groups->max_prefix < 0) return FASTOCR_ERR_INVALID;
+  if (weights && (st = check_weights(weights, true)) != FASTOCR_OK) return st;
+  if (ws_bytes < part_bytes(h, B)) return FASTOCR_ERR_INVALID;
+  if ((st = check_device(h)) != FASTOCR_OK) return st;
+
+  const long all = expected_tokens(h);
+  const long prefix = groups->max_prefix > 0 ? std::min<long>(groups->max_prefix, all) : all;
+  RowsParams r = rows_params(h, q, kv);
+  r.n_groups = groups->n;
+  r.start = groups->start;
+  r.prefix_len = groups->prefix_len;
+  r.rows = B;
+  const int bm = tile_rows(h);
+  const int64_t tiles = std::max<int64_t>(groups->n, (B * r.g + bm - 1) / bm);
+  r.splits = choose_parts(h, tiles, prefix, ws_bytes, B);
+  place_parts(h, ws, r);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if ((st = launch_rows(h, r, s)) != FASTOCR_OK) return st;
+
+  Params p = base_params(h, q, kv, out);
+  p.first = groups->prefix_len;
+  p.ext_acc = r.acc;
+  p.ext_ml = r.ml;
+  p.ext_splits = r.splits;
+  if (weights) set_weights(weights, p);
+  return launch(h, weights ? kWeigh : kTail, std::max(1L, all - (groups->max_prefix > 0 ? prefix : 0)),
+                p, stream);
+}
+
+fastocr_status fastocr_weigh_attend(fastocr_handle* h, const void* q, const fastocr_kv* kv,
+                                    const fastocr_weights* weights, void* out,
+                                    fastocr_stream stream) {
+  if (!h || !q || !out) return FASTOCR_ERR_NULL;
+  fastocr_status st = check_kv(h, kv);
+  if (st != FASTOCR_OK) return st;
+  if (!aligned16(q) || !aligned16(out)) return FASTOCR_ERR_ALIGN;
+  if ((st = check_weights(weights, true)) != FASTOCR_OK) return st;
+  if ((st = check_device(h)) != FASTOCR_OK) return st;
+  Params p = base_params(h, q, kv, out);
+  set_weights(weights, p);
+  return launch(h, kWeigh, expected_tokens(h), p, stream);
+}
+
+fastocr_status fastocr_evict(fastocr_handle* h, const fastocr_kv* kv, const fastocr_weights* weights,
+                             int32_t budget, int32_t recent, int32_t* new_len,
+                             fastocr_stream stream) {
+  if (!h) return FASTOCR_ERR_NULL;
+  fastocr_status st = check_kv(h, kv);
+  if (st != FASTOCR_OK) return st;
+  if ((st = check_weights(weights, false)) != FASTOCR_OK) return st;
+  if (budget < 1 || recent < 0 || recent > budget) return FASTOCR_ERR_INVALID;
+  if (new_len && new_len == kv->seq_len) return FASTOCR_ERR_INVALID;
+  const int rows = (int)std::min<long>(weights->stride, max_tokens(h));
+  if (rows > (long)kEvictSlice * kEvictCluster) return FASTOCR_ERR_UNSUPPORTED;
+  if ((st = check_device(h)) != FASTOCR_OK) return st;
+  EvictParams p;
+  memset(&p, 0, sizeof(p));
+  const fastocr_dims& d = h->dims;
+  p.k = static_cast<char*>(const_cast<void*>(kv->k));
+  p.v = static_cast<char*>(const_cast<void*>(kv->v));
+  p.block_table = kv->block_table;
+  p.seq_len = kv->seq_len;
+  p.num_pages = kv->num_pages;
+  p.max_pages = d.max_pages_per_seq;
+  p.log2_page = h->log2_page;
+  p.B = d.batch;
+  p.Hkv = d.num_kv_heads;
+  p.row_bytes = d.head_dim * (d.dtype == FASTOCR_DTYPE_BF16 ? 2 : 4);
+  p.mass = weights->mass;
+  p.pos = weights->pos;
+  p.protect = weights->protect;
+  p.seen = weights->seen;
+  p.stride = weights->stride;
+  p.budget = budget;
+  p.recent = recent;
+  p.new_len = new_len;
+  p.status = h->status;
+  p.cluster = 1;
+  while (p.cluster < kEvictCluster &&
+         ((long)p.cluster * kEvictSlice < rows ||
+          ((long)p.cluster * p.B * p.Hkv < h->num_sms && rows / p.cluster > 1024)))
+    p.cluster *= 2;
+  p.slice = (rows + p.cluster - 1) / p.cluster;
+  return launch_evict(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FASTOCR_OK
+                                                                           : FASTOCR_ERR_CUDA;
+}
+
+fastocr_status fastocr_cross_attend(fastocr_handle* h, const void* q, const fastocr_kv* kv,
+                                    const int32_t* q_start, int64_t rows, void* out, void* ws,
+                                    int64_t ws_bytes, fastocr_stream stream) {
+  if (!h || !q || !out || !q_start) return FASTOCR_ERR_NULL;
+  fastocr_status st = check_kv(h, kv);
+  if (st != FASTOCR_OK) return st;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(ws)) return FASTOCR_ERR_ALIGN;
+  if (rows < 0 || ws_bytes < 0 || rows * h->dims.num_q_heads >= (1LL << 31))
+    return FASTOCR_ERR_INVALID;
+  if ((st = check_device(h)) != FASTOCR_OK) return st;
+  if (rows == 0) return FASTOCR_OK;
+  RowsParams p = rows_params(h, q, kv);
+  p.out = out;
+  p.n_groups = h->dims.batch;
+  p.start = q_start;
+  p.rows = rows;
+  const int bm = tile_rows(h);
+  const int64_t tiles = std::max<int64_t>(std::min<int64_t>(p.n_groups, rows), (rows * p.g + bm - 1) / bm);
+  p.splits = choose_parts(h, tiles, expected_tokens(h), ws ? ws_bytes : 0, rows);
+  if (p.splits > 1) place_parts(h, ws, p);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if ((st = launch_rows(h, p, s)) != FASTOCR_OK || p.splits == 1) return st;
+  return launch_rows_merge(h->dims.head_dim, h->dims.dtype == FASTOCR_DTYPE_BF16, p, s) == cudaSuccess
+             ? FASTOCR_OK
+             : FASTOCR_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -296,6 +296,29 @@ __device__ __forceinline__ CtaList make_cta_list(const Params& p, int b, int spl
     if (MODE == kFull || MODE == kFocal || MODE == kProfile) {
       len1 = n_t - 1;
       in_set = 1;
+    } else if (MODE == kTail || MODE == kWeigh) {
+      int f = p.first ? __ldcg(p.first + b) : 0;
+      if (f < 0 || f > n_t) {
+        bad |= kDevBadGroup;
+        f = f < 0 ? 0 : n_t;
+      }
+      a1 = f;
+      len1 = max(0, cur - f);
+      in_set = cur >= f;
+      if constexpr (MODE == kWeigh) {   // the weighed rows take the image's place
+        int pr = __ldcg(p.protect + b);
+        if (pr < f) {
+          bad |= kDevBadWeights;
+          pr = f;
+        }
+        int rows = max(0, n_t - pr);
+        if (rows > p.w_stride) {
+          bad |= kDevBadWeights;
+          rows = p.w_stride;
+        }
+        c.img_start = pr;
+        c.n_img = rows;
+      }
     } else if (MODE == kRswa) {
       const int pre = min(p.prefix_len, n_t);
       if (cur < p.prefix_len) {
@@ -721,6 +744,8 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
   float* logit_base = nullptr;
   if (MODE == kFocal)
     logit_base = p.logits + ((size_t)b * p.Hkv + hkv) * (size_t)p.max_img * kSlots;
+  if constexpr (MODE == kWeigh)
+    logit_base = p.w_logits + ((size_t)b * p.Hkv + hkv) * (size_t)p.w_stride * kSlots;
 
   if constexpr (kMma) {
 #pragma unroll
@@ -799,7 +824,7 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
     const float s1 = posA >= 0 ? cfr[1] * p.scale_log2 : kNegInf;
     const float s2 = posB >= 0 ? cfr[2] * p.scale_log2 : kNegInf;
     const float s3 = posB >= 0 ? cfr[3] * p.scale_log2 : kNegInf;
-    if (MODE == kFocal) {
+    if (stores_logits(MODE)) {
       if (posA >= c.img_start && posA < c.img_start + c.n_img)
         *reinterpret_cast<float2*>(logit_base + (size_t)(posA - c.img_start) * kSlots + 2 * tig) =
             make_float2(s0, s1);
@@ -846,7 +871,7 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
     // probabilities themselves, so there it adds the unrounded values; so does
     // a profiling layer, whose image mass is a ratio of such sums.
     const uint32_t pk01 = pack_bf16(p0, p1), pk23 = pack_bf16(p2, p3);
-    if (MODE == kFocal || MODE == kProfile) {
+    if (stores_logits(MODE) || MODE == kProfile) {
       sm_.l[0] += p0 + p2;
       sm_.l[1] += p1 + p3;
       if constexpr (MODE == kProfile) {
@@ -955,7 +980,7 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
           s[h] += __shfl_xor_sync(0xffffffffu, s[h], 16);
           s[h] = pos >= 0 ? s[h] * p.scale_log2 : kNegInf;
         }
-        if (MODE == kFocal) {
+        if (stores_logits(MODE)) {
           if (half == 0 && pos >= c.img_start && pos < c.img_start + c.n_img) {
             float* dst = logit_base + (size_t)(pos - c.img_start) * kSlots;
             *reinterpret_cast<float4*>(dst) = make_float4(s[0], s[1], s[2], s[3]);
@@ -1013,6 +1038,52 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
   float* wl = reinterpret_cast<float*>(smem + E::kWl);
   float* wacc = reinterpret_cast<float*>(smem + E::kWacc);
   float* wil = reinterpret_cast<float*>(smem + E::kWil);   // profile mode
+  // tail: (max, sum) of the partials another kernel formed of the rows before
+  // this list, per head; read by every merging thread after the barrier below
+  constexpr bool kExternal = MODE == kTail || MODE == kWeigh;
+  float2* xml = reinterpret_cast<float2*>(smem + E::kExt);   // [8][kMaxExt]
+  const size_t q_row0 = (size_t)b * p.Hq + (size_t)hkv * p.g;
+  const size_t q_rows = (size_t)p.B * p.Hq;
+  if constexpr (kExternal) {
+    for (int e = tid; e < p.g * p.ext_splits; e += kThreads) {
+      const int h = e % p.g, s = e / p.g;
+      xml[h * kMaxExt + s] =
+          __ldcg(reinterpret_cast<const float2*>(p.ext_ml) + (size_t)s * q_rows + q_row0 + h);
+    }
+  }
+  // joins head h's external maxima to M, and sum(l * 2^(m - base)) over them
+  auto ext_max = [&](int h, float M) -> float {
+    if constexpr (kExternal)
+      for (int s = 0; s < p.ext_splits; ++s) M = fmaxf(M, xml[h * kMaxExt + s].x);
+    return M;
+  };
+  auto ext_sum = [&](int h, float base) -> float {
+    float L = 0.f;
+    if constexpr (kExternal)
+      for (int s = 0; s < p.ext_splits; ++s) {
+        const float2 ml = xml[h * kMaxExt + s];
+        L = fmaf(ml.y, fast_exp2(ml.x - base), L);
+      }
+    return L;
+  };
+  // adds partials s0, s0 + step, ... of output dims 4*c4.. of head h; one
+  // whose sum is 0 has no rows and its output was not written
+  auto ext_add = [&](int h, int c4, float base, int s0, int step, float4& a) {
+    if constexpr (kExternal) {
+      const float4* src = reinterpret_cast<const float4*>(p.ext_acc) + (q_row0 + h) * (D / 4) + c4;
+#pragma unroll 4
+      for (int s = s0; s < p.ext_splits; s += step) {
+        const float2 ml = xml[h * kMaxExt + s];
+        if (ml.y == 0.f) continue;
+        const float4 v = __ldcg(src + (size_t)s * q_rows * (D / 4));
+        const float sc = fast_exp2(ml.x - base);
+        a.x = fmaf(v.x, sc, a.x);
+        a.y = fmaf(v.y, sc, a.y);
+        a.z = fmaf(v.z, sc, a.z);
+        a.w = fmaf(v.w, sc, a.w);
+      }
+    }
+  };
   if constexpr (kMma) {
     const float l0 = warp_sum_gid(sm_.l[0]), l1 = warp_sum_gid(sm_.l[1]);
     const int h0 = warp * kSlots + 2 * tig, h1 = h0 + 1;
@@ -1063,11 +1134,11 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
   // of them, loaded now so that the load latency hides behind the merge
   constexpr int kSgU = 8;   // image tokens a thread scores per round (16 loads in flight)
   const int img_end = c.img_start + c.n_img;
-  // a focal text list is [0, N_t - 1): text index = position
-  const int sg_lo = max(c.txt_lo, c.img_start) - c.img_start;
-  const int sg_hi = min(c.txt_lo + c.n_txt, img_end) - c.img_start;
+  // a focal or weighing text list is one range from a1 on
+  const int sg_lo = max(c.a1 + c.txt_lo, c.img_start) - c.img_start;
+  const int sg_hi = min(c.a1 + c.txt_lo + c.n_txt, img_end) - c.img_start;
   float4 sgx[kSgU][2];
-  if constexpr (MODE == kFocal) {
+  if constexpr (stores_logits(MODE)) {
 #pragma unroll
     for (int u = 0; u < kSgU; ++u) {
       const int i = sg_lo + u * kThreads + tid;
@@ -1080,10 +1151,14 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
   const int S = p.splits;
   constexpr int C4 = D / 4;
   const int n_pairs = p.g * C4;
-  auto warp_scales = [&](int h, float sc[kWarps]) -> float {   // CTA max of head h
+  // max of head h over the CTA, and the scales of its warps' partials to it
+  // (a single CTA, S == 1, also joins the external partials here)
+  auto warp_scales = [&](int h, float sc[kWarps]) -> float {
     float M = kNegInf;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) M = fmaxf(M, wm[w * kSlots + h]);
+    if constexpr (kExternal)
+      if (S == 1) M = ext_max(h, M);
     const float base = M == kNegInf ? 0.f : M;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) sc[w] = fast_exp2(wm[w * kSlots + h] - base);
@@ -1110,7 +1185,7 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
     for (int e = tid; e < n_pairs; e += kThreads) {
       const int h = e / C4, c4 = e % C4;
       float sc[kWarps];
-      warp_scales(h, sc);
+      const float M = warp_scales(h, sc);
       float L = 0.f;
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -1122,15 +1197,21 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
         a.z = fmaf(v.z, sc[w], a.z);
         a.w = fmaf(v.w, sc[w], a.w);
       }
+      if constexpr (kExternal) {
+        const float base = M == kNegInf ? 0.f : M;
+        L += ext_sum(h, base);
+        ext_add(h, c4, base, 0, 1, a);
+      }
       const float inv = L > 0.f ? __frcp_rn(L) : 0.f;
       store_pair(e, make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv));
     }
-    if (MODE == kFocal && tid < kSlots) {
+    if (stores_logits(MODE) && tid < p.g) {
       float sc[kWarps];
       const float M = warp_scales(tid, sc);
       float L = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) L = fmaf(wl[w * kSlots + tid], sc[w], L);
+      if constexpr (kExternal) L += ext_sum(tid, M == kNegInf ? 0.f : M);
       sM[tid] = M == kNegInf ? 0.f : M;
       sInvL[tid] = L > 0.f ? __frcp_rn(L) : 0.f;
     }
@@ -1207,10 +1288,12 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
       float M = kNegInf;
 #pragma unroll
       for (int s = 0; s < kMaxSplits; ++s) M = fmaxf(M, ms[s]);
+      M = ext_max(h, M);
       base = M == kNegInf ? 0.f : M;
       float L = 0.f;
 #pragma unroll
       for (int s = 0; s < kMaxSplits; ++s) L = fmaf(ls[s], fast_exp2(ms[s] - base), L);
+      if constexpr (kExternal) L += ext_sum(h, base);
       inv = L > 0.f ? __frcp_rn(L) : 0.f;
     };
     // G adjacent lanes share one output pair, each summing every G-th partial
@@ -1235,6 +1318,14 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
           acc.z = fmaf(v.z, sc, acc.z);
           acc.w = fmaf(v.w, sc, acc.w);
         }
+        if constexpr (kExternal) {
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+          ext_add(h, e % C4, base, sub, G, x);
+          acc.x = fmaf(x.x, inv, acc.x);
+          acc.y = fmaf(x.y, inv, acc.y);
+          acc.z = fmaf(x.z, inv, acc.z);
+          acc.w = fmaf(x.w, inv, acc.w);
+        }
       }
       for (int o = 1; o < G; o <<= 1) {
         acc.x += __shfl_xor_sync(0xffffffffu, acc.x, o);
@@ -1244,7 +1335,7 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
       }
       if (ok && sub == 0) store_pair(e, acc);
     }
-    if (MODE == kFocal && tid < kSlots) head_stats(tid, sM[tid], sInvL[tid]);
+    if (stores_logits(MODE) && tid < p.g) head_stats(tid, sM[tid], sInvL[tid]);
     if constexpr (MODE == kProfile) {
       // this CTA's share of the unit's image mass: its image sums rescaled to
       // the heads' max over the cluster, over the heads' sum over the cluster
@@ -1269,9 +1360,10 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
   }
 
   // ---------------- focal: scores of the image tokens this CTA streamed
+  // (weigh: weights of its rows, added to what the accumulator holds)
   // (its text share; the last CTA also the current token) from the logits it
   // wrote itself and the heads' final max and sum: no other CTA's writes read
-  if constexpr (MODE == kFocal) {
+  if constexpr (stores_logits(MODE)) {
     __syncthreads();
     float Mh[kSlots], iL[kSlots];
 #pragma unroll
@@ -1288,7 +1380,7 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
       return sg;
     };
     const size_t unit = (size_t)b * p.Hkv + hkv;
-    float* sp = p.sigma_part + unit * p.max_img;
+    float* sp = MODE == kWeigh ? p.mass + unit * p.w_stride : p.sigma_part + unit * p.max_img;
     for (int i0 = sg_lo; i0 < sg_hi; i0 += kSgU * kThreads) {
       if (i0 > sg_lo) {   // later blocks of kSgU*kThreads tokens
 #pragma unroll
@@ -1303,13 +1395,14 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
       for (int u = 0; u < kSgU; ++u) {
         const int i = i0 + u * kThreads + tid;
         const float sg = score(sgx[u][0], sgx[u][1]);
-        if (i < sg_hi) sp[i] = sg;
+        if (i < sg_hi) sp[i] = MODE == kWeigh ? sp[i] + sg : sg;
       }
     }
     if (c.has_cur && tid == 0 && c.cur_pos >= c.img_start && c.cur_pos < img_end) {
       const int i = c.cur_pos - c.img_start;
       const float4* src4 = reinterpret_cast<const float4*>(logit_base + (size_t)i * kSlots);
-      sp[i] = score(__ldcg(src4), __ldcg(src4 + 1));
+      sp[i] = score(__ldcg(src4), __ldcg(src4 + 1));   // weigh: the row starts here
+      if constexpr (MODE == kWeigh) p.row_pos[unit * p.w_stride + i] = __ldcg(p.seen + b) - 1;
     }
   }
 }
@@ -1370,6 +1463,8 @@ cudaError_t prepare_modes() {
   if ((e = prepare_attend(attend_kernel<T, D, kFocal, V>, bytes))) return e;
   if ((e = prepare_attend(attend_kernel<T, D, kSparse, V>, bytes))) return e;
   if ((e = prepare_attend(attend_kernel<T, D, kProfile, V>, bytes))) return e;
+  if ((e = prepare_attend(attend_kernel<T, D, kTail, V>, bytes))) return e;
+  if ((e = prepare_attend(attend_kernel<T, D, kWeigh, V>, bytes))) return e;
   return prepare_attend(attend_kernel<T, D, kRswa, V>, bytes);
 }
 
@@ -1456,6 +1551,8 @@ cudaError_t dispatch_variant(int mode, const Params& p, cudaStream_t s) {
     case kSparse: return launch_attend<T, D, kSparse, V>(p, s);
     case kRswa: return launch_attend<T, D, kRswa, V>(p, s);
     case kProfile: return launch_attend<T, D, kProfile, V>(p, s);
+    case kTail: return launch_attend<T, D, kTail, V>(p, s);
+    case kWeigh: return launch_attend<T, D, kWeigh, V>(p, s);
   }
   return cudaErrorInvalidValue;
 }

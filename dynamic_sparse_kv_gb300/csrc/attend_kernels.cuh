@@ -8,6 +8,9 @@
 //   sparse : [0, start) ++ selected image positions ++ [start+N_img, N_t)
 //            (FastOCR, cross-layer propagation / Cross-Step Fixation Reuse)
 //   rswa   : [0, L_m) ++ [max(L_m, N_t - n), N_t)           (Unlimited OCR, R-SWA)
+//   tail   : [first, N_t), merged with partials of [0, first) that another
+//            kernel left in global memory (a prefix shared by several sequences)
+//   weigh  : as tail, and every row's attention weight is added to an accumulator
 //
 // Work decomposition (split-K flash-decode): grid = (splits, H_kv, B); the S
 // splits of one (sequence, KV head) form a thread-block cluster. A CTA owns a
@@ -55,7 +58,11 @@ constexpr int kMaxImg = 16384; // image tokens whose scores fit in shared memory
 // kProfile: full attention that also adds the layer's image-attention mass
 // to the profiler (a warm-up step whose selections are not kept): no logits,
 // no scores, no selection kernel.
-enum Mode : int { kFull = 0, kFocal = 1, kSparse = 2, kRswa = 3, kProfile = 4 };
+// kTail, kWeigh: the rows from `first` on (see Params).
+enum Mode : int { kFull = 0, kFocal = 1, kSparse = 2, kRswa = 3, kProfile = 4, kTail = 5, kWeigh = 6 };
+// Modes whose epilogue turns stored logits into head-summed probabilities.
+__host__ __device__ constexpr bool stores_logits(int mode) { return mode == kFocal || mode == kWeigh; }
+constexpr int kMaxExt = 64;   // partials of another kernel that a tail merges
 
 // device status bits (same values as FASTOCR_DEV_* in fastocr.h)
 constexpr int kDevBadPage = 1;
@@ -63,6 +70,8 @@ constexpr int kDevBadSeqLen = 2;
 constexpr int kDevBadImg = 4;
 constexpr int kDevBadSelection = 8;
 constexpr int kDevInternal = 16;   // a cache row outside the cache reached a copy
+constexpr int kDevBadGroup = 32;
+constexpr int kDevBadWeights = 64;
 
 struct Params {
   const void* q;
@@ -103,6 +112,19 @@ struct Params {
   int variant;               // host: which Variant to launch
   int32_t* status;
   int max_img;
+  // tail / weigh: the list starts at row first[b] (NULL: 0); the softmax over
+  // the rows before it comes as ext_splits partials per query row
+  const int32_t* first;
+  const float* ext_ml;       // [ext_splits, B*H_q, 2]: max (base 2), sum
+  const float* ext_acc;      // [ext_splits, B*H_q, d]: unnormalised output
+  int ext_splits;            // <= kMaxExt; 0: none
+  // weigh: rows [protect[b], N_t) have weights, row r at index r - protect[b]
+  float* mass;               // [B, H_kv, w_stride]
+  int32_t* row_pos;          // [B, H_kv, w_stride]
+  const int32_t* protect;    // [B]
+  const int32_t* seen;       // [B]
+  float* w_logits;           // [B, H_kv, w_stride, kSlots]
+  int w_stride;
 };
 
 // ---------------------------------------------------------------- PTX helpers
@@ -306,7 +328,8 @@ struct EpiSmem {
   static constexpr int kM = kWacc + kWarps * kSlots * D * 4;
   static constexpr int kInvL = kM + kSlots * 4;
   static constexpr int kWil = kInvL + kSlots * 4;
-  static constexpr int kBytes = kWil + kWarps * kSlots * 4;
+  static constexpr int kExt = kWil + kWarps * kSlots * 4;   // tail: f32 [8][kMaxExt][2]
+  static constexpr int kBytes = kExt + kSlots * kMaxExt * 8;
 };
 
 template <typename T, int D, int V = kGeneral>

@@ -1,0 +1,319 @@
+// Row attention on the CUDA cores (fp32, no TF32), and the kernel that joins
+// the parts of split keys.
+//
+// A CTA of 256 threads holds 64 query rows and streams its keys in tiles of
+// 64 through shared memory: thread (ty, tx) computes rows 4ty.. and keys tx +
+// 16j of the scores, and output dims of the same rows; softmax is online, in
+// base 2, with the row statistics of 16 neighbouring lanes joined by shuffles.
+#include <algorithm>
+
+#include <math_constants.h>
+
+#include "rows.cuh"
+
+namespace fastocr {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int BM = kRowsF32, BN = 64;
+
+template <int D>
+struct SmemF32 {
+  static constexpr int LD = D + 4;      // K rows: 16 keys apart in a warp, no bank conflicts
+  static constexpr int kQ = 0;          // [BM][D]
+  static constexpr int kK = kQ + BM * D;
+  static constexpr int kV = kK + BN * LD;
+  static constexpr int kP = kV + BN * D;     // [BM][BN]
+  static constexpr int kLive = kP + BM * BN; // int [BN]
+  static constexpr int kBytes = (kLive + BN) * 4;
+};
+
+__device__ __forceinline__ float4 load4(const float* p) { return __ldcg(reinterpret_cast<const float4*>(p)); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+  const uint2 w = __ldcg(reinterpret_cast<const uint2*>(p));
+  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
+                     __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
+}
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) rows_kernel(const RowsParams p) {
+  extern __shared__ __align__(16) float sm[];
+  using S = SmemF32<D>;
+  constexpr int LD = S::LD, DT = D / 64;   // float4 columns of the output a thread holds
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const int split = blockIdx.z, hkv = blockIdx.y;
+  float* qs = sm + S::kQ;
+  float* ks = sm + S::kK;
+  float* vs = sm + S::kV;
+  float* ps = sm + S::kP;
+  int* live = reinterpret_cast<int*>(sm + S::kLive);
+  int bad = 0;
+  const RowGroup grp = find_tile<BM>(p, blockIdx.x, bad);
+  // the kernel before may still write q and, where there is no prefix contract,
+  // the keys; the next one reads this one's output after its own wait
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  if (grp.tile < 0) {
+    if (bad) atomicOr(p.status, bad);
+    return;
+  }
+  if (split == 0 && hkv == 0 && grp.tile == 0) check_group(p, grp, bad);
+  int lo, hi;
+  split_range(grp.len, p.splits, split, lo, hi);
+  const int row0 = grp.tile * BM;
+  const int n_rows = min(BM, grp.n_rows - row0);
+  const int32_t* table = p.block_table + (size_t)grp.table_row * p.max_pages;
+  // q and out index (in heads) of row r
+  auto head_of = [&](int r) -> size_t {
+    const int x = row0 + r;
+    return (size_t)(grp.first + x / p.g) * p.Hq + hkv * p.g + x % p.g;
+  };
+  for (int e = tid; e < BM * (D / 4); e += kThreads) {
+    const int r = e / (D / 4), c = e % (D / 4);
+    const float4 v = r < n_rows ? load4(static_cast<const T*>(p.q) + head_of(r) * D + 4 * c)
+                                : make_float4(0.f, 0.f, 0.f, 0.f);
+    *reinterpret_cast<float4*>(qs + r * D + 4 * c) = v;
+  }
+  float m[4], l[4];
+  float4 o[4][DT];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    m[i] = -CUDART_INF_F;
+    l[i] = 0.f;
+#pragma unroll
+    for (int t = 0; t < DT; ++t) o[i][t] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  for (int k0 = lo; k0 < hi; k0 += BN) {
+    __syncthreads();   // the tile before is read to the end
+    for (int e = tid; e < BN * (D / 4); e += kThreads) {
+      const int j = e / (D / 4), c = e % (D / 4);
+      const int row = k0 + j < hi ? key_row(p, table, hkv, k0 + j, bad) : -1;
+      const size_t off = (size_t)max(row, 0) * D + 4 * c;
+      const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+      *reinterpret_cast<float4*>(ks + j * LD + 4 * c) = row >= 0 ? load4(static_cast<const T*>(p.k) + off) : z;
+      *reinterpret_cast<float4*>(vs + j * D + 4 * c) = row >= 0 ? load4(static_cast<const T*>(p.v) + off) : z;
+      if (c == 0) live[j] = row >= 0;
+    }
+    __syncthreads();
+    float s[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll 4
+    for (int c = 0; c < D / 4; ++c) {
+      float4 a[4], b[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(qs + (4 * ty + i) * D + 4 * c);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(ks + (tx + 16 * j) * LD + 4 * c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          s[i][j] = fmaf(a[i].x, b[j].x, s[i][j]);
+          s[i][j] = fmaf(a[i].y, b[j].y, s[i][j]);
+          s[i][j] = fmaf(a[i].z, b[j].z, s[i][j]);
+          s[i][j] = fmaf(a[i].w, b[j].w, s[i][j]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float mx = m[i];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[i][j] = live[tx + 16 * j] ? s[i][j] * p.scale_log2 : -CUDART_INF_F;
+        mx = fmaxf(mx, s[i][j]);
+      }
+#pragma unroll
+      for (int q = 8; q > 0; q >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, q));
+      const float base = mx == -CUDART_INF_F ? 0.f : mx;
+      const float al = fast_exp2(m[i] - base);
+      m[i] = mx;
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float e = fast_exp2(s[i][j] - base);
+        sum += e;
+        ps[(4 * ty + i) * BN + tx + 16 * j] = e;
+      }
+      l[i] = fmaf(l[i], al, sum);   // this lane's keys; the 16 lanes join at the end
+#pragma unroll
+      for (int t = 0; t < DT; ++t) {
+        o[i][t].x *= al;
+        o[i][t].y *= al;
+        o[i][t].z *= al;
+        o[i][t].w *= al;
+      }
+    }
+    __syncwarp();   // rows 4ty.. of ps are written and read by the same half warp
+#pragma unroll 4
+    for (int j = 0; j < BN; j += 4) {
+      float4 pr[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) pr[i] = *reinterpret_cast<const float4*>(ps + (4 * ty + i) * BN + j);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int t = 0; t < DT; ++t) {
+          const float4 v = *reinterpret_cast<const float4*>(vs + (j + u) * D + 64 * t + 4 * tx);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float w = u == 0 ? pr[i].x : u == 1 ? pr[i].y : u == 2 ? pr[i].z : pr[i].w;
+            o[i][t].x = fmaf(w, v.x, o[i][t].x);
+            o[i][t].y = fmaf(w, v.y, o[i][t].y);
+            o[i][t].z = fmaf(w, v.z, o[i][t].z);
+            o[i][t].w = fmaf(w, v.w, o[i][t].w);
+          }
+        }
+    }
+    __syncwarp();
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+#pragma unroll
+    for (int q = 8; q > 0; q >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], q);
+    const int r = 4 * ty + i;
+    if (r >= n_rows) continue;
+    const size_t head = head_of(r);
+    if (p.out && p.splits == 1) {
+      const float inv = l[i] > 0.f ? __frcp_rn(l[i]) : (l[i] == 0.f ? 0.f : l[i]);
+#pragma unroll
+      for (int t = 0; t < DT; ++t)
+        store4(static_cast<T*>(p.out) + head * D + 64 * t + 4 * tx,
+               make_float4(o[i][t].x * inv, o[i][t].y * inv, o[i][t].z * inv, o[i][t].w * inv));
+    } else {
+      const size_t at = (size_t)split * p.rows * p.Hq + head;
+      if (tx == 0) *reinterpret_cast<float2*>(p.ml + 2 * at) = make_float2(m[i], l[i]);
+      if (lo < hi) {
+#pragma unroll
+        for (int t = 0; t < DT; ++t) *reinterpret_cast<float4*>(p.acc + at * D + 64 * t + 4 * tx) = o[i][t];
+      }
+    }
+  }
+  if (bad) atomicOr(p.status, bad);
+}
+
+// Joins the parts of every row of a token that belongs to a group: one warp a
+// row, D / 32 dims a lane.
+constexpr int kMergeWarps = 8;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const RowsParams p) {
+  const int lane = threadIdx.x & 31;
+  const size_t head = (size_t)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+  const size_t n = (size_t)p.rows * p.Hq;
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  if (head >= n) return;
+  const long token = head / p.Hq;
+  if (token < __ldcg(p.start) || token >= __ldcg(p.start + p.n_groups)) return;
+  float ms[2], ls[2];   // parts lane and lane + 32
+  float M = -CUDART_INF_F;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int s = lane + 32 * u;
+    const float2 x = s < p.splits ? __ldcg(reinterpret_cast<const float2*>(p.ml) + s * n + head)
+                                  : make_float2(-CUDART_INF_F, 0.f);
+    ms[u] = x.x;
+    ls[u] = x.y;
+    M = fmaxf(M, x.x);
+  }
+#pragma unroll
+  for (int q = 16; q > 0; q >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, q));
+  const float base = M == -CUDART_INF_F ? 0.f : M;
+  float sc[2], L = 0.f;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    sc[u] = fast_exp2(ms[u] - base);
+    L = fmaf(ls[u], sc[u], L);
+  }
+#pragma unroll
+  for (int q = 16; q > 0; q >>= 1) L += __shfl_xor_sync(0xffffffffu, L, q);
+  float a[D / 32];
+#pragma unroll
+  for (int e = 0; e < D / 32; ++e) a[e] = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < p.splits; ++s) {
+    const float w = __shfl_sync(0xffffffffu, s < 32 ? sc[0] : sc[1], s & 31);
+    if (__shfl_sync(0xffffffffu, s < 32 ? ls[0] : ls[1], s & 31) == 0.f) continue;   // no rows there
+    const float* src = p.acc + (s * n + head) * D + lane * (D / 32);
+    if constexpr (D == 128) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+      a[0] = fmaf(v.x, w, a[0]);
+      a[1] = fmaf(v.y, w, a[1]);
+      a[2] = fmaf(v.z, w, a[2]);
+      a[3] = fmaf(v.w, w, a[3]);
+    } else {
+      const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+      a[0] = fmaf(v.x, w, a[0]);
+      a[1] = fmaf(v.y, w, a[1]);
+    }
+  }
+  const float inv = L > 0.f ? __frcp_rn(L) : (L == 0.f ? 0.f : L);
+  T* dst = static_cast<T*>(p.out) + head * D + lane * (D / 32);
+  if constexpr (D == 128) {
+    store4(dst, make_float4(a[0] * inv, a[1] * inv, a[2] * inv, a[3] * inv));
+  } else if constexpr (sizeof(T) == 4) {
+    *reinterpret_cast<float2*>(dst) = make_float2(a[0] * inv, a[1] * inv);
+  } else {
+    *reinterpret_cast<uint32_t*>(dst) = pack_bf16(a[0] * inv, a[1] * inv);
+  }
+}
+
+template <typename T, int D>
+cudaError_t launch_rows_t(const RowsParams& p, cudaStream_t s) {
+  RowsParams a = p;
+  void* args[] = {&a};
+  return launch_pdl(reinterpret_cast<const void*>(rows_kernel<T, D>),
+                    dim3((unsigned)max_row_tiles(p, BM), p.Hkv, p.splits), kThreads,
+                    SmemF32<D>::kBytes, s, args);
+}
+
+template <typename T, int D>
+cudaError_t launch_merge_t(const RowsParams& p, cudaStream_t s) {
+  RowsParams a = p;
+  void* args[] = {&a};
+  const long blocks = (p.rows * p.Hq + kMergeWarps - 1) / kMergeWarps;
+  return launch_pdl(reinterpret_cast<const void*>(merge_kernel<T, D>), dim3((unsigned)blocks),
+                    32 * kMergeWarps, 0, s, args);
+}
+
+template <typename T, int D>
+cudaError_t prepare_t() {
+  return cudaFuncSetAttribute(rows_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              SmemF32<D>::kBytes);
+}
+
+}  // namespace
+
+cudaError_t launch_rows_f32(int head_dim, const RowsParams& p, cudaStream_t s) {
+  return head_dim == 64 ? launch_rows_t<float, 64>(p, s) : launch_rows_t<float, 128>(p, s);
+}
+
+cudaError_t launch_rows_bf16(int head_dim, const RowsParams& p, cudaStream_t s) {
+  return head_dim == 64 ? launch_rows_t<__nv_bfloat16, 64>(p, s)
+                        : launch_rows_t<__nv_bfloat16, 128>(p, s);
+}
+
+cudaError_t launch_rows_merge(int head_dim, bool bf16, const RowsParams& p, cudaStream_t s) {
+  if (bf16)
+    return head_dim == 64 ? launch_merge_t<__nv_bfloat16, 64>(p, s)
+                          : launch_merge_t<__nv_bfloat16, 128>(p, s);
+  return head_dim == 64 ? launch_merge_t<float, 64>(p, s) : launch_merge_t<float, 128>(p, s);
+}
+
+cudaError_t prepare_rows() {
+  cudaError_t e;
+  if ((e = prepare_t<float, 64>())) return e;
+  if ((e = prepare_t<float, 128>())) return e;
+  if ((e = prepare_t<__nv_bfloat16, 64>())) return e;
+  return prepare_t<__nv_bfloat16, 128>();
+}
+
+}  // namespace fastocr

@@ -15,6 +15,10 @@ FastOCR (gist.science technical summary, "Focal-Guided Pruning" and
 Unlimited OCR (R-SWA): every layer calls fastocr_rswa_attend; with
 ring_block_table a sequence's cache holds only the prefix and a ring of
 window pages.
+Beside those, for generated text that grows long and for batches that read one
+document: share_prefix + shared_step (a prefix read once for a group of
+sequences) and track_weights + weighed_step + evict_step (every row's attention
+weight added up, the rows of least weight dropped), alone or together.
 
 The selection never leaves the GPU: every focal layer writes into its own
 fixed device buffer, and F_last *is* the deepest focal layer's buffer, which
@@ -140,6 +144,8 @@ class DecodeAttention:
         self.score_reduce = score_reduce
         self.sigma = (torch.zeros(self.batch, max(self.max_img, 1), dtype=torch.float32,
                                   device=dev) if score_reduce is not None else None)
+        self.groups = None     # share_prefix
+        self.weights = None    # track_weights
 
     def close(self):
         if self.handle:
@@ -161,6 +167,77 @@ class DecodeAttention:
             N.fastocr_set_length_hint(self.handle, n_t)
         else:
             self.seq_len.copy_(n_t, non_blocking=True)
+
+    def _per_sequence(self, x, name):
+        """int or [B] -> [B] int32 on the cache's device (a tensor that is that is taken as it is)."""
+        dev = self.k_cache.device
+        if isinstance(x, int):
+            return torch.full((self.batch,), x, dtype=torch.int32, device=dev)
+        x = torch.as_tensor(x).to(device=dev, dtype=torch.int32).contiguous()
+        if tuple(x.shape) != (self.batch,):
+            raise ValueError(f"{name} must have one value a sequence, shape ({self.batch},)")
+        return x
+
+    def share_prefix(self, group_start, prefix_len, max_prefix: int | None = None):
+        """Sequences group_start[i] .. group_start[i+1]-1 share rows [0, prefix_len)
+        of group_start[i]'s pages (group_start from 0 to B; prefix_len int or
+        [B], the same within a group). max_prefix: about the longest, for the
+        split choice only; None takes it from prefix_len (which then
+        synchronises, if it is on the device). Call it again when the groups
+        change; a CapturedStep must then be captured anew."""
+        start = torch.as_tensor(group_start).to(torch.int32)
+        if start.dim() != 1 or not 2 <= start.numel() <= self.batch + 1:
+            raise ValueError("group_start must hold 2 .. B+1 offsets")
+        if not start.is_cuda:
+            s = start.tolist()
+            if s[0] != 0 or s[-1] != self.batch or sorted(s) != s:
+                raise ValueError(f"group_start must ascend from 0 to {self.batch}")
+        prefix = self._per_sequence(prefix_len, "prefix_len")
+        if max_prefix is None:
+            max_prefix = prefix_len if isinstance(prefix_len, int) else int(prefix.max())
+        start = start.to(self.k_cache.device).contiguous()
+        ws_bytes = N.fastocr_rows_workspace(self.handle, self.batch)
+        ws = (self.groups["ws"] if self.groups else
+              torch.empty(ws_bytes, dtype=torch.uint8, device=self.k_cache.device))
+        self.groups = {"start": start, "prefix_len": prefix, "ws": ws,
+                       "c": N.make_groups(start, prefix, max_prefix)}
+
+    def track_weights(self, rows: int, protect, *, mass=None, pos=None, seen=None):
+        """Weights of up to `rows` rows behind protect (int or [B]: the prompt,
+        the image, a shared prefix) in every layer, for weighed_step and evict_step.
+
+        mass, pos: [layers, B, H_kv, rows] fp32 / int32, seen: [B] int32, taken as
+        they are if given (e.g. with a prompt's weights in them); otherwise
+        no weight, every row at its own position, and the tokens of seq_len
+        (a prompt that is already in the cache). begin_token advances seen."""
+        if rows < 1:
+            raise ValueError("rows must be at least 1")
+        dev = self.k_cache.device
+        shape = (self.layers, self.batch, self.kv_heads, rows)
+        protect = self._per_sequence(protect, "protect")
+        if mass is None:
+            mass = torch.zeros(shape, dtype=torch.float32, device=dev)
+        if pos is None:
+            pos = (protect[:, None, None] + torch.arange(rows, dtype=torch.int32, device=dev)
+                   ).expand(shape).contiguous()
+        if seen is None:
+            seen = self.seq_len.clone()
+        for x, want, dt in ((mass, shape, torch.float32), (pos, shape, torch.int32),
+                            (seen, (self.batch,), torch.int32)):
+            if tuple(x.shape) != want or x.dtype != dt or x.device != dev or not x.is_contiguous():
+                raise ValueError(f"need a contiguous {dt} tensor of shape {want} on {dev}")
+        logits = torch.empty((self.batch, self.kv_heads, rows, 8), dtype=torch.float32, device=dev)
+        self.weights = {"mass": mass, "pos": pos, "seen": seen, "protect": protect,
+                        "logits": logits, "new_len": torch.zeros_like(self.seq_len),
+                        "c": [N.make_weights(mass[l], pos[l], protect, seen, logits)
+                              for l in range(self.layers)]}
+
+    def begin_token(self):
+        """One more token in every sequence: N_t and, with weights, seen go up by
+        one (on the device; write its K/V to row N_t - 1)."""
+        self.seq_len.add_(1)
+        if self.weights:
+            self.weights["seen"].add_(1)
 
     def set_focal_layers(self, focal):
         self.focal = tuple(sorted(int(l) for l in focal))
@@ -353,14 +430,72 @@ class DecodeAttention:
             if hook:
                 hook(l, False)
 
+    def shared_layer(self, l, q_l, out_l, stream=None):
+        """Layer l of a step over shared prefixes (share_prefix); adds the rows'
+        weights if they are tracked."""
+        g = self.groups
+        if g is None:
+            raise RuntimeError("share_prefix has not been called")
+        N.fastocr_shared_attend(self.handle, q_l, self.kv[l], g["c"], out_l, g["ws"],
+                                g["ws"].numel(), self.weights["c"][l] if self.weights else None,
+                                stream)
+
+    def shared_step(self, q, out, stream=None, hook=None):
+        """Full attention in every layer, every group's prefix read once."""
+        for l in range(self.layers):
+            if hook:
+                hook(l, True)
+            self.shared_layer(l, q[l], out[l], stream)
+            if hook:
+                hook(l, False)
+
+    def weigh_layer(self, l, q_l, out_l, stream=None):
+        """Layer l of a step that adds every row's attention weight."""
+        if self.weights is None:
+            raise RuntimeError("track_weights has not been called")
+        N.fastocr_weigh_attend(self.handle, q_l, self.kv[l], self.weights["c"][l], out_l, stream)
+
+    def weighed_step(self, q, out, stream=None, hook=None):
+        """Full attention in every layer, adding every row's attention weight."""
+        for l in range(self.layers):
+            if hook:
+                hook(l, True)
+            self.weigh_layer(l, q[l], out[l], stream)
+            if hook:
+                hook(l, False)
+
+    def evict_layer(self, l, budget, recent, new_len=None, stream=None):
+        """Cut layer l's rows behind protect to `budget` a KV head, the `recent`
+        newest among them; new_len [B] int32 gets the rows left."""
+        if self.weights is None:
+            raise RuntimeError("track_weights has not been called")
+        N.fastocr_evict(self.handle, self.kv[l], self.weights["c"][l], budget, recent, new_len,
+                        stream)
+
+    def evict_step(self, budget: int, recent: int, stream=None):
+        """Cut every layer's rows and set seq_len (on the device) to the rows left."""
+        if self.weights is None:
+            raise RuntimeError("track_weights has not been called")
+        new_len = self.weights["new_len"]
+        for l in range(self.layers):
+            self.evict_layer(l, budget, recent, new_len if l == self.layers - 1 else None, stream)
+        if stream is None:
+            self.seq_len.copy_(new_len)
+        else:
+            with torch.cuda.stream(stream):
+                self.seq_len.copy_(new_len)
+
     def launches_per_step(self, kind: str) -> int:
         """Kernels one step of `kind` launches: one attend kernel per layer,
-        plus the selection kernel of every focal (or profiling) layer."""
+        plus the selection kernel of every focal (or profiling) layer, and two
+        a layer over shared prefixes."""
         if kind == "fastocr":
             return self.layers + len(self.focal)
         if kind == "profile":
             return 2 * self.layers
-        return self.layers   # "profile_mass", "dense", "rswa": one kernel a layer
+        if kind == "shared":
+            return 2 * self.layers
+        return self.layers   # "profile_mass", "dense", "rswa", "weighed": one kernel a layer
 
     def device_status(self, stream=None) -> int:
         return N.fastocr_device_status(self.handle, stream)
@@ -375,7 +510,9 @@ class CapturedStep:
     "profile" (the last step of a profiling window: full attention with
     scoring, selection and profile accumulation in every layer),
     "profile_mass" (an earlier step of the window: full attention and
-    profile accumulation only) or "rswa"; or any name with `fn`, a
+    profile accumulation only), "rswa", "shared" (share_prefix) or "weighed"
+    (track_weights; each replay adds the step's weights, and so does the warm
+    run before the capture); or any name with `fn`, a
     callable fn(q, out, stream) that issues the calls (e.g. a subset of the
     step's layers), and `launches`, the kernels it launches.
 
@@ -415,6 +552,7 @@ class CapturedStep:
             dec.begin_warmup()
         if fn is None:   # otherwise fn(q, out, stream) issues the calls and `launches` counts them
             fn = {"fastocr": dec.step, "dense": dec.dense_step, "rswa": dec.rswa_step,
+                  "shared": dec.shared_step, "weighed": dec.weighed_step,
                   "profile": dec.warmup_step,
                   "profile_mass": lambda q, out, stream=None, hook=None:
                       dec.warmup_step(q, out, stream, hook, select=False)}[kind]

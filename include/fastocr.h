@@ -83,7 +83,10 @@ extern "C" {
 /* 2 adds fastocr_focal_scores, fastocr_select, fastocr_set_variant,
  * fastocr_read_probe, fastocr_copy, fastocr_profile_attend,
  * fastocr_profiler_read / fastocr_profiler_load and fastocr_sparse_attend_ex
- * to version 1; no call of version 1 changed. */
+ * to version 1; no call of version 1 changed. fastocr_shared_attend,
+ * fastocr_weigh_attend, fastocr_evict, fastocr_cross_attend and
+ * fastocr_rows_workspace came later and changed nothing either, so the number
+ * stayed: look for the symbols. */
 #define FASTOCR_ABI_VERSION 2
 
 typedef struct fastocr_handle fastocr_handle;
@@ -107,6 +110,8 @@ typedef enum { FASTOCR_DTYPE_F32 = 0, FASTOCR_DTYPE_BF16 = 1 } fastocr_dtype;
 #define FASTOCR_DEV_BAD_IMG 4       /* img_range outside [0, N_t) */
 #define FASTOCR_DEV_BAD_SELECTION 8 /* selected position outside the image, or k > N_img */
 #define FASTOCR_DEV_INTERNAL 16     /* a kernel-internal consistency check failed (a library bug) */
+#define FASTOCR_DEV_BAD_GROUP 32    /* group or query offsets out of order, or a prefix past N_t */
+#define FASTOCR_DEV_BAD_WEIGHTS 64  /* protect < 0, below the prefix, or more rows than the stride */
 
 /* Shapes fixed for the life of a handle. */
 typedef struct {
@@ -129,6 +134,31 @@ typedef struct {
   const int32_t* seq_len;     /* [B] */
   int32_t num_pages;          /* pages in k and v (bounds check) */
 } fastocr_kv;
+
+/* Groups of sequences that share a prefix (fastocr_shared_attend). start and
+ * prefix_len are device memory, caller-owned. */
+typedef struct {
+  const int32_t* start;      /* [n + 1]: group i is sequences start[i] .. start[i+1]-1;
+                              * start[0] = 0, start[n] = B, ascending (empty groups allowed) */
+  const int32_t* prefix_len; /* [B]: rows [0, prefix_len[b]) are shared; the same in a group */
+  int32_t n;                 /* 1 .. B */
+  int32_t max_prefix;        /* host: about the longest prefix, for the split choice only (0: unknown) */
+} fastocr_groups;
+
+/* Attention weights of one layer's cache rows (fastocr_weigh_attend,
+ * fastocr_evict). Device memory, caller-owned. Rows below protect[b] (prompt,
+ * image, a shared prefix) have no weight and never go; row r >= protect[b]
+ * of sequence b and KV head j has its weight and position at index
+ * (b * H_kv + j) * stride + r - protect[b]. */
+typedef struct {
+  float* mass;            /* [B, H_kv, stride]: attention weight the row has had so far */
+  int32_t* pos;           /* [B, H_kv, stride]: position in the text of the token in the row */
+  const int32_t* protect; /* [B] */
+  const int32_t* seen;    /* [B]: tokens the sequence has had, the current one and evicted ones included */
+  float* logits;          /* scratch [B, H_kv, stride, 8], 16-byte aligned; contents meaningless;
+                           * layers of one stream may share it; fastocr_evict ignores it */
+  int32_t stride;         /* >= 1: rows that can have weights */
+} fastocr_weights;
 
 /* Library and ABI version; never fails, needs no GPU. */
 int32_t fastocr_abi_version(void);
@@ -251,6 +281,88 @@ fastocr_status fastocr_sparse_attend_ex(fastocr_handle* h, const void* q, const 
 fastocr_status fastocr_rswa_attend(fastocr_handle* h, const void* q, const fastocr_kv* kv,
                                    int32_t prefix_len, int32_t window, void* out,
                                    fastocr_stream stream);
+
+/* Bytes of workspace with which fastocr_shared_attend (rows = B) or
+ * fastocr_cross_attend over `rows` query tokens can split its keys over the
+ * whole device; about 20 MB or the size of one fp32 output, whichever is more.
+ * Negative (a fastocr_status): NULL, INVALID. */
+int64_t fastocr_rows_workspace(const fastocr_handle* h, int64_t rows);
+
+/* Decode attention of a batch whose sequences share long prefixes: several
+ * answers sampled from, or several questions about, the same document page.
+ * Computes fastocr_full_attend, with rows [0, prefix_len[b]) read through the
+ * block table of the FIRST sequence of b's group, once for the whole group,
+ * and rows [prefix_len[b], N_t) through b's own. Only the first sequence's
+ * pages need to hold the prefix; prefix_len need not be a multiple of the page
+ * size (entries of the other sequences' tables for whole prefix pages are not
+ * read). prefix_len[b] <= N_t of every sequence of the group; a longer one is
+ * reported as FASTOCR_DEV_BAD_GROUP and clamped. Offsets in start that are out
+ * of order are reported the same way; the output of a sequence in no group is
+ * then unspecified.
+ * weights: NULL, or accumulates weights like fastocr_weigh_attend (needs
+ * protect[b] >= prefix_len[b]).
+ * ws: device, 16-byte aligned, caller-owned, of at least one part's partials,
+ * B * H_q * (d + 2) * 4 bytes; fastocr_rows_workspace(h, B) for full speed.
+ * Its contents are meaningless between calls; calls that may run at once
+ * need one each.
+ * Overlap: as the other calls; start, prefix_len and the prefix's K/V rows are
+ * read before the preceding kernel completes. Two kernels.
+ * Errors: NULL, INVALID (groups, ws_bytes, another device current),
+ * UNSUPPORTED, ALIGN, CUDA. */
+fastocr_status fastocr_shared_attend(fastocr_handle* h, const void* q, const fastocr_kv* kv,
+                                     const fastocr_groups* groups, const fastocr_weights* weights,
+                                     void* out, void* ws, int64_t ws_bytes, fastocr_stream stream);
+
+/* Full decode attention over [0, N_t) that also adds up what every row is
+ * attended: mass[b][j][r - protect] += sum over the query heads of KV head j of
+ * the softmax probability of row r, for rows protect[b] <= r < N_t - 1. The
+ * current token's row N_t - 1 starts: its mass is set to that sum and its pos
+ * to seen[b] - 1. Call it once per layer and step. More than `stride` rows:
+ * FASTOCR_DEV_BAD_WEIGHTS, and those past it get no weight. protect and seen
+ * are set before the kernel preceding the call starts. One kernel. */
+fastocr_status fastocr_weigh_attend(fastocr_handle* h, const void* q, const fastocr_kv* kv,
+                                    const fastocr_weights* weights, void* out,
+                                    fastocr_stream stream);
+
+/* Eviction by accumulated weight: bounds the rows behind protect, where R-SWA
+ * keeps a window of the newest ones. For every sequence with more than
+ * `budget` rows in [protect, N_t), every KV head keeps `budget` of them: those
+ * with pos >= seen - recent, then those of largest mass (a NaN counts as
+ * smallest), ties to the lower row; among more recent rows than the budget
+ * the lower ones. Kept rows at or behind protect + budget move into the freed
+ * rows before it, in order, i-th to i-th, with K, V, mass and pos (attention
+ * does not depend on the order of rows). K and V are written although
+ * fastocr_kv has them const; rows at and behind protect + budget are left as
+ * they are. new_len[b] (device, may be NULL, must not be kv->seq_len, which
+ * every unit of the call reads) = the rows left; the next token goes to row
+ * new_len[b]. A sequence with more than `stride` rows is reported as
+ * FASTOCR_DEV_BAD_WEIGHTS and left as it is; a move from or to a page out of
+ * range moves mass and pos only (FASTOCR_DEV_BAD_PAGE). Pages behind protect
+ * must not be shared between sequences. Only prefix positions keep their
+ * meaning after it: rows are no longer in text order, so fastocr_rswa_attend's
+ * window and an image behind protect do not apply.
+ * 1 <= budget, 0 <= recent <= budget, stride <= 262144 (UNSUPPORTED). One
+ * kernel; protect, seen and seq_len are read before the preceding kernel
+ * completes, mass and pos after it. */
+fastocr_status fastocr_evict(fastocr_handle* h, const fastocr_kv* kv, const fastocr_weights* weights,
+                             int32_t budget, int32_t recent, int32_t* new_len,
+                             fastocr_stream stream);
+
+/* Cross attention: query tokens q_start[b] .. q_start[b+1]-1 of the packed q
+ * [rows, H_q, d] attend to all N_b = seq_len[b] states of sequence b in kv
+ * (0 allowed: the output is 0), without a mask. q_start [B + 1]: device,
+ * ascending from 0; sequences without queries are fine, and rows at and behind
+ * q_start[B] are left as they are. Offsets out of order or past `rows` are
+ * reported as FASTOCR_DEV_BAD_GROUP and clamped. rows * H_q < 2^31.
+ * ws: as fastocr_shared_attend, for `rows` tokens, or NULL: then the keys are
+ * not split. Overlap: only q_start, seq_len and the block table are read
+ * before the preceding kernel completes. One kernel, or two where the keys are
+ * split.
+ * Errors: NULL, INVALID (rows, ws_bytes, another device current),
+ * UNSUPPORTED, ALIGN, CUDA. */
+fastocr_status fastocr_cross_attend(fastocr_handle* h, const void* q, const fastocr_kv* kv,
+                                    const int32_t* q_start, int64_t rows, void* out, void* ws,
+                                    int64_t ws_bytes, fastocr_stream stream);
 
 /* Zero the profiler accumulator of every layer (asynchronous on stream). */
 fastocr_status fastocr_profiler_reset(fastocr_handle* h, fastocr_stream stream);

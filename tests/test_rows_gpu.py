@@ -1,0 +1,446 @@
+"""Shared-prefix attention, weighing, eviction and cross attention on the GPU
+against the fp64 oracle, at the sizes and masks where they can go wrong."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import rows as R
+from rows_harness import Paged, check_out, np64
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(autouse=True)
+def _device():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+
+
+def decoder(c, n, q_heads):
+    from dynamic_sparse_kv_gb300 import DecodeAttention
+    dec = DecodeAttention(c.k[None], c.v[None], c.gpu_table(), q_heads=q_heads)
+    dec.set_seq_len(torch.tensor(n, dtype=torch.int32, device="cuda"))
+    return dec
+
+
+def shared_case(sizes, prefixes, tails, heads, page, dtype, seed):
+    """Groups of `sizes` sequences; returns (cache, start, prefix [B], n [B], q)."""
+    hq, hkv, d = heads
+    start = np.concatenate([[0], np.cumsum(sizes)]).tolist()
+    prefix = [p for s, p in zip(sizes, prefixes) for _ in range(s)]
+    n = [p + t for p, t in zip(prefix, tails)]
+    c = Paged(len(n), max(n), hkv, d, page, dtype, seed)
+    g = torch.Generator().manual_seed(seed + 1)
+    q = (2 * torch.randn(len(n), hq, d, generator=g)).to(dtype).cuda()
+    return c, start, prefix, n, q
+
+
+def check_shared(c, start, prefix, n, q, out):
+    ps = []
+    for i in range(len(start) - 1):
+        for b in range(start[i], start[i + 1]):
+            K0, V0 = c.rows(start[i], 0, prefix[b])
+            K1, V1 = c.rows(b, prefix[b], n[b])
+            K, V = np.concatenate([K0, K1]), np.concatenate([V0, V1])
+            ps.append(check_out(out[b:b + 1], np64(q[b:b + 1]), K, V, q.dtype, f"sequence {b}"))
+    return ps
+
+
+HEADS = [(28, 4, 128), (10, 10, 128), (4, 2, 64), (8, 1, 64), (15, 3, 128)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("heads", HEADS)
+@pytest.mark.parametrize("page,sizes,prefixes,tails", [
+    (16, [3, 1, 2], [130, 17, 400], [1, 40, 7, 1, 16, 90]),
+    (1, [2], [65], [3, 1]),
+    (256, [1, 4], [511, 256], [2, 1, 300, 5, 6]),
+    (4, [5], [1], [1, 2, 3, 4, 5]),
+    (16, [2, 2], [0, 127], [1, 33, 2, 128]),
+    (32, [40], [300], list(range(1, 41))),
+])
+def test_shared_prefix(dtype, heads, page, sizes, prefixes, tails):
+    c, start, prefix, n, q = shared_case(sizes, prefixes, tails, heads, page, dtype, 3)
+    dec = decoder(c, n, heads[0])
+    dec.share_prefix(start, torch.tensor(prefix))
+    out = torch.full_like(q, float("nan"))
+    dec.shared_layer(0, q, out)
+    check_shared(c, start, prefix, n, q, out)
+    assert dec.device_status() == 0
+
+
+def test_shared_prefix_without_tail_and_with_empty_groups():
+    heads = (4, 2, 64)
+    c, _, prefix, n, q = shared_case([3], [70], [0, 0, 5], heads, 16, BF, 5)
+    from dynamic_sparse_kv_gb300 import _native as N
+    dec = decoder(c, n, 4)
+    start = torch.tensor([0, 0, 3, 3], dtype=torch.int32, device="cuda")
+    dec.share_prefix(start, torch.tensor(prefix))
+    out = torch.full_like(q, float("nan"))
+    dec.shared_layer(0, q, out)
+    check_shared(c, [0, 3], prefix, n, q, out)
+    assert dec.device_status() == 0
+    # a workspace of one part only
+    g = dec.groups
+    small = torch.empty(3 * 4 * 66 * 4, dtype=torch.uint8, device="cuda")
+    out2 = torch.full_like(q, float("nan"))
+    N.fastocr_shared_attend(dec.handle, q, dec.kv[0], g["c"], out2, small, small.numel())
+    check_shared(c, [0, 3], prefix, n, q, out2)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("heads", HEADS[:3])
+@pytest.mark.parametrize("splits", [0, 1, 5])
+def test_weighed_attention(dtype, heads, splits):
+    """Weights with and without a shared prefix; rows past the stride and protected ones get none."""
+    hq, hkv, d = heads
+    c, start, prefix, n, q = shared_case([2, 2], [40, 0], [30, 1, 200, 64], heads, 16, dtype, 7)
+    from dynamic_sparse_kv_gb300 import _native as N
+    for shared in (False, True):
+        dec = decoder(c, n, hq)
+        if splits:
+            N.fastocr_set_splits(dec.handle, 0, splits)
+        protect = [40, 40, 0, 70]       # sequence 3: nothing weighed yet but what follows
+        rows = 200
+        mass0 = torch.rand(1, 4, hkv, rows, generator=torch.Generator().manual_seed(1))
+        pos0 = torch.arange(rows, dtype=torch.int32).expand(1, 4, hkv, rows).contiguous()
+        seen = torch.tensor([100, 50, 900, 64], dtype=torch.int32, device="cuda")
+        dec.track_weights(rows, torch.tensor(protect), mass=mass0.cuda(), pos=pos0.cuda(), seen=seen)
+        out = torch.full_like(q, float("nan"))
+        if shared:
+            dec.share_prefix(start, torch.tensor(prefix))
+            dec.shared_layer(0, q, out)
+            full = [(start[0 if b < 2 else 1], prefix[b]) for b in range(4)]
+        else:
+            dec.weigh_layer(0, q, out)
+            full = [(b, 0) for b in range(4)]
+        mass, pos = np64(dec.weights["mass"][0]), dec.weights["pos"][0].cpu().numpy()
+        for b in range(4):
+            K0, V0 = c.rows(full[b][0], 0, full[b][1])
+            K1, V1 = c.rows(b, full[b][1], n[b])
+            K, V = np.concatenate([K0, K1]), np.concatenate([V0, V1])
+            p, cb = check_out(out[b:b + 1], np64(q[b:b + 1]), K, V, dtype, f"sequence {b}")
+            want, wpos = R.add_weights(np64(mass0[0, b]), pos0[0, b].numpy(), p[0], n[b], protect[b],
+                                       int(seen[b]), hkv)
+            # a sum of g probabilities, then one addition
+            tol = (cb.max() + 9 * 2.0 ** -24) * np.abs(want) + 2.0 ** -24
+            assert (np.abs(mass[b] - want) <= tol).all(), (b, np.abs(mass[b] - want).max())
+            assert np.array_equal(pos[b], wpos)
+        assert dec.device_status() == 0
+        dec.close()
+
+
+def run_evict(c, n, hq, mass, pos, seen, protect, budget, recent):
+    dec = decoder(c, n, hq)
+    dec.track_weights(mass.shape[-1], torch.tensor(protect), mass=mass.cuda()[None].contiguous(),
+                      pos=pos.cuda()[None].contiguous(),
+                      seen=torch.tensor(seen, dtype=torch.int32, device="cuda"))
+    new_len = torch.full((len(n),), -7, dtype=torch.int32, device="cuda")
+    dec.evict_layer(0, budget, recent, new_len)
+    torch.cuda.synchronize()
+    return dec, new_len
+
+
+def check_evict(c, k0, v0, n, mass0, pos0, seen, protect, budget, recent, dec, new_len):
+    """Every byte of K, V, mass and pos as the oracle's moves leave them."""
+    k, v = k0.cpu().clone(), v0.cpu().clone()
+    mass, pos = mass0.clone(), pos0.clone()
+    hkv = mass0.shape[1]
+    for b in range(len(n)):
+        rows = max(0, n[b] - protect[b])
+        assert int(new_len[b]) == min(n[b], protect[b]) + min(rows, budget), b
+        for h in range(hkv):
+            if rows <= budget:
+                continue
+            _, moves = R.evict_moves(mass0[b, h].tolist(), pos0[b, h].tolist(), rows, seen[b], budget, recent)
+            for x, y in moves:
+                mass[b, h, y], pos[b, h, y] = mass0[b, h, x], pos0[b, h, x]
+                rx, ry = x + protect[b], y + protect[b]
+                px, py = int(c.table[b, rx // c.page]), int(c.table[b, ry // c.page])
+                k[py, h, ry % c.page] = k0.cpu()[px, h, rx % c.page]
+                v[py, h, ry % c.page] = v0.cpu()[px, h, rx % c.page]
+    w = dec.weights
+    assert torch.equal(w["mass"][0].cpu().view(torch.int32), mass.view(torch.int32))
+    assert torch.equal(w["pos"][0].cpu(), pos)
+    assert torch.equal(c.k.cpu(), k) and torch.equal(c.v.cpu(), v)
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 64), (BF, 128), (F32, 64), (F32, 128)])
+@pytest.mark.parametrize("page", [1, 16])
+@pytest.mark.parametrize("rows,protect,stride,budget,recent", [
+    ([9, 1, 0, 8], [0, 5, 3, 20], 9, 8, 3),
+    ([300, 257, 256, 40], [17, 0, 1, 0], 300, 256, 100),
+    ([1000, 999, 3, 700], [0, 0, 0, 31], 1024, 1, 0),
+    ([1000, 64, 65, 513], [5, 5, 5, 5], 1000, 64, 64),
+    ([600, 100, 100, 601], [0, 0, 0, 0], 601, 300, 0),
+])
+def test_evict(dtype, d, page, rows, protect, stride, budget, recent):
+    hkv = 3
+    n = [r + p for r, p in zip(rows, protect)]
+    c = Paged(4, max(n), hkv, d, page, dtype, 11)
+    k0, v0 = c.k.clone(), c.v.clone()
+    g = torch.Generator().manual_seed(2)
+    mass = torch.exp(2 * torch.randn(4, hkv, stride, generator=g))
+    mass[:, 1] = (mass[:, 1] * 2).round() / 2          # many ties, zeros among them
+    mass[0, 2, :3] = torch.tensor([float("nan"), float("inf"), -0.0])
+    mass[3, 2] = -mass[3, 2]
+    seen = [r + 50 for r in n]
+    pos = torch.stack([torch.stack([s - 1 - torch.randperm(stride, generator=g) for _ in range(hkv)])
+                       for s in seen]).to(torch.int32)
+    dec, new_len = run_evict(c, n, 2 * hkv, mass, pos, seen, protect, budget, recent)
+    check_evict(c, k0, v0, n, mass, pos, seen, protect, budget, recent, dec, new_len)
+    assert dec.device_status() == 0
+
+
+@pytest.mark.parametrize("batch,rows,budget,recent", [(1, 20000, 5000, 64), (2, 9000, 8999, 500),
+                                                      (1, 40001, 1000, 0), (1, 70000, 60000, 1)])
+def test_evict_over_a_cluster(batch, rows, budget, recent):
+    """Rows over several CTAs; equal weights make the tie order count across them."""
+    hkv = 2
+    c = Paged(batch, rows + 3, hkv, 64, 16, BF, 12)
+    k0, v0 = c.k.clone(), c.v.clone()
+    g = torch.Generator().manual_seed(4)
+    mass = torch.randint(0, 7, (batch, hkv, rows), generator=g).float()
+    seen = [rows + 3] * batch
+    pos = (torch.arange(rows, dtype=torch.int32) + 3).expand(batch, hkv, rows).contiguous()
+    dec, new_len = run_evict(c, [rows + 3] * batch, 4, mass, pos, seen, [3] * batch, budget, recent)
+    check_evict(c, k0, v0, [rows + 3] * batch, mass, pos, seen, [3] * batch, budget, recent, dec, new_len)
+    assert dec.device_status() == 0
+
+
+def cross_case(t, n, heads, page, dtype, seed, spare=3):
+    hq, hkv, d = heads
+    c = Paged(len(n), max(max(n), 1), hkv, d, page, dtype, seed)
+    g = torch.Generator().manual_seed(seed + 1)
+    start = np.concatenate([[0], np.cumsum(t)]).astype(np.int32)
+    q = (2 * torch.randn(int(start[-1]) + spare, hq, d, generator=g)).to(dtype).cuda()
+    return c, torch.from_numpy(start).cuda(), q
+
+
+def check_cross(c, t, n, q, out, spare=3):
+    at = 0
+    for b in range(len(n)):
+        K, V = c.rows(b, 0, n[b])
+        if t[b]:
+            check_out(out[at:at + t[b]], np64(q[at:at + t[b]]), K, V, q.dtype, f"sequence {b}")
+        at += t[b]
+    assert (out[at:at + spare].float() == 7.0).all(), "rows behind the last sequence were written"
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("heads", HEADS)
+@pytest.mark.parametrize("page,t,n", [
+    (16, [1, 1, 1], [300, 1, 0]),
+    (16, [0, 37, 2, 0], [5, 700, 128, 9]),
+    (1, [3], [129]),
+    (256, [1, 130], [513, 255]),
+    (8, [19], [1000]),
+])
+@pytest.mark.parametrize("ws", [True, False])
+def test_cross_attention(dtype, heads, page, t, n, ws):
+    from dynamic_sparse_kv_gb300 import CrossAttention
+    c, start, q = cross_case(t, n, heads, page, dtype, 21)
+    ca = CrossAttention(c.k[None], c.v[None], c.gpu_table(), torch.tensor(n), q_heads=heads[0],
+                        max_rows=q.shape[0] if ws else 0)
+    out = torch.full_like(q, 7.0)
+    ca.attend(0, q, start, out)
+    check_cross(c, t, n, q, out)
+    assert ca.device_status() == 0
+
+
+def test_infinities_outside_the_attended_rows():
+    """Rows past N_t, past the prefix in the leader's pages and in unused pages may hold anything."""
+    heads = (8, 2, 128)
+    c, start, prefix, n, q = shared_case([2, 1], [100, 37], [3, 1, 20], heads, 16, BF, 31)
+    for x in (c.k, c.v):
+        own = torch.ones(x.shape[0], x.shape[2], dtype=torch.bool)
+        for i in range(2):
+            for b in range(start[i], start[i + 1]):
+                for r in range(n[b]):
+                    lead = start[i] if r < prefix[b] else b
+                    own[int(c.table[lead, r // 16]), r % 16] = False
+        x.permute(0, 2, 1, 3)[own.cuda()] = float("nan")
+    dec = decoder(c, n, 8)
+    dec.share_prefix(start, torch.tensor(prefix))
+    out = torch.full_like(q, float("nan"))
+    dec.shared_layer(0, q, out)
+    check_shared(c, start, prefix, n, q, out)
+    out2 = torch.full((8, 8, 128), 7.0, dtype=BF, device="cuda")
+    from dynamic_sparse_kv_gb300 import CrossAttention
+    ca = CrossAttention(c.k[None], c.v[None], c.gpu_table(), torch.tensor([100, 0, 37]), q_heads=8,
+                        max_rows=8)
+    q2 = torch.randn(8, 8, 128, device="cuda").to(BF)
+    ca.attend(0, q2, torch.tensor([0, 4, 5, 5], dtype=torch.int32, device="cuda"), out2)
+    check_cross(c, [4, 1, 0], [100, 0, 37], q2, out2)
+
+
+def test_bad_device_data_is_reported_and_masked():
+    from dynamic_sparse_kv_gb300 import CrossAttention, _native as N
+    heads = (4, 2, 64)
+    c, start, prefix, n, q = shared_case([2, 1], [64, 20], [3, 1, 20], heads, 16, BF, 41)
+    table = c.table.clone()
+    c.table[0, 1] = 10 ** 6
+    dec = decoder(c, n, 4)
+    dec.share_prefix(start, torch.tensor(prefix))
+    out = torch.full_like(q, float("nan"))
+    dec.shared_layer(0, q, out)
+    assert dec.device_status() == N.DEV_BAD_PAGE
+    assert torch.isfinite(out.float()).all()
+    # the masked page's rows are left out for the whole group
+    c.table = table
+    K0, V0 = c.rows(0, 0, 64)
+    for b in (0, 1):
+        K1, V1 = c.rows(b, 64, n[b])
+        keep = np.r_[0:16, 32:64]
+        check_out(out[b:b + 1], np64(q[b:b + 1]), np.concatenate([K0[keep], K1]),
+                  np.concatenate([V0[keep], V1]), BF)
+    dec.close()
+
+    dec = decoder(c, n, 4)
+    for start_bad, prefix_bad in (([0, 2, 5], prefix), ([0, 3, 2], prefix), ([-1, 2, 3], prefix),
+                                  ([0, 1, 2], prefix), (start, [64, 60, 20]), (start, [900, 900, 20]),
+                                  (start, [-1, -1, 20])):
+        dec.share_prefix(torch.tensor(start_bad, dtype=torch.int32, device="cuda"),
+                         torch.tensor(prefix_bad), max_prefix=64)
+        dec.shared_layer(0, q, out)
+        assert dec.device_status() == N.DEV_BAD_GROUP, (start_bad, prefix_bad)
+
+    dec.track_weights(4, 0)
+    dec.weigh_layer(0, q, out)
+    assert dec.device_status() == N.DEV_BAD_WEIGHTS
+    new_len = torch.zeros(3, dtype=torch.int32, device="cuda")
+    k0 = c.k.clone()
+    dec.evict_layer(0, 2, 1, new_len)      # more rows than weights: left as they are
+    assert dec.device_status() == N.DEV_BAD_WEIGHTS
+    assert new_len.tolist() == n and torch.equal(c.k, k0)
+
+    ca = CrossAttention(c.k[None], c.v[None], c.gpu_table(), torch.tensor([64, 10 ** 6, -1]), q_heads=4,
+                        max_rows=3)
+    for qs, want in (([0, 1, 2, 3], N.DEV_BAD_SEQLEN), ([0, 1, 1, 9], N.DEV_BAD_GROUP | N.DEV_BAD_SEQLEN),
+                     ([0, 1, 0, 1], N.DEV_BAD_GROUP | N.DEV_BAD_SEQLEN)):
+        ca.attend(0, q, torch.tensor(qs, dtype=torch.int32, device="cuda"), out)
+        got = ca.device_status()
+        assert got & want and not got & ~want, (qs, got)
+
+
+def simulate(steps, budget, recent, graph):
+    """Two documents, five answers: every step appends a token, attends over the shared prefix
+    with weights, and evicts; checked against the oracle after each step."""
+    from dynamic_sparse_kv_gb300 import CapturedStep, DecodeAttention
+    heads, page, dtype = (6, 2, 64), 8, BF
+    sizes, prefixes = [3, 2], [50, 27]
+    start = [0, 3, 5]
+    prefix = [50] * 3 + [27] * 2
+    protect = [p + 2 for p in prefix]          # two own tokens (a question) stay as well
+    layers = 2
+    cs = [Paged(5, 50 + 2 + budget + 4, 2, 64, page, dtype, 50 + l) for l in range(layers)]
+    k, v = torch.stack([c.k for c in cs]), torch.stack([c.v for c in cs])
+    for c in cs:
+        c.table = cs[0].table
+    dec = DecodeAttention(k, v, cs[0].gpu_table(), q_heads=6)
+    n = list(protect)
+    dec.set_seq_len(torch.tensor(n, dtype=torch.int32, device="cuda"))
+    dec.share_prefix(start, torch.tensor(prefix))
+    dec.track_weights(budget + 1, torch.tensor(protect))
+    w = dec.weights
+    mass, pos = np64(w["mass"]), w["pos"].cpu().numpy().astype(np.int64)
+    seen = list(n)
+    step = None
+    g = torch.Generator().manual_seed(9)
+    q = torch.empty(layers, 5, 6, 64, dtype=dtype, device="cuda")
+    out = torch.empty_like(q)
+    for t in range(steps):
+        dec.begin_token()
+        n = [x + 1 for x in n]
+        seen = [x + 1 for x in seen]
+        new = torch.randn(2, layers, 5, 2, 64, generator=g).to(dtype).cuda()
+        table = cs[0].table
+        for b in range(5):
+            r = n[b] - 1
+            k[:, int(table[b, r // page]), :, r % page] = new[0][:, b]
+            v[:, int(table[b, r // page]), :, r % page] = new[1][:, b]
+        q.copy_((2 * torch.randn(q.shape, generator=g)).to(dtype))
+        if graph and t == 0:
+            saved = {x: w[x].clone() for x in ("mass", "pos")}
+            step = CapturedStep(dec, "shared")
+            for x in saved:
+                w[x].copy_(saved[x])
+        if step is not None:
+            step.q.copy_(q)
+            step.replay()
+            out.copy_(step.out)
+        else:
+            dec.shared_step(q, out)
+        for l in range(layers):
+            for b in range(5):
+                lead = 0 if b < 3 else 3
+                K0, V0 = cs[l].rows(lead, 0, prefix[b], k[l], v[l])
+                K1, V1 = cs[l].rows(b, prefix[b], n[b], k[l], v[l])
+                K, V = np.concatenate([K0, K1]), np.concatenate([V0, V1])
+                p, cb = check_out(out[l, b:b + 1], np64(q[l, b:b + 1]), K, V, dtype, f"step {t} layer {l} seq {b}")
+                want, wpos = R.add_weights(mass[l, b], pos[l, b], p[0], n[b], protect[b], seen[b], 2)
+                got = np64(w["mass"][l, b])
+                assert (np.abs(got - want) <= (cb.max() + 9 * 2.0 ** -24) * np.abs(want) + 2.0 ** -24).all()
+                assert np.array_equal(w["pos"][l, b].cpu().numpy(), wpos)
+                mass[l, b], pos[l, b] = got, wpos        # go on from the GPU's weights, checked above
+        before = (k.cpu().clone(), v.cpu().clone())
+        dec.evict_step(budget, recent)
+        for l in range(layers):
+            for b in range(5):
+                rows = n[b] - protect[b]
+                if rows <= budget:
+                    continue
+                for h in range(2):
+                    _, moves = R.evict_moves(mass[l, b, h], pos[l, b, h], rows, seen[b], budget, recent)
+                    for x, y in moves:
+                        mass[l, b, h, y], pos[l, b, h, y] = mass[l, b, h, x], pos[l, b, h, x]
+                        rx, ry = x + protect[b], y + protect[b]
+                        for s, d in zip(before, (k, v)):
+                            src = s[l, int(table[b, rx // page]), h, rx % page]
+                            assert torch.equal(d[l, int(table[b, ry // page]), h, ry % page].cpu(), src)
+                assert np.array_equal(w["pos"][l, b].cpu().numpy(), pos[l, b])
+        n = [protect[b] + min(n[b] - protect[b], budget) for b in range(5)]
+        assert dec.seq_len.tolist() == n
+    assert dec.device_status() == 0
+    # the recent tokens are all there
+    for l in range(layers):
+        for b in range(5):
+            for h in range(2):
+                have = set(pos[l, b, h, :n[b] - protect[b]].tolist())
+                assert {seen[b] - 1 - i for i in range(min(recent, steps))} <= have
+
+
+@pytest.mark.parametrize("graph", [False, True])
+def test_shared_prefix_weights_and_eviction_together(graph):
+    simulate(steps=20, budget=9, recent=3, graph=graph)
+
+
+def test_on_another_stream_and_twice_at_once():
+    """Two handles on two streams, each captured once and replayed in turn."""
+    heads = (28, 4, 128)
+    runs = []
+    for seed in (61, 62):
+        c, start, prefix, n, q = shared_case([4], [700], [9, 30, 1, 4], heads, 16, BF, seed)
+        dec = decoder(c, n, 28)
+        dec.share_prefix(start, torch.tensor(prefix))
+        out = torch.full_like(q, float("nan"))
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            dec.shared_layer(0, q, out)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            dec.shared_layer(0, q, out)
+        runs.append((c, start, prefix, n, q, out, s, graph, dec))
+    torch.cuda.synchronize()
+    for _, _, _, _, _, out, _, _, _ in runs:
+        out.fill_(float("nan"))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for r in runs:
+            with torch.cuda.stream(r[6]):
+                r[7].replay()
+    torch.cuda.synchronize()
+    for c, start, prefix, n, q, out, *_ in runs:
+        check_shared(c, start, prefix, n, q, out)
