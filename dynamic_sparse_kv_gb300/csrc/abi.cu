@@ -50,7 +50,8 @@ fastocr_status fastocr_create(const fastocr_dims* dims, fastocr_handle** out) {
   if (cudaGetDeviceProperties(&prop, dev) != cudaSuccess) return FASTOCR_ERR_NO_DEVICE;
   if (prop.major != 10 || prop.minor != 3) return FASTOCR_ERR_NO_DEVICE;
   if (prepare_bf16() != cudaSuccess || prepare_f32() != cudaSuccess ||
-      prepare_rows() != cudaSuccess || prepare_evict() != cudaSuccess)
+      prepare_rows_f32() != cudaSuccess || prepare_rows_bf16() != cudaSuccess ||
+      prepare_evict() != cudaSuccess)
     return FASTOCR_ERR_CUDA;
 
   const size_t units = (size_t)d.batch * d.num_kv_heads;

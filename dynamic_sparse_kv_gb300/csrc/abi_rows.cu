@@ -59,7 +59,9 @@ int64_t part_bytes(const fastocr_handle* h, int64_t rows) {
 }
 
 // Query rows a CTA holds.
-int tile_rows(const fastocr_handle* h) { return kRowsF32; }
+int tile_rows(const fastocr_handle* h) {
+  return h->dims.dtype == FASTOCR_DTYPE_BF16 ? kRowsBf16 : kRowsF32;
+}
 
 // Parts the keys are cut into when about `tiles` row tiles a KV head run at
 // once: enough CTAs for every SM.

@@ -131,11 +131,13 @@ __device__ __forceinline__ int key_row(const RowsParams& p, const int32_t* table
 
 // Rows a CTA's tile holds, per dtype.
 constexpr int kRowsF32 = 64;
+constexpr int kRowsBf16 = 256;
 
 cudaError_t launch_rows_f32(int head_dim, const RowsParams& p, cudaStream_t s);
 cudaError_t launch_rows_bf16(int head_dim, const RowsParams& p, cudaStream_t s);
 cudaError_t launch_rows_merge(int head_dim, bool bf16, const RowsParams& p, cudaStream_t s);
-cudaError_t prepare_rows();
+cudaError_t prepare_rows_f32();
+cudaError_t prepare_rows_bf16();
 
 // Row tiles a launch must cover, whatever the groups' sizes.
 inline long max_row_tiles(const RowsParams& p, int bm) {

@@ -30,17 +30,12 @@ struct SmemF32 {
 };
 
 __device__ __forceinline__ float4 load4(const float* p) { return __ldcg(reinterpret_cast<const float4*>(p)); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-  const uint2 w = __ldcg(reinterpret_cast<const uint2*>(p));
-  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
-                     __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
-}
 __device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
 __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
   *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
 }
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsParams p) {
   extern __shared__ __align__(16) float sm[];
   using S = SmemF32<D>;
@@ -75,7 +70,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsParams p) {
   };
   for (int e = tid; e < BM * (D / 4); e += kThreads) {
     const int r = e / (D / 4), c = e % (D / 4);
-    const float4 v = r < n_rows ? load4(static_cast<const T*>(p.q) + head_of(r) * D + 4 * c)
+    const float4 v = r < n_rows ? load4(static_cast<const float*>(p.q) + head_of(r) * D + 4 * c)
                                 : make_float4(0.f, 0.f, 0.f, 0.f);
     *reinterpret_cast<float4*>(qs + r * D + 4 * c) = v;
   }
@@ -95,8 +90,8 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsParams p) {
       const int row = k0 + j < hi ? key_row(p, table, hkv, k0 + j, bad) : -1;
       const size_t off = (size_t)max(row, 0) * D + 4 * c;
       const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-      *reinterpret_cast<float4*>(ks + j * LD + 4 * c) = row >= 0 ? load4(static_cast<const T*>(p.k) + off) : z;
-      *reinterpret_cast<float4*>(vs + j * D + 4 * c) = row >= 0 ? load4(static_cast<const T*>(p.v) + off) : z;
+      *reinterpret_cast<float4*>(ks + j * LD + 4 * c) = row >= 0 ? load4(static_cast<const float*>(p.k) + off) : z;
+      *reinterpret_cast<float4*>(vs + j * D + 4 * c) = row >= 0 ? load4(static_cast<const float*>(p.v) + off) : z;
       if (c == 0) live[j] = row >= 0;
     }
     __syncthreads();
@@ -185,7 +180,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsParams p) {
       const float inv = l[i] > 0.f ? __frcp_rn(l[i]) : (l[i] == 0.f ? 0.f : l[i]);
 #pragma unroll
       for (int t = 0; t < DT; ++t)
-        store4(static_cast<T*>(p.out) + head * D + 64 * t + 4 * tx,
+        store4(static_cast<float*>(p.out) + head * D + 64 * t + 4 * tx,
                make_float4(o[i][t].x * inv, o[i][t].y * inv, o[i][t].z * inv, o[i][t].w * inv));
     } else {
       const size_t at = (size_t)split * p.rows * p.Hq + head;
@@ -266,11 +261,11 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const RowsParam
   }
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t launch_rows_t(const RowsParams& p, cudaStream_t s) {
   RowsParams a = p;
   void* args[] = {&a};
-  return launch_pdl(reinterpret_cast<const void*>(rows_kernel<T, D>),
+  return launch_pdl(reinterpret_cast<const void*>(rows_kernel<D>),
                     dim3((unsigned)max_row_tiles(p, BM), p.Hkv, p.splits), kThreads,
                     SmemF32<D>::kBytes, s, args);
 }
@@ -284,21 +279,16 @@ cudaError_t launch_merge_t(const RowsParams& p, cudaStream_t s) {
                     32 * kMergeWarps, 0, s, args);
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t prepare_t() {
-  return cudaFuncSetAttribute(rows_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  return cudaFuncSetAttribute(rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               SmemF32<D>::kBytes);
 }
 
 }  // namespace
 
 cudaError_t launch_rows_f32(int head_dim, const RowsParams& p, cudaStream_t s) {
-  return head_dim == 64 ? launch_rows_t<float, 64>(p, s) : launch_rows_t<float, 128>(p, s);
-}
-
-cudaError_t launch_rows_bf16(int head_dim, const RowsParams& p, cudaStream_t s) {
-  return head_dim == 64 ? launch_rows_t<__nv_bfloat16, 64>(p, s)
-                        : launch_rows_t<__nv_bfloat16, 128>(p, s);
+  return head_dim == 64 ? launch_rows_t<64>(p, s) : launch_rows_t<128>(p, s);
 }
 
 cudaError_t launch_rows_merge(int head_dim, bool bf16, const RowsParams& p, cudaStream_t s) {
@@ -308,12 +298,9 @@ cudaError_t launch_rows_merge(int head_dim, bool bf16, const RowsParams& p, cuda
   return head_dim == 64 ? launch_merge_t<float, 64>(p, s) : launch_merge_t<float, 128>(p, s);
 }
 
-cudaError_t prepare_rows() {
-  cudaError_t e;
-  if ((e = prepare_t<float, 64>())) return e;
-  if ((e = prepare_t<float, 128>())) return e;
-  if ((e = prepare_t<__nv_bfloat16, 64>())) return e;
-  return prepare_t<__nv_bfloat16, 128>();
+cudaError_t prepare_rows_f32() {
+  const cudaError_t e = prepare_t<64>();
+  return e != cudaSuccess ? e : prepare_t<128>();
 }
 
 }  // namespace fastocr

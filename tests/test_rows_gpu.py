@@ -64,6 +64,7 @@ def test_shared_prefix(dtype, heads, page, sizes, prefixes, tails):
     c, start, prefix, n, q = shared_case(sizes, prefixes, tails, heads, page, dtype, 3)
     dec = decoder(c, n, heads[0])
     dec.share_prefix(start, torch.tensor(prefix))
+    dec.groups["ws"].fill_(127)       # whatever was in it: huge finite floats
     out = torch.full_like(q, float("nan"))
     dec.shared_layer(0, q, out)
     check_shared(c, start, prefix, n, q, out)
@@ -243,6 +244,8 @@ def test_cross_attention(dtype, heads, page, t, n, ws):
     c, start, q = cross_case(t, n, heads, page, dtype, 21)
     ca = CrossAttention(c.k[None], c.v[None], c.gpu_table(), torch.tensor(n), q_heads=heads[0],
                         max_rows=q.shape[0] if ws else 0)
+    if ws:
+        ca.ws.fill_(127)
     out = torch.full_like(q, 7.0)
     ca.attend(0, q, start, out)
     check_cross(c, t, n, q, out)
