@@ -39,9 +39,9 @@ struct SmemBf16 {
   static constexpr int kRing = 2 * kTileBytes;
   static constexpr int kRow = kRing + kStages * kTileBytes;   // int [2][128]: cache rows of a key tile
   static constexpr int kMask = kRow + 2 * 128 * 4;            // u32 [kMaskRing][4]: keys that exist
-  static constexpr int kMl = kQ;   // float2 [2][128]: the turns' max and sum, once Q is read
+  static constexpr int kMl = kRing;   // float2 [2][128]: the turns' max and sum, once the ring is read
   static constexpr int kBar = kMask + kMaskRing * 16;
-  static constexpr int kNumBars = 2 * kStages + 1 + 4 * 2;
+  static constexpr int kNumBars = 2 * kStages + 1 + 5 * 2;
   static constexpr int kTmem = kBar + kNumBars * 8;
   static constexpr int kDead = kTmem + 4;
   static constexpr int kBytes = kDead + 4 + 1024;    // room to align the base to 1024
@@ -81,9 +81,15 @@ __device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, volatil
   if (!mbar_try(bar, parity)) mbar_wait_slow(bar, parity, dead);
 }
 
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar)
-               : "memory");
+// The issuing warp stays converged, so that operands are computed in uniform
+// registers (a divergent single thread took 60-120 cycles an instruction); the
+// instructions themselves are predicated to its one elected lane.
+__device__ __forceinline__ void tc_commit(uint32_t bar, int elected) {
+  asm volatile(
+      "{\n.reg .pred e;\nsetp.ne.b32 e, %1, 0;\n"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar),
+      "r"(elected)
+      : "memory");
 }
 __device__ __forceinline__ void tc_fence_before() {
   asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory");
@@ -145,19 +151,46 @@ __host__ __device__ constexpr uint32_t instruction(int n, bool trans_b) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (trans_b ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
          (8u << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, int acc) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, int acc,
+                                       int elected) {
   asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n.reg .pred p, e;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 e, %5, 0;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(elected)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, int acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, int acc,
+                                       int elected) {
   asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n.reg .pred p, e;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 e, %5, 0;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(elected)
       : "memory");
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(v) : "r"(lo), "r"(hi));
+  return v;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -193,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsParams p) {
   auto empty = [&](int st) { return sbase + S::kBar + 8 * (kSt + st); };
   const uint32_t q_full = sbase + S::kBar + 8 * (2 * kSt);
   auto turn_bar = [&](int kind, int t) { return q_full + 8 + 8 * (2 * kind + t); };
-  enum { kSFull = 0, kPReady = 1, kPvDone = 2, kODone = 3 };
+  enum { kSFull = 0, kPReady = 1, kPReady2 = 2, kPvDone = 3, kODone = 4 };
   // warps of a turn that hold rows
   auto warps_of = [&](int t) {
     const int r = pair ? min(kTileRows, n_rows - t * kTileRows) : n_rows;
@@ -208,6 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsParams p) {
     for (int t = 0; t < 2; ++t) {
       mbar_init(turn_bar(kSFull, t), 2);
       mbar_init(turn_bar(kPReady, t), warps_of(t));
+      mbar_init(turn_bar(kPReady2, t), warps_of(t));
       mbar_init(turn_bar(kPvDone, t), 1);
       mbar_init(turn_bar(kODone, t), 1);
     }
@@ -235,21 +269,30 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsParams p) {
     const int t = warp >> 2, w = warp & 3;
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-    // Q rows into the swizzled tiles, all warps together. Without keys nothing
-    // reads them, and nothing would keep them from the turns' max and sum below.
+    // Q rows into the swizzled tiles, all warps together
     if (n_tiles > 0) {
       const int c = tid & (D / 8 - 1);
-      constexpr int kStep = 256 / (D / 8);
+      constexpr int kStep = 256 / (D / 8), kBatch = 8;
       const int total = pair ? 2 * kTileRows : kTileRows;
-      for (int r = tid / (D / 8); r < total; r += kStep) {
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (r < n_rows) {
-          const int x = row0 + r;
-          const size_t head = (size_t)(grp.first + x / p.g) * p.Hq + hkv * p.g + x % p.g;
-          v = __ldcg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + head * D) + c);
+      for (int r0 = tid / (D / 8); r0 < total; r0 += kBatch * kStep) {
+        uint4 v[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const int r = r0 + u * kStep;
+          v[u] = make_uint4(0u, 0u, 0u, 0u);
+          if (r < n_rows) {
+            const int x = row0 + r;
+            const size_t head = (size_t)(grp.first + x / p.g) * p.Hq + hkv * p.g + x % p.g;
+            v[u] = __ldcg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + head * D) + c);
+          }
         }
-        *reinterpret_cast<uint4*>(smem + S::kQ + (r >> 7) * S::kTileBytes + (c >> 3) * 16384 +
-                                  (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const int r = r0 + u * kStep;
+          if (r < total)
+            *reinterpret_cast<uint4*>(smem + S::kQ + (r >> 7) * S::kTileBytes + (c >> 3) * 16384 +
+                                      (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4)) = v[u];
+        }
       }
       fence_async_shared();
       __syncwarp();
@@ -277,8 +320,9 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsParams p) {
         }
         float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
-        for (int c = 0; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(x[c]));
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+        for (int c = 0; c < 128; c += 2)
+          mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+        const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * p.scale_log2;
         const bool move = top > m + kLazyMax;
         if (__any_sync(0xffffffffu, move)) {
           const float al = move ? fast_exp2(m - top) : 1.f;
@@ -297,25 +341,33 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsParams p) {
           }
         }
         const float base = m == -CUDART_INF_F ? 0.f : m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint64_t scale2 = pack2(__float_as_uint(p.scale_log2), __float_as_uint(p.scale_log2));
+        const uint64_t base2 = pack2(__float_as_uint(-base), __float_as_uint(-base));
+        uint64_t sum[2] = {0ull, 0ull};
+        // P in two halves: the product over the first runs under the second
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const float a = fast_exp2(fmaf(__uint_as_float(x[32 * c + 2 * e]), p.scale_log2, -base));
-            const float b = fast_exp2(fmaf(__uint_as_float(x[32 * c + 2 * e + 1]), p.scale_log2, -base));
-            sum[e & 1] += a;
-            sum[2 + (e & 1)] += b;
+            float a, b;
+            unpack2(fma2(pack2(x[32 * c + 2 * e], x[32 * c + 2 * e + 1]), scale2, base2), a, b);
+            a = fast_exp2(a);
+            b = fast_exp2(b);
+            sum[e & 1] = add2(sum[e & 1], pack2(__float_as_uint(a), __float_as_uint(b)));
             pk[e] = pack_bf16(a, b);
           }
           tc_st16(s_col(t) + lane_base + 16 * c, pk);
+          if (c & 1) {
+            tc_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(turn_bar(c == 1 ? kPReady : kPReady2, t));
+          }
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tc_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(turn_bar(kPReady, t));
+        float s0, s1;
+        unpack2(add2(sum[0], sum[1]), s0, s1);
+        l += s0 + s1;
       }
       // ---------------- output
       const int r = 32 * w + lane;   // row in the tile
@@ -346,42 +398,62 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsParams p) {
       const int rr = pair ? t * kTileRows + r : r;
       const bool mine = rr < n_rows;
       const int xr = row0 + (mine ? rr : 0);
-      const size_t head = (size_t)(grp.first + xr / p.g) * p.Hq + hkv * p.g + xr % p.g;
-      const size_t at = (size_t)split * p.rows * p.Hq + head;
+      const int head = (grp.first + xr / p.g) * p.Hq + hkv * p.g + xr % p.g;   // < 2^31, from the host
+      const size_t part = (size_t)split * p.rows * p.Hq;
       if (!direct && mine && (pair || t == 0))
-        *reinterpret_cast<float2*>(p.ml + 2 * at) = make_float2(m, l);
+        *reinterpret_cast<float2*>(p.ml + 2 * (part + head)) = make_float2(m, l);
       if (direct || n_tiles > 0) {
-        // a pair's turn writes its whole row, otherwise half of it
-        const int c0 = pair ? 0 : t * (D / 2), c1 = pair ? D : c0 + D / 2;
+        // Half the columns at a time go through this warp's share of its turn's
+        // Q tile (read to the end by now), so that rows leave as whole
+        // segments: a thread's own 16-byte stores touch 32 rows at once. A pair's
+        // turn writes whole rows, otherwise each turn half of them.
+        constexpr int kCw = D / 2;                  // columns a round
+        unsigned char* stage = smem + S::kQ + t * S::kTileBytes + w * (S::kTileBytes / 4);
+        const int valid = min(32, (pair ? n_rows - t * kTileRows : n_rows) - 32 * w);
 #pragma unroll 1
-        for (int c = c0; c < c1; c += 32) {
-          float o[32];
+        for (int round = 0; round < (pair ? 2 : 1); ++round) {
+          const int c0 = pair ? round * kCw : t * kCw;
+#pragma unroll 1
+          for (int c = 0; c < kCw; c += 32) {
+            float o[32];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0.f;
-          for (int u = pair ? t : 0; u < (pair ? t + 1 : 2); ++u) {
-            if (!have[u]) continue;
-            uint32_t y[32];
-            tc_ld32(y, o_col(u) + lane_base + c);
-            tc_loaded(y);
+            for (int e = 0; e < 32; ++e) o[e] = 0.f;
+            for (int u = pair ? t : 0; u < (pair ? t + 1 : 2); ++u) {
+              if (!have[u]) continue;
+              uint32_t y[32];
+              tc_ld32(y, o_col(u) + lane_base + c0 + c);
+              tc_loaded(y);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = fmaf(__uint_as_float(y[e]), wt[u], o[e]);
-          }
-          if (mine) {
+              for (int e = 0; e < 32; ++e) o[e] = fmaf(__uint_as_float(y[e]), wt[u], o[e]);
+            }
             if (direct) {
-              __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + head * D + c;
 #pragma unroll
               for (int e = 0; e < 32; e += 8)
-                *reinterpret_cast<uint4*>(dst + e) =
+                *reinterpret_cast<uint4*>(stage + lane * (kCw * 2) + ((((c + e) >> 3) ^ (lane & (kCw / 8 - 1))) << 4)) =
                     make_uint4(pack_bf16(o[e] * inv, o[e + 1] * inv), pack_bf16(o[e + 2] * inv, o[e + 3] * inv),
                                pack_bf16(o[e + 4] * inv, o[e + 5] * inv), pack_bf16(o[e + 6] * inv, o[e + 7] * inv));
             } else {
-              float* dst = p.acc + at * D + c;
 #pragma unroll
               for (int e = 0; e < 32; e += 4)
-                *reinterpret_cast<float4*>(dst + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                *reinterpret_cast<float4*>(stage + lane * (kCw * 4) + ((((c + e) >> 2) ^ (lane & 7)) << 4)) =
+                    make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
             }
           }
-          __syncwarp();   // TMEM loads are for whole warps
+          __syncwarp();
+          const int per_row = direct ? kCw / 8 : kCw / 4;   // 16-byte chunks of a row
+          const int swz = direct ? kCw / 8 - 1 : 7;
+          for (int e = lane; e < 32 * per_row; e += 32) {
+            const int q = e / per_row, ch = e % per_row;
+            const int hq = __shfl_sync(0xffffffffu, head, q);
+            const uint4 v = *reinterpret_cast<const uint4*>(stage + q * per_row * 16 + ((ch ^ (q & swz)) << 4));
+            if (q < valid) {
+              if (direct)
+                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + (size_t)hq * D + c0 + 8 * ch) = v;
+              else
+                *reinterpret_cast<uint4*>(p.acc + (part + hq) * D + c0 + 4 * ch) = v;
+            }
+          }
+          __syncwarp();
         }
       }
     }
@@ -395,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsParams p) {
     constexpr int kChunks = D / 8;                    // 16-byte chunks of a row
     constexpr int kRowsAtOnce = kLoadThreads / kChunks;
     const int c = lt % kChunks, r_lane = lt / kChunks;
-    constexpr int kLag = kSt - 2;                     // copies in flight behind the newest
+    constexpr int kLag = 2;                           // copies in flight behind the newest
     const uint64_t pol = l2_policy_evict_first();
     auto resolve = [&](int j) -> int {
       const int pos = lo + j * kKeyTile + lt;
@@ -408,6 +480,11 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsParams p) {
       if (lane == 0) masks[4 * (j % kMaskRing) + (warp - 8)] = live;
       if (j + 1 < n_tiles) next = resolve(j + 1);
       asm volatile("bar.sync 2, 128;\n" ::: "memory");
+      // this thread's cache rows, read together: a load between two copies
+      // would make each wait for the last (1050 instead of ... cycles a tile)
+      int row[128 / kRowsAtOnce];
+#pragma unroll
+      for (int i = 0; i < 128 / kRowsAtOnce; ++i) row[i] = rows[(j & 1) * 128 + i * kRowsAtOnce + r_lane];
 #pragma unroll 1
       for (int kv = 0; kv < 2; ++kv) {
         const int idx = 2 * j + kv, st = idx % kSt;
@@ -417,9 +494,8 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsParams p) {
 #pragma unroll
         for (int i = 0; i < 128 / kRowsAtOnce; ++i) {
           const int r = i * kRowsAtOnce + r_lane;
-          const int row = rows[(j & 1) * 128 + r];
-          cp_async16(dst0 + r * 128 + (((c & 7) ^ (r & 7)) << 4), src + (size_t)max(row, 0) * (D * 2),
-                     row >= 0 ? 16 : 0, pol);
+          cp_async16(dst0 + r * 128 + (((c & 7) ^ (r & 7)) << 4), src + (size_t)max(row[i], 0) * (D * 2),
+                     row[i] >= 0 ? 16 : 0, pol);
         }
         cp_async_commit();
         if (idx >= kLag) {
@@ -433,30 +509,46 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsParams p) {
     fence_async_shared();
     for (int idx = max(0, 2 * n_tiles - kLag); idx < 2 * n_tiles; ++idx) mbar_arrive(full(idx % kSt));
   } else {
-    // ---------------- MMA: one thread issues for the CTA
+    // ---------------- MMA: warp 12 issues for the CTA
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegsMma));
-    if (warp == 12 && lane == 0 && n_tiles > 0) {
+    if (warp == 12 && n_tiles > 0) {
+      uint32_t elected;
+      asm volatile(
+          "{\n.reg .pred e;\nelect.sync _|e, 0xffffffff;\nselp.u32 %0, 1, 0, e;\n}\n"
+          : "=r"(elected));
       constexpr uint32_t kIdQk = instruction(128, false), kIdPv = instruction(D, true);
+      constexpr uint64_t kKMajor = 1ull << 16, kVMajor = (uint64_t)(16384 >> 4) << 16;   // leading offsets
+      const uint64_t q_op = operand(sbase + S::kQ, 0, 1024), ring_op = operand(sbase + S::kRing, 0, 1024);
       auto wait_ring = [&](int idx) { mbar_wait(full(idx % kSt), (idx / kSt) & 1, dead); };
       auto qk = [&](int t, int j) {
-        const uint32_t a = sbase + S::kQ + (pair ? t : 0) * S::kTileBytes;
-        const uint32_t b = sbase + S::kRing + ((2 * j) % kSt) * S::kTileBytes;
+        const int st = (2 * j) % kSt;
+        const uint64_t a = q_op + ((pair ? t : 0) * S::kTileBytes >> 4) + kKMajor;
+        const uint64_t b = ring_op + (st * S::kTileBytes >> 4) + kKMajor;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
-          mma_ss(s_col(t), operand(a + off, 16, 1024), operand(b + off, 16, 1024), kIdQk, k > 0);
+          const uint32_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+          mma_ss(s_col(t), a + off, b + off, kIdQk, k > 0, elected);
         }
-        tc_commit(turn_bar(kSFull, t));
-        mbar_arrive(turn_bar(kSFull, t));   // orders the key mask before the softmax's reading
-        if (!pair || t == 1) tc_commit(empty((2 * j) % kSt));
+        tc_commit(turn_bar(kSFull, t), elected);
+        if (elected) mbar_arrive(turn_bar(kSFull, t));   // orders the key mask before the softmax's reading
+        __syncwarp();
+        if (!pair || t == 1) tc_commit(empty(st), elected);
       };
-      auto pv = [&](int t, int j, bool first, bool last) {
-        const uint32_t b = sbase + S::kRing + ((2 * j + 1) % kSt) * S::kTileBytes;
+      auto pv = [&](int t, int i, int j, bool first, bool last) {
+        const int st = (2 * j + 1) % kSt;
+        const uint64_t b = ring_op + (st * S::kTileBytes >> 4) + kVMajor;
+        mbar_wait(turn_bar(kPReady, t), i & 1, dead);
+        tc_fence_after();
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          mma_ts(o_col(t), s_col(t) + 8 * k, operand(b + 2048 * k, 16384, 1024), kIdPv, !first || k > 0);
-        tc_commit(turn_bar(last ? kODone : kPvDone, t));
-        if (!pair || t == 1) tc_commit(empty((2 * j + 1) % kSt));
+        for (int k = 0; k < 4; ++k)
+          mma_ts(o_col(t), s_col(t) + 8 * k, b + (2048 * k >> 4), kIdPv, !first || k > 0, elected);
+        mbar_wait(turn_bar(kPReady2, t), i & 1, dead);
+        tc_fence_after();
+#pragma unroll
+        for (int k = 4; k < 8; ++k)
+          mma_ts(o_col(t), s_col(t) + 8 * k, b + (2048 * k >> 4), kIdPv, 1, elected);
+        tc_commit(turn_bar(last ? kODone : kPvDone, t), elected);
+        if (!pair || t == 1) tc_commit(empty(st), elected);
       };
       mbar_wait(q_full, 0, dead);
       tc_fence_after();
@@ -467,14 +559,13 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsParams p) {
           qk(t, tile_of(t, 0));
         }
       for (int i = 0; i < count_of(0); ++i)
+#pragma unroll
         for (int t = 0; t < 2; ++t) {
           const int n = count_of(t);
           if (i >= n) continue;
           const bool last = i + 1 == n;
           wait_ring(2 * tile_of(t, i) + 1);
-          mbar_wait(turn_bar(kPReady, t), i & 1, dead);
-          tc_fence_after();
-          pv(t, tile_of(t, i), i == 0, last);
+          pv(t, i, tile_of(t, i), i == 0, last);
           if (!last) {
             wait_ring(2 * tile_of(t, i + 1));
             mbar_wait(turn_bar(kPvDone, t), i & 1, dead);   // S overwrites the P that PV reads
