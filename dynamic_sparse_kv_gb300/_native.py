@@ -227,7 +227,8 @@ def fastocr_rswa_attend(handle, q, kv: fastocr_kv, prefix_len, window, out, stre
 
 
 def fastocr_rows_workspace(handle, rows) -> int:
-    """Workspace bytes of fastocr_shared_attend / fastocr_cross_attend over `rows` query tokens."""
+    """Workspace bytes of fastocr_cross_attend over up to `rows` query tokens, or of
+    fastocr_shared_attend (rows = 0)."""
     n = lib.fastocr_rows_workspace(handle, int(rows))
     if n < 0:
         raise FastOCRError("fastocr_rows_workspace", int(n))
@@ -270,7 +271,7 @@ def fastocr_evict(handle, kv: fastocr_kv, weights: fastocr_weights, budget, rece
                              int(recent), _ptr(new_len), _stream(stream)))
 
 
-def fastocr_cross_attend(handle, q, kv: fastocr_kv, q_start, rows, out, ws=None, ws_bytes=0,
+def fastocr_cross_attend(handle, q, kv: fastocr_kv, q_start, rows, out, ws, ws_bytes,
                          stream=None) -> None:
     """Packed, ragged queries against all states of their sequence."""
     _check("fastocr_cross_attend",

@@ -17,11 +17,11 @@ class CrossAttention:
     k_cache, v_cache: [layers, num_pages, H_kv, page_size, d] (bf16 or fp32)
     block_table: [B, pages_per_seq] int32; state_len: int or [B] int32, states a
     sequence has (a device int32 tensor is taken as it is and may change).
-    max_rows: query tokens of the largest call, for the workspace; a larger
-    call works, with its keys split less.
+    max_rows: query tokens of the largest call, for the workspace (None: any).
     """
 
-    def __init__(self, k_cache, v_cache, block_table, state_len, *, q_heads: int, max_rows: int = 0):
+    def __init__(self, k_cache, v_cache, block_table, state_len, *, q_heads: int,
+                 max_rows: int | None = None):
         assert k_cache.is_cuda and k_cache.shape == v_cache.shape
         self.k_cache, self.v_cache = k_cache, v_cache
         self.layers, _, self.kv_heads, self.page_size, self.head_dim = k_cache.shape
@@ -37,8 +37,9 @@ class CrossAttention:
                                        self.page_size, self.block_table.shape[1], 0, self.layers)
         self.kv = [N.make_kv(k_cache[l], v_cache[l], self.block_table, self.state_len)
                    for l in range(self.layers)]
-        n = N.fastocr_rows_workspace(self.handle, max_rows)
-        self.ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+        # the workspace stops growing where the rows of a sequence fill a row tile
+        n = N.fastocr_rows_workspace(self.handle, max(1, 256 if max_rows is None else max_rows))
+        self.ws = torch.empty(n, dtype=torch.uint8, device=dev)
 
     def close(self):
         if self.handle:
@@ -67,7 +68,7 @@ class CrossAttention:
         if rows == 0:
             return
         N.fastocr_cross_attend(self.handle, q, self.kv[l], q_start, rows, out, self.ws,
-                               self.ws.numel() if self.ws is not None else 0, stream)
+                               self.ws.numel(), stream)
 
     def device_status(self, stream=None) -> int:
         return N.fastocr_device_status(self.handle, stream)

@@ -50,44 +50,55 @@ RowsParams rows_params(const fastocr_handle* h, const void* q, const fastocr_kv*
   p.g = d.num_q_heads / d.num_kv_heads;
   p.scale_log2 = (float)(1.4426950408889634 / sqrt((double)d.head_dim));
   p.status = h->status;
+  p.min_units = 1;
   return p;
 }
 
-// Bytes of one part's partials of `rows` query tokens.
-int64_t part_bytes(const fastocr_handle* h, int64_t rows) {
-  return rows * h->dims.num_q_heads * (int64_t)(h->dims.head_dim + 2) * (int64_t)sizeof(float);
-}
-
-// Query rows a CTA holds.
+// Rows of a row tile and of a slot of the workspace, for `rows` query tokens.
 int tile_rows(const fastocr_handle* h) {
-  return h->dims.dtype == FASTOCR_DTYPE_BF16 ? kRowsBf16 : kRowsF32;
+  const int bm = h->dims.dtype == FASTOCR_DTYPE_BF16 ? kRowsBf16 : kRowsF32;
+  const int g = h->dims.num_q_heads / h->dims.num_kv_heads;
+  return bm / g * g;
+}
+int64_t slot_rows(const fastocr_handle* h, int64_t rows) {
+  return std::min<int64_t>(tile_rows(h), rows * (h->dims.num_q_heads / h->dims.num_kv_heads));
 }
 
-// Parts the keys are cut into when about `tiles` row tiles a KV head run at
-// once: enough CTAs for every SM.
-int most_parts(const fastocr_handle* h, int64_t tiles) {
-  const int64_t items = std::max<int64_t>(1, tiles) * h->dims.num_kv_heads;
-  return (int)std::min<int64_t>(kMaxExt, std::max<int64_t>(1, h->num_sms / items));
+// Lays the workspace out for `rows` query tokens from `base` on and returns its
+// size: the slots, then what the readers of the parts need (see rows.cuh).
+int64_t place_workspace(const fastocr_handle* h, int64_t rows, bool shared, char* base, RowsParams& p) {
+  const int64_t d = h->dims.head_dim, Hq = h->dims.num_q_heads, Hkv = h->dims.num_kv_heads;
+  const int64_t sr = slot_rows(h, rows), slots = 2 * (int64_t)h->num_sms * sr;
+  size_t at = 0;
+  auto take = [&](int64_t bytes) {
+    char* x = base + at;
+    at = align_up(at + (size_t)bytes, 256);
+    return x;
+  };
+  p.slot_rows = (int)sr;
+  p.slot_acc = reinterpret_cast<float*>(take(slots * d * 4));
+  p.slot_ml = reinterpret_cast<float*>(take(slots * 8));
+  if (shared) {
+    p.token_part = reinterpret_cast<int4*>(take(rows * Hkv * 16));
+    p.row_acc = reinterpret_cast<float*>(take(rows * Hq * d * 4));
+    p.row_ml = reinterpret_cast<float*>(take(rows * Hq * 8));
+  } else {
+    p.item_part = reinterpret_cast<int4*>(take((int64_t)h->num_sms * 32));
+  }
+  return (int64_t)at;
 }
 
-int choose_parts(const fastocr_handle* h, int64_t tiles, long keys, int64_t ws_bytes, int64_t rows) {
-  const long key_tiles = std::max(1L, (keys + kKeyTile - 1) / kKeyTile);
-  int64_t s = std::min<int64_t>(most_parts(h, tiles), key_tiles);
-  if (rows > 0) s = std::min<int64_t>(s, ws_bytes / part_bytes(h, rows));
-  return (int)std::max<int64_t>(1, s);
+// The kernels count units of work in 32 bits.
+bool units_fit(const fastocr_handle* h, int64_t rows, int64_t groups) {
+  const int64_t g = h->dims.num_q_heads / h->dims.num_kv_heads;
+  const int64_t tiles = rows * g / tile_rows(h) + std::min(rows, groups);
+  return (double)tiles * h->dims.num_kv_heads * (max_tokens(h) / kKeyTile + 1) < 2147483647.0;
 }
 
 fastocr_status launch_rows(const fastocr_handle* h, const RowsParams& p, cudaStream_t s) {
-  const cudaError_t e = h->dims.dtype == FASTOCR_DTYPE_BF16 ? launch_rows_bf16(h->dims.head_dim, p, s)
-                                                            : launch_rows_f32(h->dims.head_dim, p, s);
+  const cudaError_t e = h->dims.dtype == FASTOCR_DTYPE_BF16 ? launch_rows_bf16(h->dims.head_dim, h->num_sms, p, s)
+                                                            : launch_rows_f32(h->dims.head_dim, h->num_sms, p, s);
   return e == cudaSuccess ? FASTOCR_OK : FASTOCR_ERR_CUDA;
-}
-
-// Places the partials in the caller's workspace: outputs first (16-byte
-// aligned), then the row statistics.
-void place_parts(const fastocr_handle* h, void* ws, RowsParams& p) {
-  p.acc = static_cast<float*>(ws);
-  p.ml = p.acc + (size_t)p.splits * p.rows * p.Hq * h->dims.head_dim;
 }
 
 }  // namespace
@@ -97,9 +108,8 @@ extern "C" {
 int64_t fastocr_rows_workspace(const fastocr_handle* h, int64_t rows) {
   if (!h) return FASTOCR_ERR_NULL;
   if (rows < 0 || rows * h->dims.num_q_heads >= (1LL << 31)) return FASTOCR_ERR_INVALID;
-  const int bm = tile_rows(h);
-  const int g = h->dims.num_q_heads / h->dims.num_kv_heads;
-  return part_bytes(h, rows) * most_parts(h, (rows * g + bm - 1) / bm);
+  RowsParams p;
+  return place_workspace(h, rows > 0 ? rows : h->dims.batch, rows == 0, nullptr, p);
 }
 
 fastocr_status fastocr_shared_attend(fastocr_handle* h, const void* q, const fastocr_kv* kv,
@@ -113,31 +123,31 @@ fastocr_status fastocr_shared_attend(fastocr_handle* h, const void* q, const fas
   const int64_t B = h->dims.batch;
   if (groups->n < 1 || groups->n > B || groups->max_prefix < 0) return FASTOCR_ERR_INVALID;
   if (weights && (st = check_weights(weights, true)) != FASTOCR_OK) return st;
-  if (ws_bytes < part_bytes(h, B)) return FASTOCR_ERR_INVALID;
+  RowsParams r = rows_params(h, q, kv);
+  if (ws_bytes < place_workspace(h, B, true, static_cast<char*>(ws), r)) return FASTOCR_ERR_INVALID;
+  if (!units_fit(h, B, groups->n)) return FASTOCR_ERR_UNSUPPORTED;
   if ((st = check_device(h)) != FASTOCR_OK) return st;
 
-  const long all = expected_tokens(h);
-  const long prefix = groups->max_prefix > 0 ? std::min<long>(groups->max_prefix, all) : all;
-  RowsParams r = rows_params(h, q, kv);
   r.n_groups = groups->n;
   r.start = groups->start;
   r.prefix_len = groups->prefix_len;
-  r.rows = B;
-  const int bm = tile_rows(h);
-  const int64_t tiles = std::max<int64_t>(groups->n, (B * r.g + bm - 1) / bm);
-  r.splits = choose_parts(h, tiles, prefix, ws_bytes, B);
-  place_parts(h, ws, r);
+  r.rows = (int)B;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if ((st = launch_rows(h, r, s)) != FASTOCR_OK) return st;
 
+  const long all = expected_tokens(h);
+  const long prefix = groups->max_prefix > 0 ? std::min<long>(groups->max_prefix, all) : 0;
   Params p = base_params(h, q, kv, out);
   p.first = groups->prefix_len;
-  p.ext_acc = r.acc;
-  p.ext_ml = r.ml;
-  p.ext_splits = r.splits;
+  p.ext_part = r.token_part;
+  p.ext_slot_acc = r.slot_acc;
+  p.ext_slot_ml = r.slot_ml;
+  p.ext_row_acc = r.row_acc;
+  p.ext_row_ml = r.row_ml;
+  p.ext_slot_rows = r.slot_rows;
+  p.ext_ctas = h->num_sms;
   if (weights) set_weights(weights, p);
-  return launch(h, weights ? kWeigh : kTail, std::max(1L, all - (groups->max_prefix > 0 ? prefix : 0)),
-                p, stream);
+  return launch(h, weights ? kWeigh : kTail, std::max(1L, all - prefix), p, stream);
 }
 
 fastocr_status fastocr_weigh_attend(fastocr_handle* h, const void* q, const fastocr_kv* kv,
@@ -201,26 +211,25 @@ fastocr_status fastocr_evict(fastocr_handle* h, const fastocr_kv* kv, const fast
 fastocr_status fastocr_cross_attend(fastocr_handle* h, const void* q, const fastocr_kv* kv,
                                     const int32_t* q_start, int64_t rows, void* out, void* ws,
                                     int64_t ws_bytes, fastocr_stream stream) {
-  if (!h || !q || !out || !q_start) return FASTOCR_ERR_NULL;
+  if (!h || !q || !out || !q_start || !ws) return FASTOCR_ERR_NULL;
   fastocr_status st = check_kv(h, kv);
   if (st != FASTOCR_OK) return st;
   if (!aligned16(q) || !aligned16(out) || !aligned16(ws)) return FASTOCR_ERR_ALIGN;
-  if (rows < 0 || ws_bytes < 0 || rows * h->dims.num_q_heads >= (1LL << 31))
+  if (rows < 0 || rows * h->dims.num_q_heads >= (1LL << 31)) return FASTOCR_ERR_INVALID;
+  RowsParams p = rows_params(h, q, kv);
+  if (rows > 0 && ws_bytes < place_workspace(h, rows, false, static_cast<char*>(ws), p))
     return FASTOCR_ERR_INVALID;
+  if (!units_fit(h, rows, h->dims.batch)) return FASTOCR_ERR_UNSUPPORTED;
   if ((st = check_device(h)) != FASTOCR_OK) return st;
   if (rows == 0) return FASTOCR_OK;
-  RowsParams p = rows_params(h, q, kv);
   p.out = out;
   p.n_groups = h->dims.batch;
   p.start = q_start;
-  p.rows = rows;
-  const int bm = tile_rows(h);
-  const int64_t tiles = std::max<int64_t>(std::min<int64_t>(p.n_groups, rows), (rows * p.g + bm - 1) / bm);
-  p.splits = choose_parts(h, tiles, expected_tokens(h), ws ? ws_bytes : 0, rows);
-  if (p.splits > 1) place_parts(h, ws, p);
+  p.rows = (int)rows;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if ((st = launch_rows(h, p, s)) != FASTOCR_OK || p.splits == 1) return st;
-  return launch_rows_merge(h->dims.head_dim, h->dims.dtype == FASTOCR_DTYPE_BF16, p, s) == cudaSuccess
+  if ((st = launch_rows(h, p, s)) != FASTOCR_OK) return st;
+  return launch_rows_merge(h->dims.head_dim, h->dims.dtype == FASTOCR_DTYPE_BF16, h->num_sms, p, s) ==
+                 cudaSuccess
              ? FASTOCR_OK
              : FASTOCR_ERR_CUDA;
 }

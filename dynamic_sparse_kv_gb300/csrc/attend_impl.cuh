@@ -667,6 +667,9 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
       ++pre_issued;
     }
   }
+  int4 ext = make_int4(0, 0, 0, 0);   // where the prefix's parts are
+  if constexpr (MODE == kTail || MODE == kWeigh)
+    if (p.ext_part) ext = __ldcg(p.ext_part + (size_t)b * p.Hkv + hkv);
   WarpStateMma<D> sm_;
   WarpStateF32<D> sf_;
   const int gid = lane >> 2, tig = lane & 3;
@@ -1043,24 +1046,37 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
   constexpr bool kExternal = MODE == kTail || MODE == kWeigh;
   float2* xml = reinterpret_cast<float2*>(smem + E::kExt);   // [8][kMaxExt]
   const size_t q_row0 = (size_t)b * p.Hq + (size_t)hkv * p.g;
-  const size_t q_rows = (size_t)p.B * p.Hq;
+  int n_ext = 0;
+  // index of head h in part s
+  auto ext_row = [&](int s, int h) -> size_t {
+    return n_ext == 1 ? q_row0 + h
+                      : (size_t)(2 * (ext.x + s) + (s == 0 ? ext.z : 0)) * p.ext_slot_rows + ext.w + h;
+  };
   if constexpr (kExternal) {
-    for (int e = tid; e < p.g * p.ext_splits; e += kThreads) {
+    // a sequence in no group has no parts, whatever an earlier call left there
+    if (p.ext_part) {
+      if (ext.y >= 1 && ext.y <= kMaxExt && ext.x >= 0 && ext.x + ext.y <= p.ext_ctas &&
+          (ext.z & ~1) == 0 && ext.w >= 0 && ext.w + p.g <= p.ext_slot_rows)
+        n_ext = ext.y;
+      else
+        bad |= kDevBadGroup;
+    }
+    for (int e = tid; e < p.g * n_ext; e += kThreads) {
       const int h = e % p.g, s = e / p.g;
       xml[h * kMaxExt + s] =
-          __ldcg(reinterpret_cast<const float2*>(p.ext_ml) + (size_t)s * q_rows + q_row0 + h);
+          __ldcg(reinterpret_cast<const float2*>(n_ext == 1 ? p.ext_row_ml : p.ext_slot_ml) + ext_row(s, h));
     }
   }
   // joins head h's external maxima to M, and sum(l * 2^(m - base)) over them
   auto ext_max = [&](int h, float M) -> float {
     if constexpr (kExternal)
-      for (int s = 0; s < p.ext_splits; ++s) M = fmaxf(M, xml[h * kMaxExt + s].x);
+      for (int s = 0; s < n_ext; ++s) M = fmaxf(M, xml[h * kMaxExt + s].x);
     return M;
   };
   auto ext_sum = [&](int h, float base) -> float {
     float L = 0.f;
     if constexpr (kExternal)
-      for (int s = 0; s < p.ext_splits; ++s) {
+      for (int s = 0; s < n_ext; ++s) {
         const float2 ml = xml[h * kMaxExt + s];
         L = fmaf(ml.y, fast_exp2(ml.x - base), L);
       }
@@ -1070,17 +1086,25 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
   // whose sum is 0 has no rows and its output was not written
   auto ext_add = [&](int h, int c4, float base, int s0, int step, float4& a) {
     if constexpr (kExternal) {
-      const float4* src = reinterpret_cast<const float4*>(p.ext_acc) + (q_row0 + h) * (D / 4) + c4;
-#pragma unroll 4
-      for (int s = s0; s < p.ext_splits; s += step) {
-        const float2 ml = xml[h * kMaxExt + s];
-        if (ml.y == 0.f) continue;
-        const float4 v = __ldcg(src + (size_t)s * q_rows * (D / 4));
-        const float sc = fast_exp2(ml.x - base);
-        a.x = fmaf(v.x, sc, a.x);
-        a.y = fmaf(v.y, sc, a.y);
-        a.z = fmaf(v.z, sc, a.z);
-        a.w = fmaf(v.w, sc, a.w);
+      const float4* src = reinterpret_cast<const float4*>(n_ext == 1 ? p.ext_row_acc : p.ext_slot_acc) + c4;
+      constexpr int kAtOnce = 8;
+      for (int s = s0; s < n_ext; s += kAtOnce * step) {
+        float4 v[kAtOnce];
+        float sc[kAtOnce];
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+          const int x = s + u * step;
+          const float2 ml = x < n_ext ? xml[h * kMaxExt + x] : make_float2(0.f, 0.f);
+          sc[u] = ml.y != 0.f ? fast_exp2(ml.x - base) : 0.f;
+          v[u] = ml.y != 0.f ? __ldcg(src + ext_row(x, h) * (D / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+          a.x = fmaf(v[u].x, sc[u], a.x);
+          a.y = fmaf(v[u].y, sc[u], a.y);
+          a.z = fmaf(v[u].z, sc[u], a.z);
+          a.w = fmaf(v[u].w, sc[u], a.w);
+        }
       }
     }
   };

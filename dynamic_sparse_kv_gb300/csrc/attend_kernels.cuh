@@ -113,11 +113,16 @@ struct Params {
   int32_t* status;
   int max_img;
   // tail / weigh: the list starts at row first[b] (NULL: 0); the softmax over
-  // the rows before it comes as ext_splits partials per query row
+  // the rows before it comes in parts that the row kernel left: where, it says
   const int32_t* first;
-  const float* ext_ml;       // [ext_splits, B*H_q, 2]: max (base 2), sum
-  const float* ext_acc;      // [ext_splits, B*H_q, d]: unnormalised output
-  int ext_splits;            // <= kMaxExt; 0: none
+  // at ext_part[b * H_kv + j] = (first CTA, parts, its slot, row in the slot),
+  // in two slots a CTA, or as whole rows where there is one part (rows.cuh)
+  const int4* ext_part;      // NULL: none
+  const float* ext_slot_acc; // [ext_ctas, 2, ext_slot_rows, d]: unnormalised output
+  const float* ext_slot_ml;  // [ext_ctas, 2, ext_slot_rows, 2]: max (base 2), sum
+  const float* ext_row_acc;  // [B, H_q, d]
+  const float* ext_row_ml;   // [B, H_q, 2]
+  int ext_slot_rows, ext_ctas;
   // weigh: rows [protect[b], N_t) have weights, row r at index r - protect[b]
   float* mass;               // [B, H_kv, w_stride]
   int32_t* row_pos;          // [B, H_kv, w_stride]

@@ -1,10 +1,16 @@
 // Attention of many query rows to one list of keys: a prefix that a group of
 // decode sequences shares, or an encoder's states under a sequence's packed
-// queries. Row r of group i and KV head j is query token start[i] + r / g, head
-// j*g + r % g; all rows of the group attend to keys [0, len_i) of one block
-// table row, without a mask. The keys are cut into `splits` parts; every part
-// leaves (max, sum, unnormalised output) of each row, in base 2, in the
-// caller's workspace, or the output itself where one part has all keys.
+// queries. All query tokens of group i attend to keys [0, len_i) of one block
+// table row, without a mask.
+//
+// The work is a list of items -- (row tile, KV head) of every group, a row tile
+// holding as many whole tokens (g rows each) as fit BM rows -- and an item's
+// keys are a run of units. The units of all items, in order, are dealt out in
+// equal runs to one CTA per SM, whatever the groups' sizes: a CTA walks over
+// segments of items, of which only the first and the last can be cut. A cut
+// segment leaves (max, sum, unnormalised output) of its rows, in base 2, in one
+// of the CTA's two slots of the workspace; who reads them (the tail's attend
+// kernel, or merge_kernel) joins an item's parts in the order of their keys.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -16,7 +22,9 @@
 
 namespace fastocr {
 
-constexpr int kKeyTile = 128;   // keys a split's share is counted in
+constexpr int kKeyTile = 128;
+constexpr int kRowsF32 = 64;     // BM per dtype
+constexpr int kRowsBf16 = 256;
 
 struct RowsParams {
   const void* q;              // [rows, H_q, d]
@@ -30,91 +38,214 @@ struct RowsParams {
   int n_groups;
   const int32_t* start;       // [n_groups + 1]
   const int32_t* prefix_len;  // shared prefix: [B]; NULL: group i reads all of sequence i
-  long rows;                  // query tokens
-  int splits;
-  float* ml;                  // [splits, rows * H_q, 2]
-  float* acc;                 // [splits, rows * H_q, d]
+  int rows;                   // query tokens
+  int min_units;              // least units a CTA takes
+  // workspace
+  int slot_rows;              // rows a slot holds
+  float* slot_acc;            // [CTAs, 2, slot_rows, d]
+  float* slot_ml;             // [CTAs, 2, slot_rows, 2]: max, sum
+  int4* token_part;           // shared: [rows, H_kv] where a token's parts are (TokenParts)
+  float* row_acc;             // shared: [rows, H_q, d], rows that one CTA has all keys of
+  float* row_ml;              // shared: [rows, H_q, 2]
+  int4* item_part;            // cross: [CTAs, 2] the cut item that starts in each CTA
   float scale_log2;
   int32_t* status;
 };
 
-// One group as a CTA sees it.
+// token_part: x = first CTA, y = parts, z = the first CTA's slot, w = row in the
+// slot; with y == 1 the token's rows are in row_acc / row_ml.
+// item_part: [0] x = first token, y = rows, z = KV head, w = parts (0: none);
+// [1].x = the first CTA's slot.
+
+// The keys of a group and where its tokens are.
 struct RowGroup {
-  int first;       // its first query token
-  int n_rows;      // (tokens of the group) * g
-  int table_row;   // sequence whose block table holds the keys
-  int len;         // keys
-  int tile;        // this CTA's row tile in the group; -1: no tile left
+  int first, n_tok;   // query tokens
+  int table_row;      // sequence whose block table holds the keys
+  int len;            // keys
 };
 
-// Finds row tile `tile` (BM rows each, groups in order) by scanning the groups
-// 32 at a time; called by one whole warp, every lane gets the result. Lengths
-// and offsets out of range are clamped; faults are ORed into bad.
-template <int BM>
-__device__ __forceinline__ RowGroup find_tile(const RowsParams& p, int tile, int& bad) {
-  const int lane = threadIdx.x & 31;
+// Group i, offsets and lengths clamped into range; faults are ORed into bad.
+__device__ __forceinline__ RowGroup load_group(const RowsParams& p, int i, int& bad) {
   RowGroup r;
-  r.tile = -1;
-  r.first = r.n_rows = r.table_row = r.len = 0;
-  const int rows = (int)p.rows;
-  int base = 0;   // tiles of the groups before this round's
-  for (int i0 = 0; i0 < p.n_groups; i0 += 32) {
-    const int i = i0 + lane;
-    int s = 0, e = 0;
-    if (i < p.n_groups) {
-      s = __ldcg(p.start + i);
-      e = __ldcg(p.start + i + 1);
-      if (s < 0 || e < s || e > rows || (i == 0 && s != 0) ||
-          (p.prefix_len && i == p.n_groups - 1 && e != rows))
-        bad |= kDevBadGroup;
-      s = min(max(s, 0), rows);
-      e = min(max(e, s), rows);
+  int s = __ldcg(p.start + i), e = __ldcg(p.start + i + 1);
+  if (s < 0 || e < s || e > p.rows || (i == 0 && s != 0) ||
+      (p.prefix_len && i == p.n_groups - 1 && e != p.rows))
+    bad |= kDevBadGroup;
+  s = min(max(s, 0), p.rows);
+  e = min(max(e, s), p.rows);
+  r.first = s;
+  r.n_tok = e - s;
+  r.table_row = p.prefix_len ? s : i;
+  r.len = 0;
+  if (e > s) {
+    const int cap = p.max_pages << p.log2_page;
+    int len = __ldcg((p.prefix_len ? p.prefix_len : p.seq_len) + r.table_row);
+    int most = cap;
+    if (p.prefix_len) most = min(max(__ldcg(p.seq_len + r.table_row), 0), cap);
+    if (len < 0 || len > most) {
+      bad |= p.prefix_len ? kDevBadGroup : kDevBadSeqLen;
+      len = len < 0 ? 0 : most;
     }
-    const int tiles = ((e - s) * p.g + BM - 1) / BM;
-    int incl = tiles;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    const unsigned hit = __ballot_sync(0xffffffffu, base + incl > tile);
-    if (hit) {
-      const int src = __ffs(hit) - 1;
-      r.tile = tile - base - __shfl_sync(0xffffffffu, incl - tiles, src);
-      r.first = __shfl_sync(0xffffffffu, s, src);
-      r.n_rows = (__shfl_sync(0xffffffffu, e, src) - r.first) * p.g;
-      const int group = i0 + src;
-      const int cap = p.max_pages << p.log2_page;
-      r.table_row = p.prefix_len ? r.first : group;
-      int len = __ldcg((p.prefix_len ? p.prefix_len : p.seq_len) + r.table_row);
-      int most = cap;
-      if (p.prefix_len) most = min(max(__ldcg(p.seq_len + r.table_row), 0), cap);
-      if (len < 0 || len > most) {
-        bad |= p.prefix_len ? kDevBadGroup : kDevBadSeqLen;
-        len = len < 0 ? 0 : most;
-      }
-      r.len = len;
-      return r;
-    }
-    base += __shfl_sync(0xffffffffu, incl, 31);
+    r.len = len;
   }
   return r;
 }
 
-// The sequences of a group must agree on their prefix; every thread of the CTA
-// checks some.
-__device__ __forceinline__ void check_group(const RowsParams& p, const RowGroup& r, int& bad) {
+// The sequences of a group must agree on their prefix; `n` threads, of which
+// this is number `t`, check some each.
+__device__ __forceinline__ void check_group(const RowsParams& p, const RowGroup& r, int t, int n, int& bad) {
   if (!p.prefix_len) return;
-  for (int i = threadIdx.x; i < r.n_rows / p.g; i += blockDim.x)
+  for (int i = t; i < r.n_tok; i += n)
     if (__ldcg(p.prefix_len + r.first + i) != r.len) bad |= kDevBadGroup;
 }
 
-// Keys [lo, hi) of part `split`.
-__device__ __forceinline__ void split_range(int len, int splits, int split, int& lo, int& hi) {
-  const int tiles = (len + kKeyTile - 1) / kKeyTile;
-  const int per = (tiles + splits - 1) / splits;
-  lo = min(len, split * per * kKeyTile);
-  hi = min(len, lo + per * kKeyTile);
+// Units of an item: its key tiles. An item without keys still has one unit,
+// which writes its empty result.
+__device__ __forceinline__ int units_of(int len) { return max(1, (len + kKeyTile - 1) / kKeyTile); }
+
+// A run of key tiles of one item.
+struct Segment {
+  RowGroup grp;
+  int tok0, n_rows;     // the item's first token (of all) and rows
+  int hkv;
+  int k0, k1;           // key tiles
+  bool whole;           // all of the item's keys
+  bool starts;          // the item starts in this CTA
+  int slot;             // where its part goes if it is cut
+  int parts;            // starts: CTAs that share the item
+};
+
+// A CTA's walk over its segments. Units are counted in 32 bits: the host refuses
+// a call whose groups could have 2^31 of them.
+struct Walk {
+  int unit, end;     // the CTA's units [unit, end)
+  int begin, per;    // its first unit; units a CTA takes
+  int group, off;    // group and unit within it
+  RowGroup grp;
+};
+
+// Row r of an item is token r / g, head r % g: the quotient for r < 256, g <= 8.
+__device__ __forceinline__ int token_of_row(int r, int g_inv) { return (r * g_inv) >> 16; }
+__device__ __forceinline__ int inverse_of(int g) { return (65535 + g) / g; }
+
+// Units of a whole group.
+template <int BM>
+__device__ __forceinline__ int group_units(const RowsParams& p, const RowGroup& r) {
+  const int tpt = BM / p.g;
+  return (r.n_tok + tpt - 1) / tpt * p.Hkv * units_of(r.len);
+}
+
+struct PlanSmem {
+  int warp_sum[32], warp_max[32];
+  int group, off;
+  RowGroup grp;
+};
+
+// Where this CTA's units are; called by all THREADS threads. False: it has none.
+template <int BM, int THREADS>
+__device__ __forceinline__ bool plan_walk(const RowsParams& p, PlanSmem& s, Walk& w, int& bad) {
+  constexpr int NW = THREADS / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int chunk = (p.n_groups + THREADS - 1) / THREADS;   // consecutive groups a thread sums
+  const int i0 = min(p.n_groups, tid * chunk), i1 = min(p.n_groups, i0 + chunk);
+  int sum = 0, most = 0;
+  RowGroup grp = {0, 0, 0, 0};
+  for (int i = i0; i < i1; ++i) {
+    grp = load_group(p, i, bad);
+    sum += group_units<BM>(p, grp);
+    most = max(most, grp.n_tok > 0 ? units_of(grp.len) : 0);
+  }
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 31) s.warp_sum[warp] = incl;
+  if (lane == 0) s.warp_max[warp] = most;
+  __syncthreads();
+  int before = 0, all = 0;
+#pragma unroll
+  for (int v = 0; v < NW; ++v) {
+    if (v < warp) before += s.warp_sum[v];
+    all += s.warp_sum[v];
+    most = max(most, s.warp_max[v]);
+  }
+  const int mine = before + incl - sum, C = gridDim.x;
+  // an item's parts fit the merging kernels' lists
+  w.per = max((all + C - 1) / C, max(p.min_units, (most + kMaxExt - 3) / (kMaxExt - 2)));
+  const long long first = (long long)blockIdx.x * w.per;
+  if (first >= all) return false;
+  w.begin = w.unit = (int)first;
+  w.end = (int)min((long long)all, first + w.per);
+  if (mine <= w.unit && w.unit < mine + sum) {
+    int at = mine, i = i0;
+    if (chunk > 1) {   // which of this thread's groups
+      for (;; ++i) {
+        int none = 0;
+        grp = load_group(p, i, none);
+        const int u = group_units<BM>(p, grp);
+        if (w.unit < at + u) break;
+        at += u;
+      }
+    }
+    s.group = i;
+    s.off = w.unit - at;
+    s.grp = grp;
+  }
+  __syncthreads();
+  w.group = s.group;
+  w.off = s.off;
+  w.grp = s.grp;
+  return true;
+}
+
+// The next segment; false at the end. Warp-uniform.
+template <int BM>
+__device__ __forceinline__ bool next_segment(const RowsParams& p, Walk& w, Segment& s) {
+  if (w.unit >= w.end) return false;
+  const int tpt = BM / p.g;
+  while (w.off >= group_units<BM>(p, w.grp)) {   // another group with rows exists: w.unit < w.end
+    int none = 0;                                // reported by plan_walk
+    w.grp = load_group(p, ++w.group, none);
+    w.off = 0;
+  }
+  const int u = units_of(w.grp.len);
+  const int item = w.off / u, k = w.off - item * u;   // item in the group, unit in the item
+  const int tile = item / p.Hkv;
+  const int n = min(u - k, w.end - w.unit);
+  s.hkv = item - tile * p.Hkv;
+  s.grp = w.grp;
+  s.tok0 = w.grp.first + tile * tpt;
+  s.n_rows = min(tpt, w.grp.n_tok - tile * tpt) * p.g;
+  s.k0 = k;
+  s.k1 = min((w.grp.len + kKeyTile - 1) / kKeyTile, k + n);
+  s.whole = n == u;
+  s.starts = k == 0;
+  s.slot = w.unit == w.begin ? 0 : 1;
+  s.parts = (w.unit + u - 1) / w.per - (int)blockIdx.x + 1;   // of an item that starts here
+  w.unit += n;
+  w.off += n;
+  return true;
+}
+
+// Tells the tail's attend kernel where the parts of a shared prefix's item that
+// starts here are; `n` threads, of which this is number `t`.
+__device__ __forceinline__ void publish_parts(const RowsParams& p, const Segment& s, int t, int n) {
+  if (!p.token_part || !s.starts) return;
+  for (int i = t; i < s.n_rows / p.g; i += n)
+    p.token_part[(size_t)(s.tok0 + i) * p.Hkv + s.hkv] = make_int4(blockIdx.x, s.parts, s.slot, i * p.g);
+}
+
+// Tells merge_kernel the cut item that starts in this CTA (cross attention):
+// only its last segment can be one.
+__device__ __forceinline__ void publish_cut(const RowsParams& p, const Segment& s) {
+  p.item_part[2 * blockIdx.x] = make_int4(s.tok0, s.n_rows, s.hkv, s.parts);
+  p.item_part[2 * blockIdx.x + 1] = make_int4(s.slot, 0, 0, 0);
+}
+__device__ __forceinline__ void publish_no_cut(const RowsParams& p) {
+  p.item_part[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
 }
 
 // Cache row (page * H_kv + head) * page_size + slot of key `pos`, -1 where its
@@ -129,20 +260,12 @@ __device__ __forceinline__ int key_row(const RowsParams& p, const int32_t* table
   return ((page * p.Hkv + hkv) << p.log2_page) | (pos & ((1 << p.log2_page) - 1));
 }
 
-// Rows a CTA's tile holds, per dtype.
-constexpr int kRowsF32 = 64;
-constexpr int kRowsBf16 = 256;
-
-cudaError_t launch_rows_f32(int head_dim, const RowsParams& p, cudaStream_t s);
-cudaError_t launch_rows_bf16(int head_dim, const RowsParams& p, cudaStream_t s);
-cudaError_t launch_rows_merge(int head_dim, bool bf16, const RowsParams& p, cudaStream_t s);
+// One CTA an SM.
+cudaError_t launch_rows_f32(int head_dim, int ctas, const RowsParams& p, cudaStream_t s);
+cudaError_t launch_rows_bf16(int head_dim, int ctas, const RowsParams& p, cudaStream_t s);
+cudaError_t launch_rows_merge(int head_dim, bool bf16, int ctas, const RowsParams& p, cudaStream_t s);
 cudaError_t prepare_rows_f32();
 cudaError_t prepare_rows_bf16();
-
-// Row tiles a launch must cover, whatever the groups' sizes.
-inline long max_row_tiles(const RowsParams& p, int bm) {
-  return p.rows * p.g / bm + std::min<long>(p.n_groups, p.rows);
-}
 
 inline cudaError_t launch_pdl(const void* kernel, dim3 grid, int threads, int smem, cudaStream_t s,
                               void** args) {

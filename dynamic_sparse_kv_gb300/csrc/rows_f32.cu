@@ -38,36 +38,39 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
 template <int D>
 __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsParams p) {
   extern __shared__ __align__(16) float sm[];
+  __shared__ PlanSmem plan;
   using S = SmemF32<D>;
   constexpr int LD = S::LD, DT = D / 64;   // float4 columns of the output a thread holds
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const int split = blockIdx.z, hkv = blockIdx.y;
   float* qs = sm + S::kQ;
   float* ks = sm + S::kK;
   float* vs = sm + S::kV;
   float* ps = sm + S::kP;
   int* live = reinterpret_cast<int*>(sm + S::kLive);
   int bad = 0;
-  const RowGroup grp = find_tile<BM>(p, blockIdx.x, bad);
+  Walk walk;
+  const bool work = plan_walk<BM, kThreads>(p, plan, walk, bad);
   // the kernel before may still write q and, where there is no prefix contract,
   // the keys; the next one reads this one's output after its own wait
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-  if (grp.tile < 0) {
-    if (bad) atomicOr(p.status, bad);
-    return;
+  bool cut = false;
+  Segment seg;
+  while (work && next_segment<BM>(p, walk, seg)) {
+  if (seg.starts && seg.hkv == 0 && seg.tok0 == seg.grp.first) check_group(p, seg.grp, tid, kThreads, bad);
+  publish_parts(p, seg, tid, kThreads);
+  if (p.item_part && seg.starts && !seg.whole) {
+    cut = true;
+    if (tid == 0) publish_cut(p, seg);
   }
-  if (split == 0 && hkv == 0 && grp.tile == 0) check_group(p, grp, bad);
-  int lo, hi;
-  split_range(grp.len, p.splits, split, lo, hi);
-  const int row0 = grp.tile * BM;
-  const int n_rows = min(BM, grp.n_rows - row0);
-  const int32_t* table = p.block_table + (size_t)grp.table_row * p.max_pages;
+  const int lo = seg.k0 * kKeyTile, hi = min(seg.grp.len, seg.k1 * kKeyTile), hkv = seg.hkv;
+  const int n_rows = seg.n_rows;
+  const int32_t* table = p.block_table + (size_t)seg.grp.table_row * p.max_pages;
   // q and out index (in heads) of row r
   auto head_of = [&](int r) -> size_t {
-    const int x = row0 + r;
-    return (size_t)(grp.first + x / p.g) * p.Hq + hkv * p.g + x % p.g;
+    return (size_t)(seg.tok0 + r / p.g) * p.Hq + hkv * p.g + r % p.g;
   };
+  __syncthreads();   // the segment before is read to the end
   for (int e = tid; e < BM * (D / 4); e += kThreads) {
     const int r = e / (D / 4), c = e % (D / 4);
     const float4 v = r < n_rows ? load4(static_cast<const float*>(p.q) + head_of(r) * D + 4 * c)
@@ -176,45 +179,51 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsParams p) {
     const int r = 4 * ty + i;
     if (r >= n_rows) continue;
     const size_t head = head_of(r);
-    if (p.out && p.splits == 1) {
+    if (p.out && seg.whole) {
       const float inv = l[i] > 0.f ? __frcp_rn(l[i]) : (l[i] == 0.f ? 0.f : l[i]);
 #pragma unroll
       for (int t = 0; t < DT; ++t)
         store4(static_cast<float*>(p.out) + head * D + 64 * t + 4 * tx,
                make_float4(o[i][t].x * inv, o[i][t].y * inv, o[i][t].z * inv, o[i][t].w * inv));
     } else {
-      const size_t at = (size_t)split * p.rows * p.Hq + head;
-      if (tx == 0) *reinterpret_cast<float2*>(p.ml + 2 * at) = make_float2(m[i], l[i]);
+      const size_t at = seg.whole ? head : (size_t)(2 * blockIdx.x + seg.slot) * p.slot_rows + r;
+      float* ml = seg.whole ? p.row_ml : p.slot_ml;
+      float* acc = seg.whole ? p.row_acc : p.slot_acc;
+      if (tx == 0) *reinterpret_cast<float2*>(ml + 2 * at) = make_float2(m[i], l[i]);
       if (lo < hi) {
 #pragma unroll
-        for (int t = 0; t < DT; ++t) *reinterpret_cast<float4*>(p.acc + at * D + 64 * t + 4 * tx) = o[i][t];
+        for (int t = 0; t < DT; ++t) *reinterpret_cast<float4*>(acc + at * D + 64 * t + 4 * tx) = o[i][t];
       }
     }
   }
+  }
+  if (p.item_part && !cut && tid == 0) publish_no_cut(p);
   if (bad) atomicOr(p.status, bad);
 }
 
-// Joins the parts of every row of a token that belongs to a group: one warp a
-// row, D / 32 dims a lane.
+// Joins the parts of the cut items of a cross attention: block (c, y) has rows
+// 8y.. of the item that starts in CTA c of the row kernel, a warp each row.
 constexpr int kMergeWarps = 8;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const RowsParams p) {
-  const int lane = threadIdx.x & 31;
-  const size_t head = (size_t)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
-  const size_t n = (size_t)p.rows * p.Hq;
+  const int lane = threadIdx.x & 31, r = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-  if (head >= n) return;
-  const long token = head / p.Hq;
-  if (token < __ldcg(p.start) || token >= __ldcg(p.start + p.n_groups)) return;
+  const int4 item = __ldcg(p.item_part + 2 * blockIdx.x);
+  const int slot = __ldcg(p.item_part + 2 * blockIdx.x + 1).x;
+  if (r >= item.y) return;
+  const int n_parts = item.w;   // <= kMaxExt; 0 without a cut item, which has no rows either
+  auto row_at = [&](int s) -> size_t {   // of part s in the slots
+    return (size_t)(2 * (blockIdx.x + s) + (s == 0 ? slot : 0)) * p.slot_rows + r;
+  };
   float ms[2], ls[2];   // parts lane and lane + 32
   float M = -CUDART_INF_F;
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int s = lane + 32 * u;
-    const float2 x = s < p.splits ? __ldcg(reinterpret_cast<const float2*>(p.ml) + s * n + head)
-                                  : make_float2(-CUDART_INF_F, 0.f);
+    const float2 x = s < n_parts ? __ldcg(reinterpret_cast<const float2*>(p.slot_ml) + row_at(s))
+                                 : make_float2(-CUDART_INF_F, 0.f);
     ms[u] = x.x;
     ls[u] = x.y;
     M = fmaxf(M, x.x);
@@ -234,10 +243,10 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const RowsParam
 #pragma unroll
   for (int e = 0; e < D / 32; ++e) a[e] = 0.f;
 #pragma unroll 4
-  for (int s = 0; s < p.splits; ++s) {
+  for (int s = 0; s < n_parts; ++s) {
     const float w = __shfl_sync(0xffffffffu, s < 32 ? sc[0] : sc[1], s & 31);
     if (__shfl_sync(0xffffffffu, s < 32 ? ls[0] : ls[1], s & 31) == 0.f) continue;   // no rows there
-    const float* src = p.acc + (s * n + head) * D + lane * (D / 32);
+    const float* src = p.slot_acc + row_at(s) * D + lane * (D / 32);
     if constexpr (D == 128) {
       const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
       a[0] = fmaf(v.x, w, a[0]);
@@ -251,6 +260,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const RowsParam
     }
   }
   const float inv = L > 0.f ? __frcp_rn(L) : (L == 0.f ? 0.f : L);
+  const size_t head = (size_t)(item.x + r / p.g) * p.Hq + item.z * p.g + r % p.g;
   T* dst = static_cast<T*>(p.out) + head * D + lane * (D / 32);
   if constexpr (D == 128) {
     store4(dst, make_float4(a[0] * inv, a[1] * inv, a[2] * inv, a[3] * inv));
@@ -262,21 +272,19 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const RowsParam
 }
 
 template <int D>
-cudaError_t launch_rows_t(const RowsParams& p, cudaStream_t s) {
+cudaError_t launch_rows_t(int ctas, const RowsParams& p, cudaStream_t s) {
   RowsParams a = p;
   void* args[] = {&a};
-  return launch_pdl(reinterpret_cast<const void*>(rows_kernel<D>),
-                    dim3((unsigned)max_row_tiles(p, BM), p.Hkv, p.splits), kThreads,
+  return launch_pdl(reinterpret_cast<const void*>(rows_kernel<D>), dim3(ctas), kThreads,
                     SmemF32<D>::kBytes, s, args);
 }
 
 template <typename T, int D>
-cudaError_t launch_merge_t(const RowsParams& p, cudaStream_t s) {
+cudaError_t launch_merge_t(int ctas, const RowsParams& p, cudaStream_t s) {
   RowsParams a = p;
   void* args[] = {&a};
-  const long blocks = (p.rows * p.Hq + kMergeWarps - 1) / kMergeWarps;
-  return launch_pdl(reinterpret_cast<const void*>(merge_kernel<T, D>), dim3((unsigned)blocks),
-                    32 * kMergeWarps, 0, s, args);
+  return launch_pdl(reinterpret_cast<const void*>(merge_kernel<T, D>),
+                    dim3(ctas, (p.slot_rows + kMergeWarps - 1) / kMergeWarps), 32 * kMergeWarps, 0, s, args);
 }
 
 template <int D>
@@ -287,15 +295,15 @@ cudaError_t prepare_t() {
 
 }  // namespace
 
-cudaError_t launch_rows_f32(int head_dim, const RowsParams& p, cudaStream_t s) {
-  return head_dim == 64 ? launch_rows_t<64>(p, s) : launch_rows_t<128>(p, s);
+cudaError_t launch_rows_f32(int head_dim, int ctas, const RowsParams& p, cudaStream_t s) {
+  return head_dim == 64 ? launch_rows_t<64>(ctas, p, s) : launch_rows_t<128>(ctas, p, s);
 }
 
-cudaError_t launch_rows_merge(int head_dim, bool bf16, const RowsParams& p, cudaStream_t s) {
+cudaError_t launch_rows_merge(int head_dim, bool bf16, int ctas, const RowsParams& p, cudaStream_t s) {
   if (bf16)
-    return head_dim == 64 ? launch_merge_t<__nv_bfloat16, 64>(p, s)
-                          : launch_merge_t<__nv_bfloat16, 128>(p, s);
-  return head_dim == 64 ? launch_merge_t<float, 64>(p, s) : launch_merge_t<float, 128>(p, s);
+    return head_dim == 64 ? launch_merge_t<__nv_bfloat16, 64>(ctas, p, s)
+                          : launch_merge_t<__nv_bfloat16, 128>(ctas, p, s);
+  return head_dim == 64 ? launch_merge_t<float, 64>(ctas, p, s) : launch_merge_t<float, 128>(ctas, p, s);
 }
 
 cudaError_t prepare_rows_f32() {

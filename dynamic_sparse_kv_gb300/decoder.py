@@ -196,7 +196,7 @@ class DecodeAttention:
         if max_prefix is None:
             max_prefix = prefix_len if isinstance(prefix_len, int) else int(prefix.max())
         start = start.to(self.k_cache.device).contiguous()
-        ws_bytes = N.fastocr_rows_workspace(self.handle, self.batch)
+        ws_bytes = N.fastocr_rows_workspace(self.handle, 0)
         ws = (self.groups["ws"] if self.groups else
               torch.empty(ws_bytes, dtype=torch.uint8, device=self.k_cache.device))
         self.groups = {"start": start, "prefix_len": prefix, "ws": ws,

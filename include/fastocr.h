@@ -282,10 +282,9 @@ fastocr_status fastocr_rswa_attend(fastocr_handle* h, const void* q, const fasto
                                    int32_t prefix_len, int32_t window, void* out,
                                    fastocr_stream stream);
 
-/* Bytes of workspace with which fastocr_shared_attend (rows = B) or
- * fastocr_cross_attend over `rows` query tokens can split its keys over the
- * whole device; about 20 MB or the size of one fp32 output, whichever is more.
- * Negative (a fastocr_status): NULL, INVALID. */
+/* Bytes of workspace that fastocr_cross_attend over up to `rows` query tokens
+ * needs (bf16, d = 128: at most about 40 MB, however many rows), or, with rows =
+ * 0, fastocr_shared_attend. Negative (a fastocr_status): NULL, INVALID. */
 int64_t fastocr_rows_workspace(const fastocr_handle* h, int64_t rows);
 
 /* Decode attention of a batch whose sequences share long prefixes: several
@@ -301,8 +300,7 @@ int64_t fastocr_rows_workspace(const fastocr_handle* h, int64_t rows);
  * then unspecified.
  * weights: NULL, or accumulates weights like fastocr_weigh_attend (needs
  * protect[b] >= prefix_len[b]).
- * ws: device, 16-byte aligned, caller-owned, of at least one part's partials,
- * B * H_q * (d + 2) * 4 bytes; fastocr_rows_workspace(h, B) for full speed.
+ * ws: device, 16-byte aligned, caller-owned, fastocr_rows_workspace(h, 0) bytes.
  * Its contents are meaningless between calls; calls that may run at once
  * need one each.
  * Overlap: as the other calls; start, prefix_len and the prefix's K/V rows are
@@ -354,10 +352,9 @@ fastocr_status fastocr_evict(fastocr_handle* h, const fastocr_kv* kv, const fast
  * ascending from 0; sequences without queries are fine, and rows at and behind
  * q_start[B] are left as they are. Offsets out of order or past `rows` are
  * reported as FASTOCR_DEV_BAD_GROUP and clamped. rows * H_q < 2^31.
- * ws: as fastocr_shared_attend, for `rows` tokens, or NULL: then the keys are
- * not split. Overlap: only q_start, seq_len and the block table are read
- * before the preceding kernel completes. One kernel, or two where the keys are
- * split.
+ * ws: as fastocr_shared_attend, fastocr_rows_workspace(h, rows) bytes. Overlap:
+ * only q_start, seq_len and the block table are read before the preceding
+ * kernel completes. Two kernels.
  * Errors: NULL, INVALID (rows, ws_bytes, another device current),
  * UNSUPPORTED, ALIGN, CUDA. */
 fastocr_status fastocr_cross_attend(fastocr_handle* h, const void* q, const fastocr_kv* kv,
