@@ -50,11 +50,10 @@ RowsParams rows_params(const fastocr_handle* h, const void* q, const fastocr_kv*
   p.g = d.num_q_heads / d.num_kv_heads;
   p.scale_log2 = (float)(1.4426950408889634 / sqrt((double)d.head_dim));
   p.status = h->status;
-  p.min_units = 1;
   return p;
 }
 
-// Rows of a row tile and of a slot of the workspace, for `rows` query tokens.
+// Most rows of a row tile, in whole tokens.
 int tile_rows(const fastocr_handle* h) {
   const int bm = h->dims.dtype == FASTOCR_DTYPE_BF16 ? kRowsBf16 : kRowsF32;
   const int g = h->dims.num_q_heads / h->dims.num_kv_heads;
@@ -62,6 +61,31 @@ int tile_rows(const fastocr_handle* h) {
 }
 int64_t slot_rows(const fastocr_handle* h, int64_t rows) {
   return std::min<int64_t>(tile_rows(h), rows * (h->dims.num_q_heads / h->dims.num_kv_heads));
+}
+
+// Tokens of a row tile. A bf16 tile of 256 rows reads each key once for all of
+// them, one of 128 twice, but its parts are half as large: where the keys of
+// few tiles are spread over all SMs, writing and joining the parts
+// takes longer than reading the keys (kFewUnits key tiles an SM or fewer).
+int choose_tile_tokens(const fastocr_handle* h, int64_t rows, int64_t groups, long keys) {
+  const int g = h->dims.num_q_heads / h->dims.num_kv_heads;
+  if (h->dims.dtype != FASTOCR_DTYPE_BF16) return kRowsF32 / g;
+  constexpr int kFewUnits = 4;
+  const int64_t tiles = std::max(groups, (rows * g + kRowsBf16 - 1) / kRowsBf16);
+  const int64_t units = tiles * h->dims.num_kv_heads * ((keys + kKeyTile - 1) / kKeyTile);
+  return (units <= (int64_t)kFewUnits * h->num_sms ? kRowsBf16 / 2 : kRowsBf16) / g;
+}
+
+// Key tiles of a share, where few items are shared by all CTAs: a part of an item
+// costs its rows' partials written and read (about 1 KB a row), a key tile of a
+// share costs every CTA 1 to 2 us. The sum is least near sqrt(key tiles * rows /
+// 1600): measured at 2, 6, 3 and 8 for 33 tiles and 224 rows (17.5 us), 65 and
+// 896 (23.5 us), 16 and 896 (17.7 us), 65 and 1792 (30.3 us); within 1 us of
+// the best share on nine shapes. fp32 tiles cost far more than their parts.
+int choose_share(const fastocr_handle* h, int64_t rows, long keys) {
+  if (h->dims.dtype != FASTOCR_DTYPE_BF16) return 1;
+  const double tiles = (double)((keys + kKeyTile - 1) / kKeyTile);
+  return (int)std::max(2.0, sqrt(tiles * (double)rows * h->dims.num_q_heads / 1600.0) + 0.5);
 }
 
 // Lays the workspace out for `rows` query tokens from `base` on and returns its
@@ -91,7 +115,7 @@ int64_t place_workspace(const fastocr_handle* h, int64_t rows, bool shared, char
 // The kernels count units of work in 32 bits.
 bool units_fit(const fastocr_handle* h, int64_t rows, int64_t groups) {
   const int64_t g = h->dims.num_q_heads / h->dims.num_kv_heads;
-  const int64_t tiles = rows * g / tile_rows(h) + std::min(rows, groups);
+  const int64_t tiles = 2 * rows * g / tile_rows(h) + std::min(rows, groups);
   return (double)tiles * h->dims.num_kv_heads * (max_tokens(h) / kKeyTile + 1) < 2147483647.0;
 }
 
@@ -132,6 +156,9 @@ fastocr_status fastocr_shared_attend(fastocr_handle* h, const void* q, const fas
   r.start = groups->start;
   r.prefix_len = groups->prefix_len;
   r.rows = (int)B;
+  const long keys = groups->max_prefix > 0 ? groups->max_prefix : expected_tokens(h);
+  r.tile_tokens = choose_tile_tokens(h, B, groups->n, keys);
+  r.min_share = choose_share(h, B, keys);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if ((st = launch_rows(h, r, s)) != FASTOCR_OK) return st;
 
@@ -226,12 +253,24 @@ fastocr_status fastocr_cross_attend(fastocr_handle* h, const void* q, const fast
   p.n_groups = h->dims.batch;
   p.start = q_start;
   p.rows = (int)rows;
+  p.tile_tokens = choose_tile_tokens(h, rows, std::min<int64_t>(p.n_groups, rows), expected_tokens(h));
+  p.min_share = choose_share(h, rows, expected_tokens(h));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // A decode step has one query token a sequence: those go to the split-K attend
+  // kernel, whose small tiles keep more of the states in flight (16 sequences, 10
+  // heads, 2624 states: 31 us against 46 us). Where there can be
+  // such sequences and others, both kernels run and each leaves the other's alone;
+  // the row kernel finds out while the kernel before it ends.
+  const bool single = rows <= p.n_groups;
+  p.skip_tokens = single ? 1 : 0;
   if ((st = launch_rows(h, p, s)) != FASTOCR_OK) return st;
-  return launch_rows_merge(h->dims.head_dim, h->dims.dtype == FASTOCR_DTYPE_BF16, h->num_sms, p, s) ==
-                 cudaSuccess
-             ? FASTOCR_OK
-             : FASTOCR_ERR_CUDA;
+  if (launch_rows_merge(h->dims.head_dim, h->dims.dtype == FASTOCR_DTYPE_BF16, h->num_sms, p, s) != cudaSuccess)
+    return FASTOCR_ERR_CUDA;
+  if (!single) return FASTOCR_OK;
+  Params a = base_params(h, q, kv, out);
+  a.q_start = q_start;
+  a.q_rows = (int)rows;
+  return launch(h, kCross, expected_tokens(h), a, stream);
 }
 
 }  // extern "C"

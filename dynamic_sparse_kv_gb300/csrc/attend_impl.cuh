@@ -293,7 +293,7 @@ __device__ __forceinline__ CtaList make_cta_list(const Params& p, int b, int spl
   const int cur = n_t - 1;
   int a1 = 0, len1 = 0, a2 = 0, len2 = 0, in_set = 0;
   if (n_t >= 1) {
-    if (MODE == kFull || MODE == kFocal || MODE == kProfile) {
+    if (MODE == kFull || MODE == kFocal || MODE == kProfile || MODE == kCross) {
       len1 = n_t - 1;
       in_set = 1;
     } else if (MODE == kTail || MODE == kWeigh) {
@@ -395,6 +395,17 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
   unsigned char* pipe = smem + warp * ST * SM::kStageBytes;
   int* srow = reinterpret_cast<int*>(smem + SM::kRowOffset);
   int* spos = reinterpret_cast<int*>(smem + SM::kPosOffset);
+
+  // row of q and out: the sequence, or its token of a packed q
+  int q_row = b;
+  if constexpr (MODE == kCross) {
+    const int s = __ldcg(p.q_start + b), e = __ldcg(p.q_start + b + 1);
+    if (e - s != 1 || s < 0 || e > p.q_rows) {   // none, or the row kernel's: the whole cluster's answer
+      asm volatile("griddepcontrol.wait;\n" ::: "memory");   // this grid may not end before the one before it
+      return;
+    }
+    q_row = s;
+  }
 
   // announce this CTA to its cluster (the partial exchange waits for it);
   // a single split has no partner and skips every cluster barrier
@@ -639,7 +650,7 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
   // kernel, so they are read only after the wait; pulling their lines into L2
   // now is safe (L2 is where those writes land) and shortens that read.
   if (tid == 0)
-    prefetch_l2(static_cast<const T*>(p.q) + ((size_t)b * p.Hq + (size_t)hkv * p.g) * D,
+    prefetch_l2(static_cast<const T*>(p.q) + ((size_t)q_row * p.Hq + (size_t)hkv * p.g) * D,
                 p.g * D * (uint32_t)sizeof(T));
   __syncthreads();
 #pragma unroll 1
@@ -675,7 +686,7 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
   const int gid = lane >> 2, tig = lane & 3;
   if constexpr (kMma) {
     const bool have = gid < p.g;
-    const T* qrow = static_cast<const T*>(p.q) + ((size_t)b * p.Hq + hkv * p.g + (have ? gid : 0)) * D;
+    const T* qrow = static_cast<const T*>(p.q) + ((size_t)q_row * p.Hq + hkv * p.g + (have ? gid : 0)) * D;
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
       sm_.qf[ks][0] = have ? __ldcg(reinterpret_cast<const unsigned int*>(qrow + 16 * ks + 2 * tig)) : 0u;
@@ -762,7 +773,7 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
     float* qs = reinterpret_cast<float*>(smem + SM::kQOffset);
     for (int e = tid; e < kSlots * D; e += kThreads) {
       const int h = e / D, d = e % D;
-      qs[e] = h < p.g ? __ldcg(static_cast<const float*>(p.q) + ((size_t)b * p.Hq + hkv * p.g + h) * D + d) : 0.f;
+      qs[e] = h < p.g ? __ldcg(static_cast<const float*>(p.q) + ((size_t)q_row * p.Hq + hkv * p.g + h) * D + d) : 0.f;
     }
 #pragma unroll
     for (int h = 0; h < kSlots; ++h) {
@@ -1188,7 +1199,7 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
     for (int w = 0; w < kWarps; ++w) sc[w] = fast_exp2(wm[w * kSlots + h] - base);
     return M;
   };
-  T* outp = static_cast<T*>(p.out) + ((size_t)b * p.Hq + (size_t)hkv * p.g) * D;
+  T* outp = static_cast<T*>(p.out) + ((size_t)q_row * p.Hq + (size_t)hkv * p.g) * D;
   auto store_pair = [&](int e, float4 acc) {   // output dims 4*(e % C4).. of head e / C4
     T* o = outp + (e / C4) * D + 4 * (e % C4);
     if constexpr (kMma) {
@@ -1489,6 +1500,7 @@ cudaError_t prepare_modes() {
   if ((e = prepare_attend(attend_kernel<T, D, kProfile, V>, bytes))) return e;
   if ((e = prepare_attend(attend_kernel<T, D, kTail, V>, bytes))) return e;
   if ((e = prepare_attend(attend_kernel<T, D, kWeigh, V>, bytes))) return e;
+  if ((e = prepare_attend(attend_kernel<T, D, kCross, V>, bytes))) return e;
   return prepare_attend(attend_kernel<T, D, kRswa, V>, bytes);
 }
 
@@ -1577,6 +1589,7 @@ cudaError_t dispatch_variant(int mode, const Params& p, cudaStream_t s) {
     case kProfile: return launch_attend<T, D, kProfile, V>(p, s);
     case kTail: return launch_attend<T, D, kTail, V>(p, s);
     case kWeigh: return launch_attend<T, D, kWeigh, V>(p, s);
+    case kCross: return launch_attend<T, D, kCross, V>(p, s);
   }
   return cudaErrorInvalidValue;
 }

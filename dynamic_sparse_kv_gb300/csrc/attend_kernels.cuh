@@ -58,8 +58,9 @@ constexpr int kMaxImg = 16384; // image tokens whose scores fit in shared memory
 // kProfile: full attention that also adds the layer's image-attention mass
 // to the profiler (a warm-up step whose selections are not kept): no logits,
 // no scores, no selection kernel.
-// kTail, kWeigh: the rows from `first` on (see Params).
-enum Mode : int { kFull = 0, kFocal = 1, kSparse = 2, kRswa = 3, kProfile = 4, kTail = 5, kWeigh = 6 };
+// kTail, kWeigh: the rows from `first` on (see Params). kCross: all rows, of which
+// there may be none, for sequences with one query token in a packed q.
+enum Mode : int { kFull = 0, kFocal = 1, kSparse = 2, kRswa = 3, kProfile = 4, kTail = 5, kWeigh = 6, kCross = 7 };
 // Modes whose epilogue turns stored logits into head-summed probabilities.
 __host__ __device__ constexpr bool stores_logits(int mode) { return mode == kFocal || mode == kWeigh; }
 constexpr int kMaxExt = 64;   // partials of another kernel that a tail merges
@@ -123,6 +124,9 @@ struct Params {
   const float* ext_row_acc;  // [B, H_q, d]
   const float* ext_row_ml;   // [B, H_q, 2]
   int ext_slot_rows, ext_ctas;
+  // cross: sequence b's query tokens are q_start[b] .. q_start[b+1]-1 of q_rows
+  const int32_t* q_start;    // [B + 1]
+  int q_rows;
   // weigh: rows [protect[b], N_t) have weights, row r at index r - protect[b]
   float* mass;               // [B, H_kv, w_stride]
   int32_t* row_pos;          // [B, H_kv, w_stride]
@@ -267,7 +271,7 @@ __device__ __forceinline__ AttendList make_list(const Params& p, int b, int& bad
   AttendList L;
   const int cap = p.max_pages << p.log2_page;
   int n_t = __ldcg(p.seq_len + b);
-  if (n_t < 1 || n_t > cap) {
+  if (n_t < (MODE == kCross ? 0 : 1) || n_t > cap) {
     bad |= kDevBadSeqLen;
     n_t = n_t < 0 ? 0 : (n_t > cap ? cap : n_t);
   }

@@ -5,9 +5,12 @@
 //
 // The work is a list of items -- (row tile, KV head) of every group, a row tile
 // holding as many whole tokens (g rows each) as fit BM rows -- and an item's
-// keys are a run of units. The units of all items, in order, are dealt out in
-// equal runs to one CTA per SM, whatever the groups' sizes: a CTA walks over
-// segments of items, of which only the first and the last can be cut. A cut
+// keys are a run of units. With many items a unit is a key tile, and the units of
+// all items, in order, are dealt out in equal runs to one CTA per SM, whatever the
+// groups' sizes: a CTA walks over segments of items, of which only the first and
+// the last can be cut. With few items every CTA takes one unit, an equal share
+// of one item: a second segment would cost it another start and
+// output (5 us; 32 sequences on 8320 keys: 30 us dealt out, 24 us shared). A cut
 // segment leaves (max, sum, unnormalised output) of its rows, in base 2, in one
 // of the CTA's two slots of the workspace; who reads them (the tail's attend
 // kernel, or merge_kernel) joins an item's parts in the order of their keys.
@@ -24,7 +27,7 @@ namespace fastocr {
 
 constexpr int kKeyTile = 128;
 constexpr int kRowsF32 = 64;     // BM per dtype
-constexpr int kRowsBf16 = 256;
+constexpr int kRowsBf16 = 256;   // or half of it, see tile_tokens
 
 struct RowsParams {
   const void* q;              // [rows, H_q, d]
@@ -39,7 +42,9 @@ struct RowsParams {
   const int32_t* start;       // [n_groups + 1]
   const int32_t* prefix_len;  // shared prefix: [B]; NULL: group i reads all of sequence i
   int rows;                   // query tokens
-  int min_units;              // least units a CTA takes
+  int tile_tokens;            // tokens of a row tile
+  int min_share;              // least key tiles of a share, where CTAs take shares
+  int skip_tokens;            // groups of this many tokens are another kernel's (0: none)
   // workspace
   int slot_rows;              // rows a slot holds
   float* slot_acc;            // [CTAs, 2, slot_rows, d]
@@ -74,10 +79,10 @@ __device__ __forceinline__ RowGroup load_group(const RowsParams& p, int i, int& 
   s = min(max(s, 0), p.rows);
   e = min(max(e, s), p.rows);
   r.first = s;
-  r.n_tok = e - s;
+  r.n_tok = e - s == p.skip_tokens ? 0 : e - s;
   r.table_row = p.prefix_len ? s : i;
   r.len = 0;
-  if (e > s) {
+  if (r.n_tok > 0) {
     const int cap = p.max_pages << p.log2_page;
     int len = __ldcg((p.prefix_len ? p.prefix_len : p.seq_len) + r.table_row);
     int most = cap;
@@ -99,9 +104,14 @@ __device__ __forceinline__ void check_group(const RowsParams& p, const RowGroup&
     if (__ldcg(p.prefix_len + r.first + i) != r.len) bad |= kDevBadGroup;
 }
 
-// Units of an item: its key tiles. An item without keys still has one unit,
-// which writes its empty result.
-__device__ __forceinline__ int units_of(int len) { return max(1, (len + kKeyTile - 1) / kKeyTile); }
+__device__ __forceinline__ int key_tiles(int len) { return (len + kKeyTile - 1) / kKeyTile; }
+
+// Units of an item: its key tiles, or shares of about `share` of them (share > 0).
+// An item without keys still has one unit, which writes its empty result.
+__device__ __forceinline__ int units_of(int len, int share) {
+  const int k = key_tiles(len);
+  return max(1, share > 0 ? (k + share - 1) / share : k);
+}
 
 // A run of key tiles of one item.
 struct Segment {
@@ -121,6 +131,7 @@ struct Walk {
   int unit, end;     // the CTA's units [unit, end)
   int begin, per;    // its first unit; units a CTA takes
   int group, off;    // group and unit within it
+  int share;         // see units_of
   RowGroup grp;
 };
 
@@ -128,53 +139,85 @@ struct Walk {
 __device__ __forceinline__ int token_of_row(int r, int g_inv) { return (r * g_inv) >> 16; }
 __device__ __forceinline__ int inverse_of(int g) { return (65535 + g) / g; }
 
-// Units of a whole group.
-template <int BM>
-__device__ __forceinline__ int group_units(const RowsParams& p, const RowGroup& r) {
-  const int tpt = BM / p.g;
-  return (r.n_tok + tpt - 1) / tpt * p.Hkv * units_of(r.len);
+// Items and units of a whole group.
+__device__ __forceinline__ int group_items(const RowsParams& p, const RowGroup& r) {
+  return (r.n_tok + p.tile_tokens - 1) / p.tile_tokens * p.Hkv;
+}
+__device__ __forceinline__ int group_units(const RowsParams& p, const RowGroup& r, int share) {
+  return group_items(p, r) * units_of(r.len, share);
 }
 
 struct PlanSmem {
-  int warp_sum[32], warp_max[32];
+  int warp_sum[2][32], warp_items[32], warp_max[32];
   int group, off;
   RowGroup grp;
 };
 
 // Where this CTA's units are; called by all THREADS threads. False: it has none.
-template <int BM, int THREADS>
+template <int THREADS>
 __device__ __forceinline__ bool plan_walk(const RowsParams& p, PlanSmem& s, Walk& w, int& bad) {
   constexpr int NW = THREADS / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int chunk = (p.n_groups + THREADS - 1) / THREADS;   // consecutive groups a thread sums
   const int i0 = min(p.n_groups, tid * chunk), i1 = min(p.n_groups, i0 + chunk);
-  int sum = 0, most = 0;
+  int sum = 0, items = 0, most = 0;
   RowGroup grp = {0, 0, 0, 0};
   for (int i = i0; i < i1; ++i) {
     grp = load_group(p, i, bad);
-    sum += group_units<BM>(p, grp);
-    most = max(most, grp.n_tok > 0 ? units_of(grp.len) : 0);
+    sum += group_units(p, grp, 0);
+    items += group_items(p, grp);
+    most = max(most, grp.n_tok > 0 ? key_tiles(grp.len) : 0);
   }
-  int incl = sum;
+  // units before this warp, and of all
+  int mine, all;
+  auto scan = [&](int x, int* warp_sum) {
+    int incl = x;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
-  }
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    int before = 0;
+    all = 0;
+#pragma unroll
+    for (int v = 0; v < NW; ++v) {
+      const int c = warp_sum[v];
+      if (v < warp) before += c;
+      all += c;
+    }
+    mine = before + incl - x;
+  };
+  items = __reduce_add_sync(0xffffffffu, items);
   most = __reduce_max_sync(0xffffffffu, most);
-  if (lane == 31) s.warp_sum[warp] = incl;
-  if (lane == 0) s.warp_max[warp] = most;
-  __syncthreads();
-  int before = 0, all = 0;
+  if (lane == 0) {
+    s.warp_items[warp] = items;
+    s.warp_max[warp] = most;
+  }
+  scan(sum, s.warp_sum[0]);
+  items = 0;
 #pragma unroll
   for (int v = 0; v < NW; ++v) {
-    if (v < warp) before += s.warp_sum[v];
-    all += s.warp_sum[v];
+    items += s.warp_items[v];
     most = max(most, s.warp_max[v]);
   }
-  const int mine = before + incl - sum, C = gridDim.x;
   // an item's parts fit the merging kernels' lists
-  w.per = max((all + C - 1) / C, max(p.min_units, (most + kMaxExt - 3) / (kMaxExt - 2)));
+  const int C = gridDim.x, least = max(1, (most + kMaxExt - 3) / (kMaxExt - 2));
+  w.share = 0;
+  if (2 * items <= C) {   // the shares are at most all / share + items <= C
+    w.share = max(max(p.min_share, least), (all + C - items - 1) / (C - items));
+    w.per = 1;
+    sum = 0;
+    for (int i = i0; i < i1; ++i) {
+      int none = 0;
+      if (chunk > 1) grp = load_group(p, i, none);
+      sum += group_units(p, grp, w.share);
+    }
+    scan(sum, s.warp_sum[1]);
+  } else {
+    w.per = max(least, (all + C - 1) / C);
+  }
   const long long first = (long long)blockIdx.x * w.per;
   if (first >= all) return false;
   w.begin = w.unit = (int)first;
@@ -185,7 +228,7 @@ __device__ __forceinline__ bool plan_walk(const RowsParams& p, PlanSmem& s, Walk
       for (;; ++i) {
         int none = 0;
         grp = load_group(p, i, none);
-        const int u = group_units<BM>(p, grp);
+        const int u = group_units(p, grp, w.share);
         if (w.unit < at + u) break;
         at += u;
       }
@@ -202,16 +245,15 @@ __device__ __forceinline__ bool plan_walk(const RowsParams& p, PlanSmem& s, Walk
 }
 
 // The next segment; false at the end. Warp-uniform.
-template <int BM>
 __device__ __forceinline__ bool next_segment(const RowsParams& p, Walk& w, Segment& s) {
   if (w.unit >= w.end) return false;
-  const int tpt = BM / p.g;
-  while (w.off >= group_units<BM>(p, w.grp)) {   // another group with rows exists: w.unit < w.end
+  const int tpt = p.tile_tokens;
+  while (w.off >= group_units(p, w.grp, w.share)) {   // another group with rows exists: w.unit < w.end
     int none = 0;                                // reported by plan_walk
     w.grp = load_group(p, ++w.group, none);
     w.off = 0;
   }
-  const int u = units_of(w.grp.len);
+  const int u = units_of(w.grp.len, w.share), n_tiles = key_tiles(w.grp.len);
   const int item = w.off / u, k = w.off - item * u;   // item in the group, unit in the item
   const int tile = item / p.Hkv;
   const int n = min(u - k, w.end - w.unit);
@@ -219,8 +261,8 @@ __device__ __forceinline__ bool next_segment(const RowsParams& p, Walk& w, Segme
   s.grp = w.grp;
   s.tok0 = w.grp.first + tile * tpt;
   s.n_rows = min(tpt, w.grp.n_tok - tile * tpt) * p.g;
-  s.k0 = k;
-  s.k1 = min((w.grp.len + kKeyTile - 1) / kKeyTile, k + n);
+  s.k0 = (int)((long long)k * n_tiles / u);
+  s.k1 = (int)((long long)(k + n) * n_tiles / u);
   s.whole = n == u;
   s.starts = k == 0;
   s.slot = w.unit == w.begin ? 0 : 1;

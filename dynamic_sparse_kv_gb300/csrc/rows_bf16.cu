@@ -200,7 +200,7 @@ __device__ __forceinline__ bool next_from(const RowsParams& p, Walk* walk, Segme
   Walk w = *walk;
   Segment s;
   __syncwarp();
-  const bool more = next_segment<kRowsBf16>(p, w, s);
+  const bool more = next_segment(p, w, s);
   if ((threadIdx.x & 31) == 0) {
     *walk = w;
     if (more) *seg = s;
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsParams p) {
   Walk* walk = reinterpret_cast<Walk*>(smem + S::kWalk) + min(warp, 12);
   {
     Walk w;
-    if (!plan_walk<kRowsBf16, kThreads>(p, *reinterpret_cast<PlanSmem*>(smem), w, bad)) {
+    if (!plan_walk<kThreads>(p, *reinterpret_cast<PlanSmem*>(smem), w, bad)) {
       asm volatile("griddepcontrol.wait;\n" ::: "memory");
       if (p.item_part && tid == 0) publish_no_cut(p);
       if (bad) atomicOr(p.status, bad);
@@ -277,6 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsParams p) {
     // ---------------- softmax of turn t
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kRegsSoftmax));
     const int t = warp >> 2, w = warp & 3;
+    bool more = next_from(p, walk, seg_p);   // there is a first segment; found while the kernel before ends
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     const uint32_t lane_base = (uint32_t)(32 * w) << 16;
@@ -286,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsParams p) {
     int k_count = 0;      // key tiles of the segments before
     int n_seg = 0;
     bool cut = false;
-    for (; next_from(p, walk, seg_p); ++n_seg) {
+    for (; more; more = next_from(p, walk, seg_p), ++n_seg) {
       const int n_tiles = seg_p->k1 - seg_p->k0;
       const bool pair = seg_p->n_rows > kTileRows;
       const int n = count_of(pair, n_tiles, t);
@@ -302,9 +303,10 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsParams p) {
       if (n_seg > 0) asm volatile("bar.sync 1, 256;\n" ::: "memory");   // the output before is staged there
       if (n_tiles > 0) {
         const int c = tid & (D / 8 - 1);
-        constexpr int kStep = 256 / (D / 8), kBatch = 8;
+        constexpr int kStep = 256 / (D / 8), kBatch = 2 * kTileRows / kStep;   // loads in flight
         const int total = pair ? 2 * kTileRows : kTileRows;
-        for (int r0 = tid / (D / 8); r0 < total; r0 += kBatch * kStep) {
+        {
+          const int r0 = tid / (D / 8);
           uint4 v[kBatch];
 #pragma unroll
           for (int u = 0; u < kBatch; ++u) {
@@ -553,7 +555,6 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsParams p) {
     // copy gets its row by a shuffle, so that the warps need not meet.
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegsLoad));
     const int w = warp - 8;
-    if (!p.prefix_len) asm volatile("griddepcontrol.wait;\n" ::: "memory");
     uint32_t* masks = reinterpret_cast<uint32_t*>(smem + S::kMask);
     constexpr int kChunks = D / 8;                    // 16-byte chunks of a row
     constexpr int kRowsAtOnce = 32 / kChunks;         // rows an instruction covers

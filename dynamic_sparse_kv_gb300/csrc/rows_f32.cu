@@ -49,14 +49,14 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsParams p) {
   int* live = reinterpret_cast<int*>(sm + S::kLive);
   int bad = 0;
   Walk walk;
-  const bool work = plan_walk<BM, kThreads>(p, plan, walk, bad);
-  // the kernel before may still write q and, where there is no prefix contract,
-  // the keys; the next one reads this one's output after its own wait
+  const bool work = plan_walk<kThreads>(p, plan, walk, bad);
+  // the kernel before may still write q or read the workspace; the next one
+  // reads this one's output after its own wait
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   bool cut = false;
   Segment seg;
-  while (work && next_segment<BM>(p, walk, seg)) {
+  while (work && next_segment(p, walk, seg)) {
   if (seg.starts && seg.hkv == 0 && seg.tok0 == seg.grp.first) check_group(p, seg.grp, tid, kThreads, bad);
   publish_parts(p, seg, tid, kThreads);
   if (p.item_part && seg.starts && !seg.whole) {

@@ -353,8 +353,8 @@ fastocr_status fastocr_evict(fastocr_handle* h, const fastocr_kv* kv, const fast
  * q_start[B] are left as they are. Offsets out of order or past `rows` are
  * reported as FASTOCR_DEV_BAD_GROUP and clamped. rows * H_q < 2^31.
  * ws: as fastocr_shared_attend, fastocr_rows_workspace(h, rows) bytes. Overlap:
- * only q_start, seq_len and the block table are read before the preceding
- * kernel completes. Two kernels.
+ * as the other calls; q_start and the states' K/V rows are read before the
+ * preceding kernel completes. Two kernels, or three where rows <= B.
  * Errors: NULL, INVALID (rows, ws_bytes, another device current),
  * UNSUPPORTED, ALIGN, CUDA. */
 fastocr_status fastocr_cross_attend(fastocr_handle* h, const void* q, const fastocr_kv* kv,

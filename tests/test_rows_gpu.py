@@ -234,6 +234,9 @@ def check_cross(c, t, n, q, out, spare=3):
     (1, [3], [129]),
     (256, [1, 130], [513, 255]),
     (8, [19], [1000]),
+    (16, [1, 1, 1, 1], [700, 0, 1, 333]),       # a decode step
+    (16, [0, 3, 0, 1, 0], [40, 50, 60, 700, 0]),  # few tokens, not one a sequence
+    (4, [1, 0, 2], [129, 5, 64]),
 ])
 @pytest.mark.parametrize("any_rows", [False, True])
 def test_cross_attention(dtype, heads, page, t, n, any_rows):
