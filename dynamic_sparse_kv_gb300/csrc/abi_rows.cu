@@ -225,10 +225,15 @@ fastocr_status fastocr_evict(fastocr_handle* h, const fastocr_kv* kv, const fast
   p.recent = recent;
   p.new_len = new_len;
   p.status = h->status;
+  // Two CTAs fit an SM. More CTAs a (sequence, KV head) shorten the selection, but
+  // each of its rounds then crosses the cluster, and a second wave of CTAs costs more
+  // than it brings. Measured, 1 / 2 / 4 / 8 CTAs: 128 units of 8192 rows 51 / 43 / 69 /
+  // 145 us, 32 units 28 / 21 / 20 / 29, 4 units 26 / 19 / 17 / 19; 128 units of
+  // 2048 rows 17 / 23 / 41 / 101.
   p.cluster = 1;
   while (p.cluster < kEvictCluster &&
          ((long)p.cluster * kEvictSlice < rows ||
-          ((long)p.cluster * p.B * p.Hkv < h->num_sms && rows / p.cluster > 1024)))
+          (2L * p.cluster * p.B * p.Hkv <= 2L * h->num_sms && rows / (2 * p.cluster) >= 2048)))
     p.cluster *= 2;
   p.slice = (rows + p.cluster - 1) / p.cluster;
   return launch_evict(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FASTOCR_OK

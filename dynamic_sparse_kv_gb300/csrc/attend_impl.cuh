@@ -1173,6 +1173,17 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
   const int sg_lo = max(c.a1 + c.txt_lo, c.img_start) - c.img_start;
   const int sg_hi = min(c.a1 + c.txt_lo + c.n_txt, img_end) - c.img_start;
   float4 sgx[kSgU][2];
+  float held[kSgU];   // weigh: what the accumulator holds of them
+  int seen = 0;
+  if constexpr (MODE == kWeigh) {
+    const float* mass = p.mass + ((size_t)b * p.Hkv + hkv) * p.w_stride;
+#pragma unroll
+    for (int u = 0; u < kSgU; ++u) {
+      const int i = sg_lo + u * kThreads + tid;
+      held[u] = i < sg_hi ? __ldcg(mass + i) : 0.f;
+    }
+    if (c.has_cur && tid == 0) seen = __ldcg(p.seen + b);
+  }
   if constexpr (stores_logits(MODE)) {
 #pragma unroll
     for (int u = 0; u < kSgU; ++u) {
@@ -1424,20 +1435,21 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
           const float4* src4 = reinterpret_cast<const float4*>(logit_base + (size_t)i * kSlots);
           sgx[u][0] = i < sg_hi ? __ldcg(src4) : make_float4(0.f, 0.f, 0.f, 0.f);
           sgx[u][1] = i < sg_hi ? __ldcg(src4 + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
+          if constexpr (MODE == kWeigh) held[u] = i < sg_hi ? __ldcg(sp + i) : 0.f;
         }
       }
 #pragma unroll
       for (int u = 0; u < kSgU; ++u) {
         const int i = i0 + u * kThreads + tid;
         const float sg = score(sgx[u][0], sgx[u][1]);
-        if (i < sg_hi) sp[i] = MODE == kWeigh ? sp[i] + sg : sg;
+        if (i < sg_hi) sp[i] = MODE == kWeigh ? held[u] + sg : sg;
       }
     }
     if (c.has_cur && tid == 0 && c.cur_pos >= c.img_start && c.cur_pos < img_end) {
       const int i = c.cur_pos - c.img_start;
       const float4* src4 = reinterpret_cast<const float4*>(logit_base + (size_t)i * kSlots);
       sp[i] = score(__ldcg(src4), __ldcg(src4 + 1));   // weigh: the row starts here
-      if constexpr (MODE == kWeigh) p.row_pos[unit * p.w_stride + i] = __ldcg(p.seen + b) - 1;
+      if constexpr (MODE == kWeigh) p.row_pos[unit * p.w_stride + i] = seen - 1;
     }
   }
 }

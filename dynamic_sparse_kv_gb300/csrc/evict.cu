@@ -8,8 +8,9 @@
 // read and written once and no kept row before `keep` moves at all.
 //
 // One cluster of CTAs has a (sequence, KV head). A CTA keeps the 32-bit sort
-// keys of its slice of rows in shared memory; an 8-bit radix select finds the
-// keep-th largest key, the CTAs joining their histograms through distributed
+// keys of its slice of rows in shared memory; a radix select by 11, 11 and 10 bits
+// finds the keep-th largest key (weights share few exponents: with 8-bit digits
+// the first pass's counts met in a handful of bins), the CTAs joining their histograms through distributed
 // shared memory; each CTA then lists its holes and survivors, and the moves
 // are dealt out evenly over the cluster by rank, whoever listed them.
 #include "evict.cuh"
@@ -22,12 +23,14 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kSub = 4;        // histogram copies, against equal digits of neighbouring warps
-constexpr int kMoveBatch = 8;  // rows a warp has in flight
+constexpr int kSub = 2;        // histogram copies, against equal digits of neighbouring warps
+constexpr int kBins = 2048;    // four a thread
+static_assert(kBins == 4 * kThreads, "a thread's bins");
+constexpr int kMoveBatch = 4;  // row copies a warp has in flight
 
 struct EvictSmem {
-  int hist[4][kSub][256];   // a pass's digits of this CTA's rows
-  int total[4][256];        // this CTA's sums, read by the cluster
+  int hist[kSub][kBins];    // a pass's digits of this CTA's rows, bins in descending order
+  int total[2][kBins];      // their sums, read by the cluster; passes take turns
   int counts[4];            // equal keys, holes, survivors of this CTA, read by the cluster
   int warp_sum[kWarps];
   int pick[4];              // digit, rows above it, rows in it
@@ -44,6 +47,14 @@ __device__ __forceinline__ int ld_peer(uint32_t a) {
   asm volatile("ld.shared::cluster.s32 %0, [%1];\n" : "=r"(v) : "r"(a) : "memory");
   return v;
 }
+__device__ __forceinline__ int4 ld_peer4(uint32_t a) {
+  int4 v;
+  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];\n"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
 __device__ __forceinline__ int ld_peer_u16(uint32_t a) {
   uint16_t v;
   asm volatile("ld.shared::cluster.u16 %0, [%1];\n" : "=h"(v) : "r"(a) : "memory");
@@ -55,6 +66,17 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   if (w != w) return 0u;
   const uint32_t u = __float_as_uint(w + 0.f);   // -0 as +0
   return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+// Counts digit d (of a warp's active lanes; -1: none). Equal digits of a whole warp,
+// e.g. of rows that have no weight yet, count as one.
+__device__ __forceinline__ void count_digit(int* hist, int d) {
+  const int first = __shfl_sync(0xffffffffu, d, 0);
+  if (__all_sync(0xffffffffu, d == first)) {
+    if ((threadIdx.x & 31) == 0 && d >= 0) atomicAdd(hist + (kBins - 1 - d), 32);
+  } else if (d >= 0) {
+    atomicAdd(hist + (kBins - 1 - d), 1);
+  }
 }
 
 // Exclusive prefix of x over the block's threads, and the block's sum.
@@ -80,7 +102,7 @@ __device__ __forceinline__ int block_scan(int x, int* warp_sum, int& sum) {
   return before + incl - x;
 }
 
-__global__ void __launch_bounds__(kThreads) evict_kernel(const EvictParams p) {
+__global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams p) {
   extern __shared__ __align__(16) unsigned char dyn[];
   __shared__ EvictSmem s;
   uint32_t* keys = reinterpret_cast<uint32_t*>(dyn);                        // [slice]
@@ -112,7 +134,7 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictParams p) {
     bad |= kDevBadWeights;
     keep = n;
   }
-  for (int i = tid; i < 4 * kSub * 256; i += kThreads) (&s.hist[0][0][0])[i] = 0;
+  for (int i = tid; i < kSub * kBins; i += kThreads) (&s.hist[0][0])[i] = 0;
 
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
@@ -125,82 +147,99 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictParams p) {
   const float* mass = p.mass + unit * p.stride;
   const int32_t* pos = p.pos + unit * p.stride;
   __syncthreads();
-  for (int i = tid; i < mine; i += kThreads) {
-    const uint32_t key = __ldcg(pos + lo + i) >= edge ? 0xffffffffu
-                                                     : weight_key(__ldcg(mass + lo + i));
-    keys[i] = key;
-    atomicAdd(&s.hist[0][warp % kSub][key >> 24], 1);
+  constexpr int kKeyBatch = 8;   // rows a thread has in flight (one after the other: 1 us each)
+  int* my_hist = s.hist[warp % kSub];
+  for (int i0 = tid; i0 - lane < mine; i0 += kKeyBatch * kThreads) {
+    int at[kKeyBatch];
+    float w[kKeyBatch];
+#pragma unroll
+    for (int u = 0; u < kKeyBatch; ++u) {
+      const int i = i0 + u * kThreads;
+      at[u] = i < mine ? __ldcg(pos + lo + i) : 0;
+      w[u] = i < mine ? __ldcg(mass + lo + i) : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < kKeyBatch; ++u) {
+      const int i = i0 + u * kThreads;
+      const uint32_t key = at[u] >= edge ? 0xffffffffu : weight_key(w[u]);
+      if (i < mine) keys[i] = key;
+      if (i - lane < mine) count_digit(my_hist, i < mine ? (int)(key >> 21) : -1);
+    }
   }
   // --- the keep-th largest key
   uint32_t prefix = 0, mask = 0;
   int krem = keep;
-  for (int pass = 0; pass < 4; ++pass) {
-    const int shift = 24 - 8 * pass;
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const uint32_t digits = pass == 2 ? 0x3ffu : 0x7ffu;
     if (pass > 0) {
-      for (int i = tid; i < mine; i += kThreads) {
-        const uint32_t key = keys[i];
-        if ((key & mask) == prefix) atomicAdd(&s.hist[pass][warp % kSub][(key >> shift) & 255u], 1);
+      for (int i = tid; i - lane < mine; i += kThreads) {
+        const uint32_t key = i < mine ? keys[i] : 0u;
+        const bool in = i < mine && (key & mask) == prefix;
+        if (__any_sync(0xffffffffu, in)) count_digit(my_hist, in ? (int)((key >> shift) & digits) : -1);
       }
     }
     __syncthreads();
-    if (tid < 256) {
-      int c = 0;
+    int4 c = *reinterpret_cast<const int4*>(&s.hist[0][4 * tid]);
 #pragma unroll
-      for (int q = 0; q < kSub; ++q) c += s.hist[pass][q][tid];
-      s.total[pass][tid] = c;
+    for (int q = 1; q < kSub; ++q) {
+      const int4 x = *reinterpret_cast<const int4*>(&s.hist[q][4 * tid]);
+      c = make_int4(c.x + x.x, c.y + x.y, c.z + x.z, c.w + x.w);
     }
-    cluster_barrier();
-    if (warp == 0) {   // lane L has bins 255-8L .. 248-8L
-      int cnt[8], tot = 0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) cnt[j] = 0;
-      for (int r = 0; r < S; ++r) {
+    for (int q = 0; q < kSub; ++q) *reinterpret_cast<int4*>(&s.hist[q][4 * tid]) = make_int4(0, 0, 0, 0);
+    if (S > 1) {
+      *reinterpret_cast<int4*>(&s.total[pass & 1][4 * tid]) = c;
+      cluster_sync();
+      int4 v[kEvictCluster];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int* at = &s.total[pass][255 - 8 * lane - j];
-          cnt[j] += S > 1 ? ld_peer(peer(at, r)) : *at;
-        }
+      for (int r = 0; r < kEvictCluster; ++r)
+        v[r] = r < S ? ld_peer4(peer(&s.total[pass & 1][4 * tid], r)) : make_int4(0, 0, 0, 0);
+      c = make_int4(0, 0, 0, 0);
+#pragma unroll
+      for (int r = 0; r < kEvictCluster; ++r)
+        c = make_int4(c.x + v[r].x, c.y + v[r].y, c.z + v[r].z, c.w + v[r].w);
+    }
+    int all;
+    const int above = block_scan(c.x + c.y + c.z + c.w, s.warp_sum, all);   // bins in descending order
+    const int bin[4] = {c.x, c.y, c.z, c.w};
+    int run = above;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (run < krem && krem <= run + bin[j]) {
+        s.pick[0] = kBins - 1 - (4 * tid + j);
+        s.pick[1] = run;
+        s.pick[2] = bin[j];
       }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) tot += cnt[j];
-      int incl = tot;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      int c = incl - tot;
-      if (c < krem && krem <= incl) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (c < krem && krem <= c + cnt[j]) {
-            s.pick[0] = 255 - 8 * lane - j;
-            s.pick[1] = c;
-            s.pick[2] = cnt[j];
-          }
-          c += cnt[j];
-        }
-      }
+      run += bin[j];
     }
     __syncthreads();
     prefix |= (uint32_t)s.pick[0] << shift;
-    mask |= 255u << shift;
+    mask |= digits << shift;
     krem -= s.pick[1];
     if (krem == s.pick[2]) break;   // every key with this prefix stays: the same in every CTA
     __syncthreads();
   }
 
   // --- who stays: a key above the prefix, or one of the first krem equal ones
-  const int chunk = (mine + kThreads - 1) / kThreads;   // a thread's consecutive rows
+  const int chunk = (mine + kThreads - 1) / kThreads | 1;   // a thread's consecutive rows; odd: no bank conflicts
   const int c0 = min(mine, tid * chunk), c1 = min(mine, c0 + chunk);
-  int eq = 0;
-  for (int i = c0; i < c1; ++i) eq += (keys[i] & mask) == prefix;
-  int eq_all;
-  int eq_run = block_scan(eq, s.warp_sum, eq_all);
-  if (S > 1) {
-    if (tid == 0) s.counts[0] = eq_all;
-    cluster_sync();
-    for (int r = 0; r < rank; ++r) eq_run += ld_peer(peer(&s.counts[0], r));
+  int eq_run = 0;   // equal keys of the rows before this thread's; not needed where all of them stay
+  if (krem != s.pick[2]) {
+    int eq = 0, eq_all;
+    for (int i = c0; i < c1; ++i) eq += (keys[i] & mask) == prefix;
+    eq_run = block_scan(eq, s.warp_sum, eq_all);
+    if (S > 1) {
+      if (tid == 0) s.counts[0] = eq_all;
+      cluster_sync();
+      int v[kEvictCluster];
+#pragma unroll
+      for (int r = 0; r < kEvictCluster; ++r) v[r] = r < rank ? ld_peer(peer(&s.counts[0], r)) : 0;
+#pragma unroll
+      for (int r = 0; r < kEvictCluster; ++r) eq_run += v[r];
+    }
+  } else {
+    krem = 0x7fffffff;
   }
   const int cut = min(max(keep - lo, 0), mine);   // rows of the slice before `keep`
   int holes = 0, stays = 0, e = eq_run;
@@ -210,9 +249,11 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictParams p) {
     holes += !stay && i < cut;
     stays += stay && i >= cut;
   }
-  int holes_all, stays_all;
-  int hole_at = block_scan(holes, s.warp_sum, holes_all);
-  int stay_at = block_scan(stays, s.warp_sum, stays_all);
+  // both in one scan: a slice has at most 2^15 of either
+  int both_all;
+  const uint32_t before = (uint32_t)block_scan((int)((uint32_t)holes << 16 | (uint32_t)stays), s.warp_sum, both_all);
+  const int holes_all = (int)((uint32_t)both_all >> 16), stays_all = both_all & 0xffff;
+  int hole_at = (int)(before >> 16), stay_at = (int)(before & 0xffffu);
   e = eq_run;
   for (int i = c0; i < c1; ++i) {   // holes fill the list from its start, survivors behind them
     const uint32_t key = keys[i] & mask;
@@ -225,16 +266,26 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictParams p) {
     s.counts[2] = stays_all;
   }
   cluster_barrier();
-  if (tid == 0) {
+  if (warp == 0) {   // lane r: the lists of CTA r
     int x = 0, y = 0;
-    for (int r = 0; r < S; ++r) {
-      s.hole_base[r] = x;
-      s.stay_base[r] = y;
-      x += S > 1 ? ld_peer(peer(&s.counts[1], r)) : holes_all;
-      y += S > 1 ? ld_peer(peer(&s.counts[2], r)) : stays_all;
+    if (lane < S) {
+      x = S > 1 ? ld_peer(peer(&s.counts[1], lane)) : holes_all;
+      y = S > 1 ? ld_peer(peer(&s.counts[2], lane)) : stays_all;
     }
-    s.hole_base[S] = x;
-    s.stay_base[S] = y;
+    int xs = x, ys = y;
+#pragma unroll
+    for (int o = 1; o < kEvictCluster; o <<= 1) {
+      const int a = __shfl_up_sync(0xffffffffu, xs, o), b2 = __shfl_up_sync(0xffffffffu, ys, o);
+      if (lane >= o) {
+        xs += a;
+        ys += b2;
+      }
+    }
+    if (lane < S) {
+      s.hole_base[lane + 1] = xs;
+      s.stay_base[lane + 1] = ys;
+    }
+    if (lane == 0) s.hole_base[0] = s.stay_base[0] = 0;
   }
   __syncthreads();
   const int moves = min(s.hole_base[S], s.stay_base[S]);   // equal
