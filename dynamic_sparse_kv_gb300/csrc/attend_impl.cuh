@@ -1175,6 +1175,7 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
   float4 sgx[kSgU][2];
   float held[kSgU];   // weigh: what the accumulator holds of them
   int seen = 0;
+  float4 cur_x[2];    // weigh: the current token's logits
   if constexpr (MODE == kWeigh) {
     const float* mass = p.mass + ((size_t)b * p.Hkv + hkv) * p.w_stride;
 #pragma unroll
@@ -1182,7 +1183,14 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
       const int i = sg_lo + u * kThreads + tid;
       held[u] = i < sg_hi ? __ldcg(mass + i) : 0.f;
     }
-    if (c.has_cur && tid == 0) seen = __ldcg(p.seen + b);
+    if (c.has_cur && tid == 0) {
+      seen = __ldcg(p.seen + b);
+      if (c.cur_pos >= c.img_start && c.cur_pos < img_end) {
+        const float4* src4 = reinterpret_cast<const float4*>(logit_base + (size_t)(c.cur_pos - c.img_start) * kSlots);
+        cur_x[0] = __ldcg(src4);
+        cur_x[1] = __ldcg(src4 + 1);
+      }
+    }
   }
   if constexpr (stores_logits(MODE)) {
 #pragma unroll
@@ -1447,9 +1455,13 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
     }
     if (c.has_cur && tid == 0 && c.cur_pos >= c.img_start && c.cur_pos < img_end) {
       const int i = c.cur_pos - c.img_start;
-      const float4* src4 = reinterpret_cast<const float4*>(logit_base + (size_t)i * kSlots);
-      sp[i] = score(__ldcg(src4), __ldcg(src4 + 1));   // weigh: the row starts here
-      if constexpr (MODE == kWeigh) p.row_pos[unit * p.w_stride + i] = seen - 1;
+      if constexpr (MODE == kWeigh) {   // the row starts here
+        sp[i] = score(cur_x[0], cur_x[1]);
+        p.row_pos[unit * p.w_stride + i] = seen - 1;
+      } else {
+        const float4* src4 = reinterpret_cast<const float4*>(logit_base + (size_t)i * kSlots);
+        sp[i] = score(__ldcg(src4), __ldcg(src4 + 1));
+      }
     }
   }
 }
