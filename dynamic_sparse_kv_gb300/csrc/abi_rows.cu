@@ -270,7 +270,7 @@ fastocr_status fastocr_cross_attend(fastocr_handle* h, const void* q, const fast
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   // A decode step has one query token a sequence: those go to the split-K attend
   // kernel, whose small tiles keep more of the states in flight (16 sequences, 10
-  // heads, 2624 states: 31 us against 46 us). Where there can be
+  // heads, 2624 states: 37 us against 46 us). Where there can be
   // such sequences and others, both kernels run and each leaves the other's alone;
   // the row kernel finds out while the kernel before it ends.
   const bool single = rows <= p.n_groups;

@@ -4,7 +4,7 @@
 // 128 and streams its share of the keys in tiles of 128:
 //   S = Q K^T   tcgen05.mma, Q and K in shared memory, S in TMEM (fp32)
 //   P           softmax warps: one thread a row reads S, exponentiates in base 2
-//               against a lazily moved running max and writes P (bf16) over S
+//               against the row's base and writes P (bf16) over S
 //   O += P V    tcgen05.mma, P from TMEM, V from shared memory, O in TMEM (fp32)
 // The two row tiles take turns, so that one's softmax runs under the other's
 // products. With at most 128 rows both turns work on the same rows and
@@ -13,7 +13,18 @@
 // Roles: warps 0-3 and 4-7 the softmax of turn 0 and 1 (warp w owns TMEM lanes
 // 32 (w % 4)..), warps 8-11 copy K and V rows, gathered from pages of any size,
 // into 128-byte-swizzled tiles with 16-byte cp.async, warp 12 issues the MMAs
-// (warps 13-15 only make its register share a whole warpgroup's).
+// (warps 13-15 only make its register share a whole warpgroup's). TMA in the
+// copies' place was slower here: a page of 16 keys makes boxes of 2 KB, 23
+// bytes a cycle and SM (4 x 1024 queries on 8320 states 437 us), and four
+// gathered rows an instruction 7 (1190 us); K by TMA next to V by cp.async 380 us;
+// cp.async alone 370 us, all before the work was dealt out evenly.
+//
+// Many rows: 128 x 128 x d products take 2048 cycles a key tile of two row tiles,
+// and 64 KB of keys must arrive meanwhile. Over all SMs that is
+// more than the L2 delivers: a tile takes 3400 cycles at 5.7 TB/s (4 x 1024
+// queries, 28 heads, 8320 states: 301 us, 1.08 PFLOP/s). Few rows: the chain
+// of a start, one or two tiles and the output, 9 us in all (8 sequences on 4160
+// keys), and the parts' way through the L2.
 #include <math_constants.h>
 
 #include <type_traits>

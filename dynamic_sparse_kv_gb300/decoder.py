@@ -318,7 +318,8 @@ class DecodeAttention:
         C, the selections of the focal layers (the deepest one is F_last, the
         next step's carried selection) and, while a warm-up window is open, the
         profiler's accumulated image mass (with the per-layer selection buffers
-        of warmup_step(select=True), which the scheduled window leaves unused).
+        of warmup_step(select=True), which the scheduled window leaves unused);
+        and the rows' weights and positions, if they are tracked.
         Synchronises the stream. The KV cache is the caller's and not part of it."""
         if stream is not None:
             stream.synchronize()
@@ -328,7 +329,9 @@ class DecodeAttention:
               "tau": self.tau, "max_img": self.max_img, "focal": tuple(self.focal),
               "has_f_last": self.has_f_last,
               "sel": {l: (idx.cpu(), k.cpu()) for l, (idx, k) in self.sel.items()},
-              "warm": None}
+              "warm": None, "weights": None}
+        if self.weights is not None:
+            st["weights"] = {x: self.weights[x].cpu() for x in ("mass", "pos", "seen", "protect")}
         if self.warm_idx is not None:
             st["warm"] = (self.warm_idx.cpu(), self.warm_k.cpu(),
                           N.fastocr_profiler_read(self.handle, self.layers, stream))
@@ -350,6 +353,12 @@ class DecodeAttention:
         for l, (idx, k) in st["sel"].items():
             self.sel[l][0].copy_(idx)
             self.sel[l][1].copy_(k)
+        weights = st.get("weights")
+        if weights is not None:
+            if self.weights is None or self.weights["mass"].shape != weights["mass"].shape:
+                raise ValueError("checkpoint has weights: call track_weights with as many rows first")
+            for x, t in weights.items():
+                self.weights[x].copy_(t)
         self.has_f_last = bool(st["has_f_last"])
         if st["warm"] is None:
             self.warm_idx = self.warm_k = None

@@ -446,3 +446,174 @@ def test_on_another_stream_and_twice_at_once():
     torch.cuda.synchronize()
     for c, start, prefix, n, q, out, *_ in runs:
         check_shared(c, start, prefix, n, q, out)
+
+
+def test_refusals():
+    from dynamic_sparse_kv_gb300 import CrossAttention, _native as N
+    heads = (4, 2, 64)
+    c, start, prefix, n, q = shared_case([2, 1], [40, 20], [3, 1, 20], heads, 16, BF, 71)
+    dec = decoder(c, n, 4)
+    out = torch.full_like(q, 7.0)
+    with pytest.raises(RuntimeError):
+        dec.shared_layer(0, q, out)
+    with pytest.raises(RuntimeError):
+        dec.weigh_layer(0, q, out)
+    with pytest.raises(RuntimeError):
+        dec.evict_layer(0, 1, 0)
+    with pytest.raises(RuntimeError):
+        dec.evict_step(1, 0)
+    for bad in ([0, 2], [1, 3], [0, 2, 1, 3], [0], [0, 1, 1, 2, 3, 3]):
+        with pytest.raises(ValueError):
+            dec.share_prefix(bad, torch.tensor(prefix))
+    with pytest.raises(ValueError):
+        dec.share_prefix(start, torch.tensor([40, 20]))
+    with pytest.raises(ValueError):
+        dec.track_weights(0, 0)
+    with pytest.raises(ValueError):
+        dec.track_weights(5, 0, mass=torch.zeros(1, 3, 2, 4, device="cuda"))
+    with pytest.raises(ValueError):
+        dec.track_weights(5, 0, seen=torch.zeros(3, dtype=torch.int64, device="cuda"))
+    dec.share_prefix(start, torch.tensor(prefix))
+    dec.track_weights(64, torch.tensor(prefix))
+    g, w = dec.groups, dec.weights["c"][0]
+
+    def status(call, *args):
+        with pytest.raises(N.FastOCRError) as e:
+            call(*args)
+        return e.value.status
+
+    ws = g["ws"]
+    assert status(N.fastocr_shared_attend, dec.handle, q, dec.kv[0], g["c"], out, ws, ws.numel() - 1) \
+        == N.FASTOCR_ERR_INVALID
+    assert status(N.fastocr_shared_attend, dec.handle, q, dec.kv[0], g["c"], out, None, 0) == N.FASTOCR_ERR_NULL
+    assert status(N.fastocr_shared_attend, dec.handle, q, dec.kv[0], g["c"], out, ws.data_ptr() + 4,
+                  ws.numel()) == N.FASTOCR_ERR_ALIGN
+    none = N.make_groups(g["start"], g["prefix_len"])
+    none.n = 0
+    assert status(N.fastocr_shared_attend, dec.handle, q, dec.kv[0], none, out, ws, ws.numel()) \
+        == N.FASTOCR_ERR_INVALID
+    none.n = 4
+    assert status(N.fastocr_shared_attend, dec.handle, q, dec.kv[0], none, out, ws, ws.numel()) \
+        == N.FASTOCR_ERR_INVALID
+    for budget, recent in ((0, 0), (4, 5), (4, -1)):
+        assert status(N.fastocr_evict, dec.handle, dec.kv[0], w, budget, recent) == N.FASTOCR_ERR_INVALID
+    assert status(N.fastocr_evict, dec.handle, dec.kv[0], w, 4, 1, dec.seq_len) == N.FASTOCR_ERR_INVALID
+    no_logits = N.make_weights(dec.weights["mass"][0], dec.weights["pos"][0], dec.weights["protect"],
+                               dec.weights["seen"], None)
+    assert status(N.fastocr_weigh_attend, dec.handle, q, dec.kv[0], no_logits, out) == N.FASTOCR_ERR_NULL
+    no_logits.stride = 0
+    assert status(N.fastocr_evict, dec.handle, dec.kv[0], no_logits, 4, 1) == N.FASTOCR_ERR_INVALID
+    assert status(N.fastocr_rows_workspace, dec.handle, -1) == N.FASTOCR_ERR_INVALID
+    assert status(N.fastocr_rows_workspace, dec.handle, 1 << 40) == N.FASTOCR_ERR_INVALID
+    ca = CrossAttention(c.k[None], c.v[None], c.gpu_table(), 20, q_heads=4, max_rows=1)
+    qs = torch.tensor([0, 1, 2, 3], dtype=torch.int32, device="cuda")
+    with pytest.raises(N.FastOCRError):      # more rows than the workspace is for
+        ca.attend(0, q, qs, out)
+    for args in ((q.float(), qs, out), (q, qs.long(), out), (q, qs[:3], out), (q, qs.cpu(), out),
+                 (q, qs, out[:2]), (q.transpose(0, 1), qs, out.transpose(0, 1))):
+        with pytest.raises(ValueError):
+            ca.attend(0, *args)
+    ca.attend(0, q[:0], torch.zeros(4, dtype=torch.int32, device="cuda"), out[:0])
+    torch.cuda.synchronize()
+    assert (out == 7.0).all() and dec.device_status() == 0 and ca.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_large_logits_and_a_rising_max(dtype):
+    """Logits of hundreds that rise from tile to tile: the row's base has to move; and a first tile
+    far above the rest."""
+    heads = (2, 1, 64)
+    from dynamic_sparse_kv_gb300 import CrossAttention
+    n = 700
+    for order in (1.0, -1.0):
+        c, start, q = cross_case([3, 200], [n, n], heads, 16, dtype, 81)
+        q[:] = 4.0
+        level = order * torch.linspace(-20, 20, n)     # logit = 4 * 64 * level / 8 up to 640
+        for b in range(2):
+            r = torch.arange(n)
+            rows = torch.full((n, 64), 1.0) * level[:, None] + 0.01 * torch.randn(n, 64)
+            c.k[c.table[b][r // 16].long(), 0, r % 16] = rows.to(dtype).cuda()
+        ca = CrossAttention(c.k[None], c.v[None], c.gpu_table(), n, q_heads=2)
+        out = torch.full_like(q, 7.0)
+        ca.attend(0, q, start, out)
+        check_cross(c, [3, 200], [n, n], q, out)
+
+
+def test_rows_past_4_gib():
+    """Cache offsets that need more than 32 bits: shared prefix, weights and eviction."""
+    hkv, page, d = 4, 16, 128
+    pages = (5 << 30) // (hkv * page * d * 2)
+    k = torch.empty(1, pages, hkv, page, d, dtype=BF, device="cuda")
+    v = torch.empty_like(k)
+    g = torch.Generator().manual_seed(3)
+    cols = 12
+    table = (pages - 1 - torch.randperm(2 * cols, generator=g)).to(torch.int32).view(2, cols)
+    for x in (k, v):
+        x[0, pages - 2 * cols:] = torch.randn(2 * cols, hkv, page, d, generator=g).to(BF).cuda()
+    from dynamic_sparse_kv_gb300 import DecodeAttention
+    dec = DecodeAttention(k, v, table, q_heads=8)
+    n = [180, 170]
+    dec.set_seq_len(torch.tensor(n, dtype=torch.int32, device="cuda"))
+    dec.share_prefix([0, 2], 130)
+    dec.track_weights(60, 130)
+
+    class Cache:
+        pass
+    c = Cache()
+    c.page, c.table = page, table - (pages - 2 * cols)
+    c.k, c.v = k[0, pages - 2 * cols:], v[0, pages - 2 * cols:]
+    c.rows = lambda b, lo, hi: Paged.rows(c, b, lo, hi)
+    q = torch.randn(2, 8, d, generator=g).to(BF).cuda()
+    out = torch.full_like(q, float("nan"))
+    dec.shared_layer(0, q, out)
+    check_shared(c, [0, 2], [130, 130], n, q, out)
+    k0, v0 = c.k.clone(), c.v.clone()
+    mass0, pos0 = dec.weights["mass"][0].cpu(), dec.weights["pos"][0].cpu()
+    new_len = torch.zeros(2, dtype=torch.int32, device="cuda")
+    dec.evict_layer(0, 20, 5, new_len)
+    check_evict(c, k0, v0, n, mass0, pos0, n, [130, 130], 20, 5, dec, new_len)
+    assert dec.device_status() == 0
+
+
+def test_weights_are_part_of_a_checkpoint():
+    heads = (4, 2, 64)
+    c, _, _, n, q = shared_case([2], [0], [30, 21], heads, 16, BF, 91)
+    out = torch.empty_like(q)
+    dec = decoder(c, n, 4)
+    dec.track_weights(40, 0)
+    dec.weigh_layer(0, q, out)
+    st = dec.state_dict()
+    other = decoder(c, n, 4)
+    with pytest.raises(ValueError):
+        other.load_state_dict(st)
+    other.track_weights(40, 0)
+    other.load_state_dict(st)
+    for x in ("mass", "pos", "seen", "protect"):
+        assert torch.equal(other.weights[x], dec.weights[x])
+    for d in (dec, other):
+        d.weigh_layer(0, q, out)
+    assert torch.equal(other.weights["mass"], dec.weights["mass"])
+
+
+def test_weighed_step_captured():
+    """A replay adds the step's weights once."""
+    from dynamic_sparse_kv_gb300 import CapturedStep
+    heads = (6, 2, 64)
+    c, _, _, n, q = shared_case([3], [0], [90, 21, 300], heads, 16, BF, 95)
+    runs = []
+    for graph in (False, True):
+        dec = decoder(c, n, 6)
+        dec.track_weights(300, 0)
+        out = torch.empty_like(q)[None]
+        if graph:
+            step = CapturedStep(dec, "weighed")
+            assert step.launches == 1
+            dec.weights["mass"].zero_()
+            step.q.copy_(q[None])
+            step.replay()
+            step.replay()
+        else:
+            dec.weighed_step(q[None], out)
+            dec.weighed_step(q[None], out)
+        runs.append((dec.weights["mass"].clone(), dec.weights["pos"].clone()))
+    assert torch.equal(runs[0][0], runs[1][0]) and torch.equal(runs[0][1], runs[1][1])
