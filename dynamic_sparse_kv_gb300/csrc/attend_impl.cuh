@@ -1098,7 +1098,7 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
   auto ext_add = [&](int h, int c4, float base, int s0, int step, float4& a) {
     if constexpr (kExternal) {
       const float4* src = reinterpret_cast<const float4*>(n_ext == 1 ? p.ext_row_acc : p.ext_slot_acc) + c4;
-      constexpr int kAtOnce = 8;
+      constexpr int kAtOnce = 12;
       for (int s = s0; s < n_ext; s += kAtOnce * step) {
         float4 v[kAtOnce];
         float sc[kAtOnce];

@@ -153,30 +153,79 @@ struct PlanSmem {
   RowGroup grp;
 };
 
+// Units a CTA takes and the share of an item, from the totals over all groups.
+__device__ __forceinline__ void choose_share(const RowsParams& p, int all, int items, int most, Walk& w) {
+  // an item's parts fit the merging kernels' lists
+  const int C = gridDim.x, least = max(1, (most + kMaxExt - 3) / (kMaxExt - 2));
+  w.share = 0;
+  if (2 * items <= C) {   // the shares are at most all / share + items <= C
+    w.share = max(max(p.min_share, least), (all + C - items - 1) / (C - items));
+    w.per = 1;
+  } else {
+    w.per = max(least, (all + C - 1) / C);
+  }
+}
+
+// The CTA's run of `all` units; false: it has none.
+__device__ __forceinline__ bool take_units(int all, Walk& w) {
+  const long long first = (long long)blockIdx.x * w.per;
+  w.begin = w.unit = (int)min((long long)all, first);
+  w.end = (int)min((long long)all, first + w.per);
+  return first < all;
+}
+
 // Where this CTA's units are; called by all THREADS threads. False: it has none.
+// Up to 32 groups every warp works it out for itself, without a barrier (every
+// call starts with this: 2 us through barriers, half of that without).
 template <int THREADS>
 __device__ __forceinline__ bool plan_walk(const RowsParams& p, PlanSmem& s, Walk& w, int& bad) {
   constexpr int NW = THREADS / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int chunk = (p.n_groups + THREADS - 1) / THREADS;   // consecutive groups a thread sums
-  const int i0 = min(p.n_groups, tid * chunk), i1 = min(p.n_groups, i0 + chunk);
-  int sum = 0, items = 0, most = 0;
-  RowGroup grp = {0, 0, 0, 0};
-  for (int i = i0; i < i1; ++i) {
-    grp = load_group(p, i, bad);
-    sum += group_units(p, grp, 0);
-    items += group_items(p, grp);
-    most = max(most, grp.n_tok > 0 ? key_tiles(grp.len) : 0);
-  }
-  // units before this warp, and of all
-  int mine, all;
-  auto scan = [&](int x, int* warp_sum) {
+  auto warp_prefix = [&](int x) {
     int incl = x;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += y;
     }
+    return incl;
+  };
+  RowGroup grp = {0, 0, 0, 0};
+  if (p.n_groups <= 32) {
+    int sum = 0, items = 0, most = 0;
+    if (lane < p.n_groups) {
+      grp = load_group(p, lane, bad);
+      sum = group_units(p, grp, 0);
+      items = group_items(p, grp);
+      most = grp.n_tok > 0 ? key_tiles(grp.len) : 0;
+    }
+    choose_share(p, __reduce_add_sync(0xffffffffu, sum), __reduce_add_sync(0xffffffffu, items),
+                 __reduce_max_sync(0xffffffffu, most), w);
+    if (w.share > 0) sum = group_units(p, grp, w.share);   // 0 for a lane without a group
+    const int incl = warp_prefix(sum);
+    if (!take_units(__shfl_sync(0xffffffffu, incl, 31), w)) return false;
+    const int src = __ffs(__ballot_sync(0xffffffffu, incl > w.unit)) - 1;
+    w.group = src;
+    w.off = w.unit - __shfl_sync(0xffffffffu, incl - sum, src);
+    w.grp.first = __shfl_sync(0xffffffffu, grp.first, src);
+    w.grp.n_tok = __shfl_sync(0xffffffffu, grp.n_tok, src);
+    w.grp.table_row = __shfl_sync(0xffffffffu, grp.table_row, src);
+    w.grp.len = __shfl_sync(0xffffffffu, grp.len, src);
+    return true;
+  }
+  const int chunk = (p.n_groups + THREADS - 1) / THREADS;   // consecutive groups a thread sums
+  const int i0 = min(p.n_groups, tid * chunk), i1 = min(p.n_groups, i0 + chunk);
+  int sum = 0, items = 0, most = 0;
+  for (int i = i0; i < i1; ++i) {
+    grp = load_group(p, i, bad);
+    sum += group_units(p, grp, 0);
+    items += group_items(p, grp);
+    most = max(most, grp.n_tok > 0 ? key_tiles(grp.len) : 0);
+  }
+  // units before this thread, and of all
+  int mine, all;
+  auto scan = [&](int x, int* warp_sum) {
+    const int incl = warp_prefix(x);
     if (lane == 31) warp_sum[warp] = incl;
     __syncthreads();
     int before = 0;
@@ -202,12 +251,8 @@ __device__ __forceinline__ bool plan_walk(const RowsParams& p, PlanSmem& s, Walk
     items += s.warp_items[v];
     most = max(most, s.warp_max[v]);
   }
-  // an item's parts fit the merging kernels' lists
-  const int C = gridDim.x, least = max(1, (most + kMaxExt - 3) / (kMaxExt - 2));
-  w.share = 0;
-  if (2 * items <= C) {   // the shares are at most all / share + items <= C
-    w.share = max(max(p.min_share, least), (all + C - items - 1) / (C - items));
-    w.per = 1;
+  choose_share(p, all, items, most, w);
+  if (w.share > 0) {
     sum = 0;
     for (int i = i0; i < i1; ++i) {
       int none = 0;
@@ -215,13 +260,8 @@ __device__ __forceinline__ bool plan_walk(const RowsParams& p, PlanSmem& s, Walk
       sum += group_units(p, grp, w.share);
     }
     scan(sum, s.warp_sum[1]);
-  } else {
-    w.per = max(least, (all + C - 1) / C);
   }
-  const long long first = (long long)blockIdx.x * w.per;
-  if (first >= all) return false;
-  w.begin = w.unit = (int)first;
-  w.end = (int)min((long long)all, first + w.per);
+  if (!take_units(all, w)) return false;
   if (mine <= w.unit && w.unit < mine + sum) {
     int at = mine, i = i0;
     if (chunk > 1) {   // which of this thread's groups
