@@ -617,3 +617,42 @@ def test_weighed_step_captured():
             dec.weighed_step(q[None], out)
         runs.append((dec.weights["mass"].clone(), dec.weights["pos"].clone()))
     assert torch.equal(runs[0][0], runs[1][0]) and torch.equal(runs[0][1], runs[1][1])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("batch", [33, 700])
+def test_many_groups(dtype, batch):
+    """More groups than a warp's lanes and than a CTA's threads, empty ones among them."""
+    heads = (4, 2, 64)
+    g = np.random.default_rng(batch)
+    sizes = [int(x) for x in g.integers(0, 3, batch)]
+    sizes = [x for x in sizes if x] or [1]
+    prefixes = [int(x) for x in g.integers(0, 300, len(sizes))]
+    tails = [int(x) for x in g.integers(1, 20, sum(sizes))]
+    c, start, prefix, n, q = shared_case(sizes, prefixes, tails, heads, 16, dtype, batch)
+    dec = decoder(c, n, 4)
+    dec.share_prefix(start, torch.tensor(prefix))
+    dec.groups["ws"].fill_(127)
+    out = torch.full_like(q, float("nan"))
+    dec.shared_layer(0, q, out)
+    some = sorted(set([0, 1, len(sizes) - 1] + [int(x) for x in g.integers(0, len(sizes), 12)]))
+    for i in some:
+        for b in range(start[i], start[i + 1]):
+            K0, V0 = c.rows(start[i], 0, prefix[b])
+            K1, V1 = c.rows(b, prefix[b], n[b])
+            check_out(out[b:b + 1], np64(q[b:b + 1]), np.concatenate([K0, K1]), np.concatenate([V0, V1]),
+                      dtype, f"sequence {b}")
+    assert torch.isfinite(out.float()).all() and dec.device_status() == 0
+    from dynamic_sparse_kv_gb300 import CrossAttention
+    t = [int(x) for x in g.integers(0, 4, len(n))]
+    cs = torch.from_numpy(np.concatenate([[0], np.cumsum(t)]).astype(np.int32)).cuda()
+    qx = (2 * torch.randn(sum(t), 4, 64, generator=torch.Generator().manual_seed(1))).to(dtype).cuda()
+    ca = CrossAttention(c.k[None], c.v[None], c.gpu_table(), torch.tensor(n), q_heads=4)
+    ox = torch.full_like(qx, 7.0)
+    ca.attend(0, qx, cs, ox)
+    at = np.concatenate([[0], np.cumsum(t)])
+    for b in some:
+        if t[b]:
+            K, V = c.rows(b, 0, n[b])
+            check_out(ox[at[b]:at[b + 1]], np64(qx[at[b]:at[b + 1]]), K, V, dtype, f"cross {b}")
+    assert torch.isfinite(ox.float()).all() and ca.device_status() == 0
