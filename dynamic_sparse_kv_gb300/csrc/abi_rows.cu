@@ -122,7 +122,8 @@ int64_t place_workspace(const fastocr_handle* h, int64_t rows, bool shared, char
 // The kernels count units of work in 32 bits.
 bool units_fit(const fastocr_handle* h, int64_t rows, int64_t groups) {
   const int64_t g = h->dims.num_q_heads / h->dims.num_kv_heads;
-  const int64_t tiles = 2 * rows * g / tile_rows(h) + std::min(rows, groups);
+  const int64_t least = (h->dims.dtype == FASTOCR_DTYPE_BF16 ? kRowsBf16 / 2 : 16) / g;   // tokens of a row tile
+  const int64_t tiles = rows / least + std::min(rows, groups);
   return (double)tiles * h->dims.num_kv_heads * (max_tokens(h) / kKeyTile + 1) < 2147483647.0;
 }
 

@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
   int q_row = b;
   if constexpr (MODE == kCross) {
     const int s = __ldcg(p.q_start + b), e = __ldcg(p.q_start + b + 1);
-    if (e - s != 1 || s < 0 || e > p.q_rows) {   // none, or the row kernel's: the whole cluster's answer
+    if (s < 0 || e > p.q_rows || s >= e || e - s != 1) {   // none, or the row kernel's: the whole cluster's answer
       asm volatile("griddepcontrol.wait;\n" ::: "memory");   // this grid may not end before the one before it
       return;
     }

@@ -69,10 +69,12 @@ struct RowGroup {
   int len;            // keys
 };
 
-// Group i, offsets and lengths clamped into range; faults are ORed into bad.
-__device__ __forceinline__ RowGroup load_group(const RowsParams& p, int i, int& bad) {
+// Group i, offsets and lengths clamped into range; faults are ORed into bad, and
+// `disordered` is set where the group ends before it starts.
+__device__ __forceinline__ RowGroup load_group(const RowsParams& p, int i, int& bad, bool& disordered) {
   RowGroup r;
   int s = __ldcg(p.start + i), e = __ldcg(p.start + i + 1);
+  disordered |= e < s;
   if (s < 0 || e < s || e > p.rows || (i == 0 && s != 0) ||
       (p.prefix_len && i == p.n_groups - 1 && e != p.rows))
     bad |= kDevBadGroup;
@@ -175,6 +177,8 @@ __device__ __forceinline__ bool take_units(int all, Walk& w) {
 }
 
 // Where this CTA's units are; called by all THREADS threads. False: it has none.
+// Offsets out of order leave all CTAs without work: groups would share rows, and
+// their units could be more than 32 bits count.
 // Up to 32 groups every warp works it out for itself, without a barrier (every
 // call starts with this: 2 us through barriers, half of that without).
 template <int THREADS>
@@ -191,14 +195,16 @@ __device__ __forceinline__ bool plan_walk(const RowsParams& p, PlanSmem& s, Walk
     return incl;
   };
   RowGroup grp = {0, 0, 0, 0};
+  bool disordered = false;
   if (p.n_groups <= 32) {
     int sum = 0, items = 0, most = 0;
     if (lane < p.n_groups) {
-      grp = load_group(p, lane, bad);
+      grp = load_group(p, lane, bad, disordered);
       sum = group_units(p, grp, 0);
       items = group_items(p, grp);
       most = grp.n_tok > 0 ? key_tiles(grp.len) : 0;
     }
+    if (__any_sync(0xffffffffu, disordered)) return false;
     choose_share(p, __reduce_add_sync(0xffffffffu, sum), __reduce_add_sync(0xffffffffu, items),
                  __reduce_max_sync(0xffffffffu, most), w);
     if (w.share > 0) sum = group_units(p, grp, w.share);   // 0 for a lane without a group
@@ -217,11 +223,12 @@ __device__ __forceinline__ bool plan_walk(const RowsParams& p, PlanSmem& s, Walk
   const int i0 = min(p.n_groups, tid * chunk), i1 = min(p.n_groups, i0 + chunk);
   int sum = 0, items = 0, most = 0;
   for (int i = i0; i < i1; ++i) {
-    grp = load_group(p, i, bad);
+    grp = load_group(p, i, bad, disordered);
     sum += group_units(p, grp, 0);
     items += group_items(p, grp);
     most = max(most, grp.n_tok > 0 ? key_tiles(grp.len) : 0);
   }
+  if (__syncthreads_or(disordered)) return false;
   // units before this thread, and of all
   int mine, all;
   auto scan = [&](int x, int* warp_sum) {
@@ -255,8 +262,7 @@ __device__ __forceinline__ bool plan_walk(const RowsParams& p, PlanSmem& s, Walk
   if (w.share > 0) {
     sum = 0;
     for (int i = i0; i < i1; ++i) {
-      int none = 0;
-      if (chunk > 1) grp = load_group(p, i, none);
+      if (chunk > 1) grp = load_group(p, i, bad, disordered);
       sum += group_units(p, grp, w.share);
     }
     scan(sum, s.warp_sum[1]);
@@ -266,8 +272,7 @@ __device__ __forceinline__ bool plan_walk(const RowsParams& p, PlanSmem& s, Walk
     int at = mine, i = i0;
     if (chunk > 1) {   // which of this thread's groups
       for (;; ++i) {
-        int none = 0;
-        grp = load_group(p, i, none);
+        grp = load_group(p, i, bad, disordered);
         const int u = group_units(p, grp, w.share);
         if (w.unit < at + u) break;
         at += u;
@@ -290,7 +295,8 @@ __device__ __forceinline__ bool next_segment(const RowsParams& p, Walk& w, Segme
   const int tpt = p.tile_tokens;
   while (w.off >= group_units(p, w.grp, w.share)) {   // another group with rows exists: w.unit < w.end
     int none = 0;                                // reported by plan_walk
-    w.grp = load_group(p, ++w.group, none);
+    bool disordered = false;
+    w.grp = load_group(p, ++w.group, none, disordered);
     w.off = 0;
   }
   const int u = units_of(w.grp.len, w.share), n_tiles = key_tiles(w.grp.len);

@@ -295,9 +295,8 @@ int64_t fastocr_rows_workspace(const fastocr_handle* h, int64_t rows);
  * pages need to hold the prefix; prefix_len need not be a multiple of the page
  * size (entries of the other sequences' tables for whole prefix pages are not
  * read). prefix_len[b] <= N_t of every sequence of the group; a longer one is
- * reported as FASTOCR_DEV_BAD_GROUP and clamped. Offsets in start that are out
- * of order are reported the same way; the output of a sequence in no group is
- * then unspecified.
+ * reported as FASTOCR_DEV_BAD_GROUP and clamped. Offsets in start that do not
+ * ascend from 0 to B are reported the same way; the output is then unspecified.
  * weights: NULL, or accumulates weights like fastocr_weigh_attend (needs
  * protect[b] >= prefix_len[b]).
  * ws: device, 16-byte aligned, caller-owned, fastocr_rows_workspace(h, 0) bytes.
@@ -335,8 +334,8 @@ fastocr_status fastocr_weigh_attend(fastocr_handle* h, const void* q, const fast
  * every unit of the call reads) = the rows left; the next token goes to row
  * new_len[b]. A sequence with more than `stride` rows is reported as
  * FASTOCR_DEV_BAD_WEIGHTS and left as it is; a move from or to a page out of
- * range moves mass and pos only (FASTOCR_DEV_BAD_PAGE). Pages behind protect
- * must not be shared between sequences. Only prefix positions keep their
+ * range moves mass and pos only (FASTOCR_DEV_BAD_PAGE). A page behind protect
+ * must not be in two sequences' tables, nor twice in one. Only prefix positions keep their
  * meaning after it: rows are no longer in text order, so fastocr_rswa_attend's
  * window and an image behind protect do not apply.
  * 1 <= budget, 0 <= recent <= budget, stride <= 262144 (UNSUPPORTED). One
@@ -350,8 +349,9 @@ fastocr_status fastocr_evict(fastocr_handle* h, const fastocr_kv* kv, const fast
  * [rows, H_q, d] attend to all N_b = seq_len[b] states of sequence b in kv
  * (0 allowed: the output is 0), without a mask. q_start [B + 1]: device,
  * ascending from 0; sequences without queries are fine, and rows at and behind
- * q_start[B] are left as they are. Offsets out of order or past `rows` are
- * reported as FASTOCR_DEV_BAD_GROUP and clamped. rows * H_q < 2^31.
+ * q_start[B] are left as they are. Offsets below 0, past `rows` or out of order
+ * are reported as FASTOCR_DEV_BAD_GROUP, and the output is then unspecified.
+ * rows * H_q < 2^31.
  * ws: as fastocr_shared_attend, fastocr_rows_workspace(h, rows) bytes. Overlap:
  * as the other calls; q_start and the states' K/V rows are read before the
  * preceding kernel completes. Two kernels, or three where rows <= B.

@@ -656,3 +656,27 @@ def test_many_groups(dtype, batch):
             K, V = c.rows(b, 0, n[b])
             check_out(ox[at[b]:at[b + 1]], np64(qx[at[b]:at[b + 1]]), K, V, dtype, f"cross {b}")
     assert torch.isfinite(ox.float()).all() and ca.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("batch", [5, 70, 700])
+def test_disordered_offsets_leave_rows_alone(dtype, batch):
+    """Offsets that run back and forth: every other group would have all rows."""
+    from dynamic_sparse_kv_gb300 import CrossAttention, _native as N
+    c, _, prefix, n, q = shared_case([1] * batch, [20] * batch, [3] * batch, (4, 2, 64), 16, dtype, batch)
+    zigzag = torch.tensor([0, batch] * (batch // 2 + 1), dtype=torch.int32, device="cuda")[:batch + 1].contiguous()
+    dec = decoder(c, n, 4)
+    dec.share_prefix(zigzag, torch.tensor(prefix), max_prefix=20)
+    dec.groups["ws"].fill_(255)
+    dec.shared_layer(0, q, torch.empty_like(q))
+    assert dec.device_status() == N.DEV_BAD_GROUP
+    dec.share_prefix(list(range(batch + 1)), torch.tensor(prefix))   # and a good call after it
+    out = torch.full_like(q, float("nan"))
+    dec.shared_layer(0, q, out)
+    assert torch.isfinite(out.float()).all() and dec.device_status() == 0
+    qx = torch.cat([q, q])
+    back = torch.tensor([0, 2 * batch] * (batch // 2 + 1), dtype=torch.int32, device="cuda")[:batch + 1].contiguous()
+    ca = CrossAttention(c.k[None], c.v[None], c.gpu_table(), torch.tensor(n), q_heads=4)
+    ox = torch.full_like(qx, 7.0)
+    ca.attend(0, qx, back, ox)
+    assert ca.device_status() == N.DEV_BAD_GROUP and (ox == 7.0).all()
