@@ -19,12 +19,18 @@
 // gathered rows an instruction 7 (1190 us); K by TMA next to V by cp.async 380 us;
 // cp.async alone 370 us, all before the work was dealt out evenly.
 //
-// Many rows: 128 x 128 x d products take 2048 cycles a key tile of two row tiles,
-// and 64 KB of keys must arrive meanwhile. Over all SMs that is
-// more than the L2 delivers: a tile takes 3400 cycles at 5.7 TB/s (4 x 1024
-// queries, 28 heads, 8320 states: 301 us, 1.08 PFLOP/s). Few rows: the chain
-// of a start, one or two tiles and the output, 9 us in all (8 sequences on 4160
-// keys), and the parts' way through the L2.
+// Many rows (4 x 1024 queries, 28 heads, up to 8320 states: 275 us, 1.18
+// PFLOP/s): the products of a key tile of two row tiles take 2048 cycles, alone and
+// at full rate as measured, a tile here 3200. What bounds it is a turn's chain:
+// S = QK^T, 1400 cycles of softmax behind TMEM loads, PV, and about 250 cycles each time
+// a commit or a P has to be seen through a barrier; a sixth of a CTA's cycles are the starts and ends of
+// its three or four segments. Not the copies: with none at all it took 273 us.
+// Sixteen softmax warps with half a row each (283 us, the issuing warp then the
+// slowest link), an issuing warp a turn (309 us: the turns' products interleave
+// and both end late), a warp apart for the block table (283 us) and S loaded in
+// blocks of 32 columns under the exponentials (351 us, spills) brought nothing.
+// Few rows: the chain of a start, one or two tiles and the output, 9 us in all (8
+// sequences on 4160 keys), and the parts' way through the L2.
 #include <math_constants.h>
 
 #include <type_traits>
@@ -296,9 +302,13 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsParams p) {
     const int g_inv = inverse_of(p.g);
     int s_count = 0;      // S tiles this turn has seen
     int k_count = 0;      // key tiles of the segments before
-    int n_seg = 0;
     bool cut = false;
-    for (; more; more = next_from(p, walk, seg_p), ++n_seg) {
+    // index (in heads of q and out) of row r of an item
+    auto head_of = [&](int tok0, int hkv, int r) -> int {   // < 2^31, from the host
+      const int tok = token_of_row(r, g_inv);
+      return (tok0 + tok) * p.Hq + hkv * p.g + r - tok * p.g;
+    };
+    for (int n_seg = 0; more; ++n_seg) {
       const int n_tiles = seg_p->k1 - seg_p->k0;
       const bool pair = seg_p->n_rows > kTileRows;
       const int n = count_of(pair, n_tiles, t);
@@ -323,11 +333,9 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsParams p) {
           for (int u = 0; u < kBatch; ++u) {
             const int r = r0 + u * kStep;
             v[u] = make_uint4(0u, 0u, 0u, 0u);
-            if (r < seg.n_rows) {
-              const int tok = token_of_row(r, g_inv);
-              const int head = (seg.tok0 + tok) * p.Hq + seg.hkv * p.g + r - tok * p.g;   // < 2^31, from the host
-              v[u] = __ldcg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + (size_t)head * D) + c);
-            }
+            if (r < seg.n_rows)
+              v[u] = __ldcg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
+                                                           (size_t)head_of(seg.tok0, seg.hkv, r) * D) + c);
           }
 #pragma unroll
           for (int u = 0; u < kBatch; ++u) {
@@ -451,8 +459,21 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsParams p) {
       }
       k_count += n_tiles;
 
-      // ---------------- output
+      // ---------------- output; the next segment is found, and its Q fetched
+      // into L2, under the last products
       const int r = 32 * w + lane;   // row in the turn's tile
+      const int rr = (pair ? t * kTileRows : 0) + (lane < valid ? r : 0);
+      const bool whole = seg_p->whole, direct = p.out && whole;
+      // where this row goes: the output, a slot, or a shared prefix's whole rows
+      const int at = whole ? head_of(seg_p->tok0, seg_p->hkv, rr)
+                           : (2 * (int)blockIdx.x + seg_p->slot) * p.slot_rows + rr;
+      more = next_from(p, walk, seg_p);
+      if (more && tid < seg_p->n_rows) {
+        const char* row = reinterpret_cast<const char*>(static_cast<const __nv_bfloat16*>(p.q) +
+                                                        (size_t)head_of(seg_p->tok0, seg_p->hkv, tid) * D);
+#pragma unroll
+        for (int e = 0; e < D * 2; e += 128) asm volatile("prefetch.global.L2 [%0];\n" ::"l"(row + e));
+      }
       float wt[2] = {1.f, 1.f};      // weights of the turns' O
       bool have[2] = {n > 0, n > 0};
       mbar_wait(turn_bar(kODone, t), n_seg & 1, dead);
@@ -474,16 +495,9 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsParams p) {
       }
       tc_fence_after();
       if (valid > 0) {
-        const volatile Segment& seg = *seg_p;   // read again: not kept over the loop
-        const bool direct = p.out && seg.whole;
         const float inv = direct ? (l > 0.f ? __frcp_rn(l) : (l == 0.f ? 0.f : l)) : 1.f;
-        const int rr = (pair ? t * kTileRows : 0) + (lane < valid ? r : 0);
-        const int tok = token_of_row(rr, g_inv);
-        const int head = (seg.tok0 + tok) * p.Hq + seg.hkv * p.g + rr - tok * p.g;
-        // where this row goes: the output, a slot, or a shared prefix's whole rows
-        const int at = direct || seg.whole ? head : (2 * (int)blockIdx.x + seg.slot) * p.slot_rows + rr;
-        float* ml_dst = seg.whole ? p.row_ml : p.slot_ml;
-        float* acc_dst = seg.whole ? p.row_acc : p.slot_acc;
+        float* ml_dst = whole ? p.row_ml : p.slot_ml;
+        float* acc_dst = whole ? p.row_acc : p.slot_acc;
         if (!direct && lane < valid && (pair || t == 0))
           *reinterpret_cast<float2*>(ml_dst + 2 * (size_t)at) = make_float2(m, l);
         if (direct || n_tiles > 0) {
@@ -704,10 +718,10 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsParams p) {
             const int n = count[t];
             if (i >= n) continue;
             const bool last = i + 1 == n;
-            wait_ring(2 * tile_of(pair, t, i) + 1);
+            if (t == 0 || !pair) wait_ring(2 * tile_of(pair, t, i) + 1);   // else the other turn waited
             pv(t, tile_of(pair, t, i), i == 0, last);
             if (!last) {
-              wait_ring(2 * tile_of(pair, t, i + 1));
+              if (t == 0 || !pair) wait_ring(2 * tile_of(pair, t, i + 1));
               mbar_wait(turn_bar(kPvDone, t), pv_count[t] & 1, dead);   // S overwrites the P that PV reads
               ++pv_count[t];
               tc_fence_after();
