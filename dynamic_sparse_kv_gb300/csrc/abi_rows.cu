@@ -86,8 +86,8 @@ int choose_tile_tokens(const fastocr_handle* h, int64_t rows, int64_t groups, lo
 // Key tiles of a share, where few items are shared by all CTAs: a part of an item
 // costs its rows' partials written and read (about 1 KB a row), a key tile of a
 // share costs every CTA 1 to 2 us. The sum is least near sqrt(key tiles * rows /
-// 1600): measured at 2, 6, 3 and 8 for 33 tiles and 224 rows (17.5 us), 65 and
-// 896 (23.5 us), 16 and 896 (17.7 us), 65 and 1792 (30.3 us); within 1 us of
+// 1600): measured at 2, 6, 3 and 8 for 33 tiles and 224 rows (17.3 us), 65 and
+// 896 (22.4 us), 16 and 896 (17.7 us), 65 and 1792 (30.3 us); within 1 us of
 // the best share on nine shapes. fp32 tiles cost far more than their parts.
 int choose_share(const fastocr_handle* h, int64_t rows, long keys) {
   if (h->dims.dtype != FASTOCR_DTYPE_BF16) return 1;
@@ -271,7 +271,7 @@ fastocr_status fastocr_cross_attend(fastocr_handle* h, const void* q, const fast
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   // A decode step has one query token a sequence: those go to the split-K attend
   // kernel, whose small tiles keep more of the states in flight (16 sequences, 10
-  // heads, 2624 states: 37 us against 46 us). Where there can be
+  // heads, 2624 states: 36 us against 46 us). Where there can be
   // such sequences and others, both kernels run and each leaves the other's alone;
   // the row kernel finds out while the kernel before it ends.
   const bool single = rows <= p.n_groups;

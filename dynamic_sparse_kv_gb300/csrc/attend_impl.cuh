@@ -1066,8 +1066,8 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
   if constexpr (kExternal) {
     // a sequence in no group has no parts, whatever an earlier call left there
     if (p.ext_part) {
-      if (ext.y >= 1 && ext.y <= kMaxExt && ext.x >= 0 && ext.x + ext.y <= p.ext_ctas &&
-          (ext.z & ~1) == 0 && ext.w >= 0 && ext.w + p.g <= p.ext_slot_rows)
+      if (ext.y >= 1 && ext.y <= kMaxExt && ext.x >= 0 && ext.x <= p.ext_ctas - ext.y &&
+          (ext.z & ~1) == 0 && ext.w >= 0 && ext.w <= p.ext_slot_rows - p.g)
         n_ext = ext.y;
       else
         bad |= kDevBadGroup;

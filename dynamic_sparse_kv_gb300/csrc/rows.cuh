@@ -10,7 +10,7 @@
 // groups' sizes: a CTA walks over segments of items, of which only the first and
 // the last can be cut. With few items every CTA takes one unit, an equal share
 // of one item: a second segment would cost it another start and
-// output (5 us; 32 sequences on 8320 keys: 30 us dealt out, 24 us shared). A cut
+// output (5 us; 32 sequences on 8320 keys: 30 us dealt out, 22 us shared). A cut
 // segment leaves (max, sum, unnormalised output) of its rows, in base 2, in one
 // of the CTA's two slots of the workspace; who reads them (the tail's attend
 // kernel, or merge_kernel) joins an item's parts in the order of their keys.
@@ -180,7 +180,7 @@ __device__ __forceinline__ bool take_units(int all, Walk& w) {
 // Offsets out of order leave all CTAs without work: groups would share rows, and
 // their units could be more than 32 bits count.
 // Up to 32 groups every warp works it out for itself, without a barrier (every
-// call starts with this: 2 us through barriers, half of that without).
+// call starts with this: 2 us through barriers, about 1 us without).
 template <int THREADS>
 __device__ __forceinline__ bool plan_walk(const RowsParams& p, PlanSmem& s, Walk& w, int& bad) {
   constexpr int NW = THREADS / 32;

@@ -22,13 +22,14 @@
 // Many rows (4 x 1024 queries, 28 heads, up to 8320 states: 275 us, 1.18
 // PFLOP/s): the products of a key tile of two row tiles take 2048 cycles, alone and
 // at full rate as measured, a tile here 3200. What bounds it is a turn's chain:
-// S = QK^T, 1400 cycles of softmax behind TMEM loads, PV, and about 250 cycles each time
-// a commit or a P has to be seen through a barrier; a sixth of a CTA's cycles are the starts and ends of
-// its three or four segments. Not the copies: with none at all it took 273 us.
-// Sixteen softmax warps with half a row each (283 us, the issuing warp then the
-// slowest link), an issuing warp a turn (309 us: the turns' products interleave
-// and both end late), a warp apart for the block table (283 us) and S loaded in
-// blocks of 32 columns under the exponentials (351 us, spills) brought nothing.
+// S = QK^T, 1400 cycles of softmax behind TMEM loads, PV, and about 250 cycles
+// each time a commit or a P has to be seen through a barrier; a sixth of a CTA's
+// cycles are the starts and ends of its three or four segments. It is not the
+// copies: without any, 284 us became 273. Against those 284 us, sixteen softmax
+// warps with half a row each took 283 (the issuing warp is the slowest link
+// then), an issuing warp a turn 309 (the turns' products interleave and both end
+// late), a warp apart for the block table 283, and S loaded in blocks of 32 columns
+// under the exponentials 351 (spills).
 // Few rows: the chain of a start, one or two tiles and the output, 9 us in all (8
 // sequences on 4160 keys), and the parts' way through the L2.
 #include <math_constants.h>

@@ -475,7 +475,8 @@ class DecodeAttention:
 
     def evict_layer(self, l, budget, recent, new_len=None, stream=None):
         """Cut layer l's rows behind protect to `budget` a KV head, the `recent`
-        newest among them; new_len [B] int32 gets the rows left."""
+        newest among them; new_len [B] int32 gets the rows left. Something else
+        (evict_step copies new_len) must run before the layer attends again."""
         if self.weights is None:
             raise RuntimeError("track_weights has not been called")
         N.fastocr_evict(self.handle, self.kv[l], self.weights["c"][l], budget, recent, new_len,

@@ -340,7 +340,9 @@ fastocr_status fastocr_weigh_attend(fastocr_handle* h, const void* q, const fast
  * window and an image behind protect do not apply.
  * 1 <= budget, 0 <= recent <= budget, stride <= 262144 (UNSUPPORTED). One
  * kernel; protect, seen and seq_len are read before the preceding kernel
- * completes, mass and pos after it. */
+ * completes, mass and pos after it. A call that attends to the moved rows
+ * reads them before the kernel preceding it completes (see Overlap above), so
+ * another kernel or a copy, e.g. of new_len to seq_len, must come between. */
 fastocr_status fastocr_evict(fastocr_handle* h, const fastocr_kv* kv, const fastocr_weights* weights,
                              int32_t budget, int32_t recent, int32_t* new_len,
                              fastocr_stream stream);
