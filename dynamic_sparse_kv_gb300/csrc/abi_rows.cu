@@ -66,10 +66,10 @@ int64_t slot_rows(const fastocr_handle* h, int64_t rows) {
 // Tokens of a row tile. A bf16 tile of 256 rows reads each key once for all of
 // them, one of 128 twice, but its parts are half as large: where the keys of
 // few tiles are spread over all SMs, writing and joining the parts takes longer than
-// reading the keys (4 key tiles an SM or fewer: 896 rows on 8320 keys 28 us with
-// 256 rows, 24 us with 128). An fp32 tile of 64 rows reads shared memory less
+// reading the keys (4 key tiles an SM or fewer: 896 rows on 8320 keys 27 us with
+// 256 rows, 22 us with 128). An fp32 tile of 64 rows reads shared memory less
 // for a product; one of 16 is done sooner, where groups have few rows or all tiles
-// of 16 still find an SM each (12 rows on 272 keys: 20 us and 13.5 us).
+// of 16 still find an SM each (12 rows on 272 keys: 17.5 us and 13.6 us).
 int choose_tile_tokens(const fastocr_handle* h, int64_t rows, int64_t groups, long keys) {
   const int64_t g = h->dims.num_q_heads / h->dims.num_kv_heads;
   auto units = [&](int bm) {   // about

@@ -10,7 +10,7 @@
 // groups' sizes: a CTA walks over segments of items, of which only the first and
 // the last can be cut. With few items every CTA takes one unit, an equal share
 // of one item: a second segment would cost it another start and
-// output (5 us; 32 sequences on 8320 keys: 30 us dealt out, 22 us shared). A cut
+// output (5 us; 32 sequences on 8320 keys: 29 us dealt out, 22 us shared). A cut
 // segment leaves (max, sum, unnormalised output) of its rows, in base 2, in one
 // of the CTA's two slots of the workspace; who reads them (the tail's attend
 // kernel, or merge_kernel) joins an item's parts in the order of their keys.
