@@ -680,3 +680,33 @@ def test_disordered_offsets_leave_rows_alone(dtype, batch):
     ox = torch.full_like(qx, 7.0)
     ca.attend(0, qx, back, ox)
     assert ca.device_status() == N.DEV_BAD_GROUP and (ox == 7.0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows", [4, 90])
+def test_cross_attention_captured(dtype, rows):
+    """A replay follows lengths, offsets, queries and states that changed on the device; 4 rows for
+    4 sequences take the form for single tokens too."""
+    from dynamic_sparse_kv_gb300 import CrossAttention
+    heads = (4, 2, 64)
+    g = np.random.default_rng(rows)
+    c = Paged(4, 400, heads[1], heads[2], 16, dtype, rows)
+    n = torch.zeros(4, dtype=torch.int32, device="cuda")
+    qs = torch.zeros(5, dtype=torch.int32, device="cuda")
+    q = torch.zeros(rows, 4, 64, dtype=dtype, device="cuda")
+    out = torch.empty_like(q)
+    ca = CrossAttention(c.k[None], c.v[None], c.gpu_table(), n, q_heads=4, max_rows=rows)
+    ca.attend(0, q, qs, out)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ca.attend(0, q, qs, out)
+    for step in range(4):
+        t = [1] * 4 if step == 0 and rows == 4 else [int(x) for x in g.multinomial(rows, [0.25] * 4)]
+        lens = [int(x) for x in g.integers(0, 400, 4)]
+        n.copy_(torch.tensor(lens, dtype=torch.int32))
+        qs.copy_(torch.from_numpy(np.concatenate([[0], np.cumsum(t)]).astype(np.int32)))
+        q.copy_(torch.randn(rows, 4, 64, generator=torch.Generator().manual_seed(step)).to(dtype))
+        out.fill_(float("nan"))
+        graph.replay()
+        check_cross(c, t, lens, q, out, spare=0)
+        assert ca.device_status() == 0
