@@ -262,28 +262,29 @@ fastocr_status fastocr_cross_attend(fastocr_handle* h, const void* q, const fast
   if (!units_fit(h, rows, h->dims.batch)) return FASTOCR_ERR_UNSUPPORTED;
   if ((st = check_device(h)) != FASTOCR_OK) return st;
   if (rows == 0) return FASTOCR_OK;
+  // A decode step has one query token a sequence, or none. Those go to the split-K
+  // attend kernel, a token a unit, whose small tiles keep more of the states in
+  // flight (16 sequences, 10 heads, up to 2624 states: 32 us, row kernel and merge
+  // 46; two tokens in every other sequence 26 us and 32). Only the number of rows
+  // is known here, so tokens of one sequence may come this way too and read its
+  // states from L2 again: all 16 in one sequence, 8320 states, 23 us and 18.
+  if (rows <= h->dims.batch) {
+    Params a = base_params(h, q, kv, out);
+    a.q_start = q_start;
+    a.q_rows = (int)rows;
+    return launch(h, kCross, expected_tokens(h), a, stream);
+  }
   p.out = out;
   p.n_groups = h->dims.batch;
   p.start = q_start;
   p.rows = (int)rows;
-  p.tile_tokens = choose_tile_tokens(h, rows, std::min<int64_t>(p.n_groups, rows), expected_tokens(h));
+  p.tile_tokens = choose_tile_tokens(h, rows, p.n_groups, expected_tokens(h));
   p.min_share = choose_share(h, rows, expected_tokens(h));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // A decode step has one query token a sequence: those go to the split-K attend
-  // kernel, whose small tiles keep more of the states in flight (16 sequences, 10
-  // heads, 2624 states: 36 us against 46 us). Where there can be
-  // such sequences and others, both kernels run and each leaves the other's alone;
-  // the row kernel finds out while the kernel before it ends.
-  const bool single = rows <= p.n_groups;
-  p.skip_tokens = single ? 1 : 0;
   if ((st = launch_rows(h, p, s)) != FASTOCR_OK) return st;
-  if (launch_rows_merge(h->dims.head_dim, h->dims.dtype == FASTOCR_DTYPE_BF16, h->num_sms, p, s) != cudaSuccess)
-    return FASTOCR_ERR_CUDA;
-  if (!single) return FASTOCR_OK;
-  Params a = base_params(h, q, kv, out);
-  a.q_start = q_start;
-  a.q_rows = (int)rows;
-  return launch(h, kCross, expected_tokens(h), a, stream);
+  return launch_rows_merge(h->dims.head_dim, h->dims.dtype == FASTOCR_DTYPE_BF16, h->num_sms, p, s) == cudaSuccess
+             ? FASTOCR_OK
+             : FASTOCR_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -279,6 +279,27 @@ struct CtaList {
   int img_start, n_img;
 };
 
+// Cross: the sequence of query token `row` in a packed q, which is the number of
+// sequences that end at or before it; -1: none has it. Offsets out of order are
+// reported, and no token has a sequence then. Warp-uniform.
+__device__ __forceinline__ int sequence_of_token(const Params& p, int row) {
+  const int lane = threadIdx.x & 31;
+  bool mine = false, disordered = false;
+  int b = 0;
+  for (int i0 = 0; i0 < p.B; i0 += 32) {
+    const int i = i0 + lane;
+    const int s = i < p.B ? __ldcg(p.q_start + i) : 0, e = i < p.B ? __ldcg(p.q_start + i + 1) : 0;
+    disordered |= e < s || e > p.q_rows || (i == 0 && s != 0);
+    mine |= i < p.B && s <= row && row < e;
+    b += __popc(__ballot_sync(0xffffffffu, i < p.B && e <= row));
+  }
+  if (__any_sync(0xffffffffu, disordered)) {
+    if (threadIdx.x == 0) atomicOr(p.status, kDevBadGroup);
+    return -1;
+  }
+  return __any_sync(0xffffffffu, mine) ? b : -1;
+}
+
 template <int MODE>
 __device__ __forceinline__ CtaList make_cta_list(const Params& p, int b, int split, int& bad) {
   CtaList c;
@@ -386,8 +407,16 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
   constexpr int CH = ROWB / 16;                 // 16-byte chunks per row
   const float kNegInf = -CUDART_INF_F;
 
-  const int split = blockIdx.x, hkv = blockIdx.y, b = blockIdx.z;
+  const int split = blockIdx.x, hkv = blockIdx.y;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int q_row = blockIdx.z;   // row of q and out: the sequence, or cross: the query token
+  const int b = MODE == kCross ? sequence_of_token(p, q_row) : q_row;
+  if constexpr (MODE == kCross) {
+    if (b < 0) {   // a row behind the last sequence: the whole cluster's answer
+      asm volatile("griddepcontrol.wait;\n" ::: "memory");   // this grid may not end before the one before it
+      return;
+    }
+  }
   const T* __restrict__ kg = static_cast<const T*>(p.k);
   const T* __restrict__ vg = static_cast<const T*>(p.v);
   const int32_t* __restrict__ bt = p.block_table + (size_t)b * p.max_pages;
@@ -395,17 +424,6 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
   unsigned char* pipe = smem + warp * ST * SM::kStageBytes;
   int* srow = reinterpret_cast<int*>(smem + SM::kRowOffset);
   int* spos = reinterpret_cast<int*>(smem + SM::kPosOffset);
-
-  // row of q and out: the sequence, or its token of a packed q
-  int q_row = b;
-  if constexpr (MODE == kCross) {
-    const int s = __ldcg(p.q_start + b), e = __ldcg(p.q_start + b + 1);
-    if (s < 0 || e > p.q_rows || s >= e || e - s != 1) {   // none, or the row kernel's: the whole cluster's answer
-      asm volatile("griddepcontrol.wait;\n" ::: "memory");   // this grid may not end before the one before it
-      return;
-    }
-    q_row = s;
-  }
 
   // announce this CTA to its cluster (the partial exchange waits for it);
   // a single split has no partner and skips every cluster barrier
@@ -1476,7 +1494,7 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
 template <typename T, int D, int MODE, int V>
 cudaError_t launch_attend(const Params& p, cudaStream_t stream) {
   cudaLaunchAttribute attr[2];
-  cudaLaunchConfig_t cfg = pdl_config(dim3(p.splits, p.Hkv, p.B), dim3(32 * warps_for(V), 1, 1),
+  cudaLaunchConfig_t cfg = pdl_config(dim3(p.splits, p.Hkv, MODE == kCross ? p.q_rows : p.B), dim3(32 * warps_for(V), 1, 1),
                                       attend_smem_bytes<T, D, V>(), stream, attr);
   attr[1].id = cudaLaunchAttributeClusterDimension;   // the splits of one (b, hkv)
   attr[1].val.clusterDim.x = p.splits;

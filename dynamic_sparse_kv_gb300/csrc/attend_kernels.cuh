@@ -59,7 +59,7 @@ constexpr int kMaxImg = 16384; // image tokens whose scores fit in shared memory
 // to the profiler (a warm-up step whose selections are not kept): no logits,
 // no scores, no selection kernel.
 // kTail, kWeigh: the rows from `first` on (see Params). kCross: all rows, of which
-// there may be none, for sequences with one query token in a packed q.
+// there may be none, for each query token of a packed q.
 enum Mode : int { kFull = 0, kFocal = 1, kSparse = 2, kRswa = 3, kProfile = 4, kTail = 5, kWeigh = 6, kCross = 7 };
 // Modes whose epilogue turns stored logits into head-summed probabilities.
 __host__ __device__ constexpr bool stores_logits(int mode) { return mode == kFocal || mode == kWeigh; }

@@ -44,7 +44,6 @@ struct RowsParams {
   int rows;                   // query tokens
   int tile_tokens;            // tokens of a row tile
   int min_share;              // least key tiles of a share, where CTAs take shares
-  int skip_tokens;            // groups of this many tokens are another kernel's (0: none)
   // workspace
   int slot_rows;              // rows a slot holds
   float* slot_acc;            // [CTAs, 2, slot_rows, d]
@@ -81,7 +80,7 @@ __device__ __forceinline__ RowGroup load_group(const RowsParams& p, int i, int& 
   s = min(max(s, 0), p.rows);
   e = min(max(e, s), p.rows);
   r.first = s;
-  r.n_tok = e - s == p.skip_tokens ? 0 : e - s;
+  r.n_tok = e - s;
   r.table_row = p.prefix_len ? s : i;
   r.len = 0;
   if (r.n_tok > 0) {

@@ -356,7 +356,7 @@ fastocr_status fastocr_evict(fastocr_handle* h, const fastocr_kv* kv, const fast
  * rows * H_q < 2^31.
  * ws: as fastocr_shared_attend, fastocr_rows_workspace(h, rows) bytes. Overlap:
  * as the other calls; q_start and the states' K/V rows are read before the
- * preceding kernel completes. Two kernels, or three where rows <= B.
+ * preceding kernel completes. Two kernels, or one where rows <= B.
  * Errors: NULL, INVALID (rows, ws_bytes, another device current),
  * UNSUPPORTED, ALIGN, CUDA. */
 fastocr_status fastocr_cross_attend(fastocr_handle* h, const void* q, const fastocr_kv* kv,

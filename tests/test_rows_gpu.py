@@ -710,3 +710,23 @@ def test_cross_attention_captured(dtype, rows):
         graph.replay()
         check_cross(c, t, lens, q, out, spare=0)
         assert ca.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("heads", HEADS)
+@pytest.mark.parametrize("page,t,n", [
+    (16, [1, 1, 1, 1, 1], [700, 0, 1, 333, 128]),
+    (1, [0, 2, 0, 1], [5, 300, 7, 129]),
+    (256, [0, 0, 0, 3], [1, 1, 1, 513]),
+    (4, [1] + [0] * 39 + [30] + [0] * 30, [9] * 40 + [257] + [3] * 30),
+    (16, [0, 0], [20, 30]),
+])
+def test_cross_attention_of_no_more_tokens_than_sequences(dtype, heads, page, t, n):
+    from dynamic_sparse_kv_gb300 import CrossAttention
+    spare = len(t) - sum(t)
+    c, start, q = cross_case(t, n, heads, page, dtype, 22, spare)
+    ca = CrossAttention(c.k[None], c.v[None], c.gpu_table(), torch.tensor(n), q_heads=heads[0])
+    out = torch.full_like(q, 7.0)
+    ca.attend(0, q, start, out)
+    check_cross(c, t, n, q, out, spare)
+    assert ca.device_status() == 0
