@@ -48,7 +48,7 @@ struct RowsParams {
   int slot_rows;              // rows a slot holds
   float* slot_acc;            // [CTAs, 2, slot_rows, d]
   float* slot_ml;             // [CTAs, 2, slot_rows, 2]: max, sum
-  int4* token_part;           // shared: [rows, H_kv] where a token's parts are (TokenParts)
+  int4* token_part;           // shared: [rows, H_kv] where a token's parts are (see below)
   float* row_acc;             // shared: [rows, H_q, d], rows that one CTA has all keys of
   float* row_ml;              // shared: [rows, H_q, 2]
   int4* item_part;            // cross: [CTAs, 2] the cut item that starts in each CTA

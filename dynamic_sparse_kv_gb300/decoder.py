@@ -184,7 +184,7 @@ class DecodeAttention:
         [B], the same within a group). max_prefix: about the longest, for the
         split choice only; None takes it from prefix_len (which then
         synchronises, if it is on the device). Call it again when the groups
-        change; a CapturedStep must then be captured anew."""
+        change; a CapturedStep goes on with the groups it was captured with."""
         start = torch.as_tensor(group_start).to(torch.int32)
         if start.dim() != 1 or not 2 <= start.numel() <= self.batch + 1:
             raise ValueError("group_start must hold 2 .. B+1 offsets")
@@ -209,7 +209,8 @@ class DecodeAttention:
         mass, pos: [layers, B, H_kv, rows] fp32 / int32, seen: [B] int32, taken as
         they are if given (e.g. with a prompt's weights in them); otherwise
         no weight, every row at its own position, and the tokens of seq_len
-        (a prompt that is already in the cache). begin_token advances seen."""
+        (a prompt that is already in the cache). begin_token advances seen. A
+        CapturedStep goes on with the weights it was captured with."""
         if rows < 1:
             raise ValueError("rows must be at least 1")
         dev = self.k_cache.device
@@ -548,6 +549,8 @@ class CapturedStep:
                  launches: int | None = None, host_io: bool = False,
                  side_copy_bytes: int = 2 << 20):
         self.dec, self.kind = dec, kind
+        # the graph's own, should share_prefix or track_weights be called again
+        self._groups, self._weights = dec.groups, dec.weights
         self.side_copy_bytes = int(side_copy_bytes)
         shape = (dec.layers, dec.batch, dec.q_heads, dec.head_dim)
         self.q = torch.zeros(shape, dtype=dec.k_cache.dtype, device=dec.k_cache.device)

@@ -730,3 +730,25 @@ def test_cross_attention_of_no_more_tokens_than_sequences(dtype, heads, page, t,
     ca.attend(0, q, start, out)
     check_cross(c, t, n, q, out, spare)
     assert ca.device_status() == 0
+
+
+def test_captured_step_keeps_its_groups_and_weights():
+    """share_prefix and track_weights again after a capture: the graph's own tensors stay alive."""
+    from dynamic_sparse_kv_gb300 import CapturedStep
+    heads = (4, 2, 64)
+    c, start, prefix, n, q = shared_case([2, 1], [64, 20], [9, 11, 20], heads, 16, BF, 51)
+    dec = decoder(c, n, 4)
+    dec.share_prefix(start, torch.tensor(prefix))
+    dec.track_weights(64, torch.tensor(prefix))
+    step = CapturedStep(dec, "shared")
+    old = dec.weights["mass"]
+    dec.share_prefix([0, 1, 2, 3], 0)
+    dec.track_weights(256, 0)
+    junk = [torch.full((1 << 12,), -1, dtype=torch.int32, device="cuda") for _ in range(64)]
+    old.zero_()
+    step.q.copy_(q[None])
+    step.replay()
+    torch.cuda.synchronize()
+    check_shared(c, start, prefix, n, q, step.out[0])
+    assert old.sum() > 0 and dec.weights["mass"].sum() == 0
+    assert all((x == -1).all() for x in junk) and dec.device_status() == 0
