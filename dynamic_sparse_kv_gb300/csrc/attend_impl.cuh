@@ -392,6 +392,18 @@ __device__ __forceinline__ void add_selection(const Params& p, int k, int split,
   c.n_sel = max(0, min(per, k - c.sel_lo));
 }
 
+// Position of a row whose page is out of range: negative, so that it is masked.
+// Where logits are stored it keeps its place under the sign bit, and the row's
+// logits become -inf: the epilogue reads those of every row, and the scratch
+// holds an earlier layer's.
+template <int MODE>
+__device__ __forceinline__ int masked(int pos) {
+  return stores_logits(MODE) ? pos | (int)0x80000000 : -1;
+}
+// The place of position `pos` in the logits, masked or not; padding (-1) lies
+// behind every row.
+__device__ __forceinline__ int logit_pos(int pos) { return pos & 0x7fffffff; }
+
 // V: the kernel variant (warps per CTA and cp.async stages per warp).
 template <typename T, int D, int MODE, int V>
 __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kernel(const Params p) {
@@ -506,7 +518,7 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
       if (ps >= 0) {
         if (page[j] < 0 || page[j] >= p.num_pages) {
           bad |= kDevBadPage;
-          ps = -1;
+          ps = masked<MODE>(ps);
         } else {
           row = ((page[j] * p.Hkv + hkv) << p.log2_page) | (ps & page_mask);
         }
@@ -617,7 +629,7 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
       if (ps >= 0) {
         if (tpage[j] < 0 || tpage[j] >= p.num_pages) {
           bad |= kDevBadPage;
-          ps = -1;
+          ps = masked<MODE>(ps);
         } else {
           row = ((tpage[j] * p.Hkv + hkv) << p.log2_page) | (ps & page_mask);
         }
@@ -658,7 +670,7 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
         prefetch_l2(vg + (size_t)row * D, ROWB);
       } else {
         bad |= kDevBadPage;
-        ps = -1;
+        ps = masked<MODE>(ps);
       }
       srow[n_pre] = row;
       spos[n_pre] = ps;
@@ -857,11 +869,12 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
     const float s2 = posB >= 0 ? cfr[2] * p.scale_log2 : kNegInf;
     const float s3 = posB >= 0 ? cfr[3] * p.scale_log2 : kNegInf;
     if (stores_logits(MODE)) {
-      if (posA >= c.img_start && posA < c.img_start + c.n_img)
-        *reinterpret_cast<float2*>(logit_base + (size_t)(posA - c.img_start) * kSlots + 2 * tig) =
+      const int atA = logit_pos(posA), atB = logit_pos(posB);
+      if (atA >= c.img_start && atA < c.img_start + c.n_img)
+        *reinterpret_cast<float2*>(logit_base + (size_t)(atA - c.img_start) * kSlots + 2 * tig) =
             make_float2(s0, s1);
-      if (posB >= c.img_start && posB < c.img_start + c.n_img)
-        *reinterpret_cast<float2*>(logit_base + (size_t)(posB - c.img_start) * kSlots + 2 * tig) =
+      if (atB >= c.img_start && atB < c.img_start + c.n_img)
+        *reinterpret_cast<float2*>(logit_base + (size_t)(atB - c.img_start) * kSlots + 2 * tig) =
             make_float2(s2, s3);
     }
     // Online softmax with a lazily moved running max (base-2 logits): the
@@ -1013,8 +1026,9 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
           s[h] = pos >= 0 ? s[h] * p.scale_log2 : kNegInf;
         }
         if (stores_logits(MODE)) {
-          if (half == 0 && pos >= c.img_start && pos < c.img_start + c.n_img) {
-            float* dst = logit_base + (size_t)(pos - c.img_start) * kSlots;
+          const int at = logit_pos(pos);
+          if (half == 0 && at >= c.img_start && at < c.img_start + c.n_img) {
+            float* dst = logit_base + (size_t)(at - c.img_start) * kSlots;
             *reinterpret_cast<float4*>(dst) = make_float4(s[0], s[1], s[2], s[3]);
             *reinterpret_cast<float4*>(dst + 4) = make_float4(s[4], s[5], s[6], s[7]);
           }
