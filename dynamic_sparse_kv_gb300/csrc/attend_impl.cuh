@@ -1096,7 +1096,7 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
                       : (size_t)(2 * (ext.x + s) + (s == 0 ? ext.z : 0)) * p.ext_slot_rows + ext.w + h;
   };
   if constexpr (kExternal) {
-    // a sequence in no group has no parts, whatever an earlier call left there
+    // a sequence in no group has no parts (publish_none)
     if (p.ext_part) {
       if (ext.y >= 1 && ext.y <= kMaxExt && ext.x >= 0 && ext.x <= p.ext_ctas - ext.y &&
           (ext.z & ~1) == 0 && ext.w >= 0 && ext.w <= p.ext_slot_rows - p.g)

@@ -178,10 +178,11 @@ __device__ __forceinline__ bool take_units(int all, Walk& w) {
 // Where this CTA's units are; called by all THREADS threads. False: it has none.
 // Offsets out of order leave all CTAs without work: groups would share rows, and
 // their units could be more than 32 bits count.
+// faulty: the offsets or lengths are, so some tokens may be in no group.
 // Up to 32 groups every warp works it out for itself, without a barrier (every
 // call starts with this: 2 us through barriers, about 1 us without).
 template <int THREADS>
-__device__ __forceinline__ bool plan_walk(const RowsParams& p, PlanSmem& s, Walk& w, int& bad) {
+__device__ __forceinline__ bool plan_walk(const RowsParams& p, PlanSmem& s, Walk& w, bool& faulty, int& bad) {
   constexpr int NW = THREADS / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   auto warp_prefix = [&](int x) {
@@ -195,6 +196,7 @@ __device__ __forceinline__ bool plan_walk(const RowsParams& p, PlanSmem& s, Walk
   };
   RowGroup grp = {0, 0, 0, 0};
   bool disordered = false;
+  faulty = false;
   if (p.n_groups <= 32) {
     int sum = 0, items = 0, most = 0;
     if (lane < p.n_groups) {
@@ -203,7 +205,8 @@ __device__ __forceinline__ bool plan_walk(const RowsParams& p, PlanSmem& s, Walk
       items = group_items(p, grp);
       most = grp.n_tok > 0 ? key_tiles(grp.len) : 0;
     }
-    if (__any_sync(0xffffffffu, disordered)) return false;
+    faulty = __any_sync(0xffffffffu, bad & kDevBadGroup);
+    if (faulty && __any_sync(0xffffffffu, disordered)) return false;
     choose_share(p, __reduce_add_sync(0xffffffffu, sum), __reduce_add_sync(0xffffffffu, items),
                  __reduce_max_sync(0xffffffffu, most), w);
     if (w.share > 0) sum = group_units(p, grp, w.share);   // 0 for a lane without a group
@@ -227,7 +230,8 @@ __device__ __forceinline__ bool plan_walk(const RowsParams& p, PlanSmem& s, Walk
     items += group_items(p, grp);
     most = max(most, grp.n_tok > 0 ? key_tiles(grp.len) : 0);
   }
-  if (__syncthreads_or(disordered)) return false;
+  faulty = __syncthreads_or(bad & kDevBadGroup);
+  if (faulty && __syncthreads_or(disordered)) return false;
   // units before this thread, and of all
   int mine, all;
   auto scan = [&](int x, int* warp_sum) {
@@ -323,6 +327,23 @@ __device__ __forceinline__ void publish_parts(const RowsParams& p, const Segment
   if (!p.token_part || !s.starts) return;
   for (int i = t; i < s.n_rows / p.g; i += n)
     p.token_part[(size_t)(s.tok0 + i) * p.Hkv + s.hkv] = make_int4(blockIdx.x, s.parts, s.slot, i * p.g);
+}
+
+// A token that no group has gets no parts, so that the tail's attend kernel does not
+// join what an earlier call left there. For `n` threads of CTA 0, of which this is
+// number `t`, after its wait: the kernel before may read the workspace. Without any
+// work in CTA 0 (no_work) no token is in a group, else those from the first offset to
+// the last are.
+__device__ __forceinline__ void publish_none(const RowsParams& p, bool no_work, int t, int n) {
+  if (!p.token_part || blockIdx.x != 0) return;
+  int s = p.rows, e = p.rows;
+  if (!no_work) {
+    s = min(max(__ldcg(p.start), 0), p.rows);
+    e = min(max(__ldcg(p.start + p.n_groups), s), p.rows);
+  }
+  s *= p.Hkv;
+  e *= p.Hkv;
+  for (int i = t; i < s + p.rows * p.Hkv - e; i += n) p.token_part[i < s ? i : i - s + e] = make_int4(0, 0, 0, 0);
 }
 
 // Tells merge_kernel the cut item that starts in this CTA (cross attention):

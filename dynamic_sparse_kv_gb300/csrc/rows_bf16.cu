@@ -67,7 +67,8 @@ struct SmemBf16 {
   static constexpr int kNumBars = 2 * kStages + 2 + 5 * 2;
   static constexpr int kTmem = kBar + kNumBars * 8;
   static constexpr int kDead = kTmem + 4;
-  static constexpr int kBytes = kDead + 4;
+  static constexpr int kFaulty = kDead + 4;          // see plan_walk
+  static constexpr int kBytes = kFaulty + 4;
 };
 static_assert(SmemBf16<128>::kBytes <= 227 * 1024, "shared memory of one CTA");
 
@@ -241,13 +242,16 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsParams p) {
   Walk* walk = reinterpret_cast<Walk*>(smem + S::kWalk) + min(warp, 12);
   {
     Walk w;
-    if (!plan_walk<kThreads>(p, *reinterpret_cast<PlanSmem*>(smem), w, bad)) {
+    bool faulty;
+    if (!plan_walk<kThreads>(p, *reinterpret_cast<PlanSmem*>(smem), w, faulty, bad)) {
       asm volatile("griddepcontrol.wait;\n" ::: "memory");
+      publish_none(p, true, tid, kThreads);
       if (p.item_part && tid == 0) publish_no_cut(p);
       if (bad) atomicOr(p.status, bad);
       return;
     }
     if (lane == 0 && warp < 13) *walk = w;
+    if (tid == 0) *reinterpret_cast<int*>(smem + S::kFaulty) = faulty;
   }
 
   // barriers: ring full / empty, Q, O read, then per turn: S full, P ready (two
@@ -747,6 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsParams p) {
   tc_fence_before();
   __syncthreads();
   if (tid == 0 && *dead) atomicOr(p.status, kDevInternal);
+  if (*reinterpret_cast<const int*>(smem + S::kFaulty)) publish_none(p, false, tid, kThreads);
   if (warp == 12)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem));
 }

@@ -53,11 +53,13 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsParams p) {
   int* rows = reinterpret_cast<int*>(sm + S::kRow);
   int bad = 0;
   Walk walk;
-  const bool work = plan_walk<kThreads>(p, plan, walk, bad);
+  bool faulty;
+  const bool work = plan_walk<kThreads>(p, plan, walk, faulty, bad);
   // the kernel before may still write q or read the workspace; the next one
   // reads this one's output after its own wait
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  if (faulty || !work) publish_none(p, !work, tid, kThreads);
   bool cut = false;
   Segment seg;
   while (work && next_segment(p, walk, seg)) {

@@ -296,7 +296,9 @@ int64_t fastocr_rows_workspace(const fastocr_handle* h, int64_t rows);
  * size (entries of the other sequences' tables for whole prefix pages are not
  * read). prefix_len[b] <= N_t of every sequence of the group; a longer one is
  * reported as FASTOCR_DEV_BAD_GROUP and clamped. Offsets in start that do not
- * ascend from 0 to B are reported the same way; the output is then unspecified.
+ * ascend from 0 to B are reported the same way: a sequence outside [start[0],
+ * start[n]), or every one if they are out of order, then attends to its rows
+ * from prefix_len on alone.
  * weights: NULL, or accumulates weights like fastocr_weigh_attend (needs
  * protect[b] >= prefix_len[b]).
  * ws: device, 16-byte aligned, caller-owned, fastocr_rows_workspace(h, 0) bytes.
