@@ -522,10 +522,13 @@ class CapturedStep:
     scoring, selection and profile accumulation in every layer),
     "profile_mass" (an earlier step of the window: full attention and
     profile accumulation only), "rswa", "shared" (share_prefix) or "weighed"
-    (track_weights; each replay adds the step's weights, and so does the warm
-    run before the capture); or any name with `fn`, a
+    (track_weights); or any name with `fn`, a
     callable fn(q, out, stream) that issues the calls (e.g. a subset of the
     step's layers), and `launches`, the kernels it launches.
+
+    The step runs once, on zero queries, before it is captured. The rows'
+    weights and positions are put back after that run, so only replays add to
+    them; what a callable of the caller's own does in it stays.
 
     host_io=True (step kinds only) adds page-locked host buffers q_host and
     out_host, and the graph itself moves the step's queries in and its
@@ -563,6 +566,9 @@ class CapturedStep:
             self.out_host = torch.zeros(shape, dtype=self.q.dtype, pin_memory=True)
         if kind in ("profile", "profile_mass") and dec.warm_idx is None:
             dec.begin_warmup()
+        kept = {}   # what the warm run may not change
+        if fn is None and kind in ("shared", "weighed") and dec.weights is not None:
+            kept = {x: dec.weights[x] for x in ("mass", "pos")}
         if fn is None:   # otherwise fn(q, out, stream) issues the calls and `launches` counts them
             fn = {"fastocr": dec.step, "dense": dec.dense_step, "rswa": dec.rswa_step,
                   "shared": dec.shared_step, "weighed": dec.weighed_step,
@@ -573,7 +579,10 @@ class CapturedStep:
         side = torch.cuda.Stream()
         side.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(side):
+            saved = {x: t.clone() for x, t in kept.items()}
             fn(self.q, self.out)             # warm run outside the capture
+            for x, t in kept.items():
+                t.copy_(saved[x])
         torch.cuda.current_stream().wait_stream(side)
         self.graph = torch.cuda.CUDAGraph()
         if host_io:
