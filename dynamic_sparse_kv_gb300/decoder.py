@@ -31,6 +31,7 @@ This module only sequences library calls; all arithmetic is in the kernels.
 from __future__ import annotations
 
 import math
+import weakref
 
 import torch
 
@@ -94,6 +95,10 @@ class ProfileSchedule:
         return pos if pos < self.window else -1
 
 
+class _Weights(dict):
+    """What track_weights made; a dict that can be held weakly."""
+
+
 class DecodeAttention:
     """Decode attention of a stack of layers over a paged KV cache.
 
@@ -146,6 +151,7 @@ class DecodeAttention:
                                   device=dev) if score_reduce is not None else None)
         self.groups = None     # share_prefix
         self.weights = None    # track_weights
+        self._tracked = []     # weak references to all weights still in use, captured steps' among them
 
     def close(self):
         if self.handle:
@@ -210,7 +216,8 @@ class DecodeAttention:
         they are if given (e.g. with a prompt's weights in them); otherwise
         no weight, every row at its own position, and the tokens of seq_len
         (a prompt that is already in the cache). begin_token advances seen. A
-        CapturedStep goes on with the weights it was captured with."""
+        CapturedStep goes on with the weights it was captured with, whose seen
+        begin_token advances too."""
         if rows < 1:
             raise ValueError("rows must be at least 1")
         dev = self.k_cache.device
@@ -228,17 +235,19 @@ class DecodeAttention:
             if tuple(x.shape) != want or x.dtype != dt or x.device != dev or not x.is_contiguous():
                 raise ValueError(f"need a contiguous {dt} tensor of shape {want} on {dev}")
         logits = torch.empty((self.batch, self.kv_heads, rows, 8), dtype=torch.float32, device=dev)
-        self.weights = {"mass": mass, "pos": pos, "seen": seen, "protect": protect,
-                        "logits": logits, "new_len": torch.zeros_like(self.seq_len),
-                        "c": [N.make_weights(mass[l], pos[l], protect, seen, logits)
-                              for l in range(self.layers)]}
+        self.weights = _Weights(mass=mass, pos=pos, seen=seen, protect=protect, logits=logits,
+                                new_len=torch.zeros_like(self.seq_len),
+                                c=[N.make_weights(mass[l], pos[l], protect, seen, logits)
+                                   for l in range(self.layers)])
+        self._tracked = [r for r in self._tracked if r() is not None] + [weakref.ref(self.weights)]
 
     def begin_token(self):
         """One more token in every sequence: N_t and, with weights, seen go up by
         one (on the device; write its K/V to row N_t - 1)."""
         self.seq_len.add_(1)
-        if self.weights:
-            self.weights["seen"].add_(1)
+        seen = [w["seen"] for w in (r() for r in self._tracked) if w is not None]
+        for x in {t.data_ptr(): t for t in seen}.values():   # one counter may serve several
+            x.add_(1)
 
     def set_focal_layers(self, focal):
         self.focal = tuple(sorted(int(l) for l in focal))

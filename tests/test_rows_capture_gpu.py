@@ -50,3 +50,33 @@ def test_a_capture_leaves_the_weights_alone(kind, host_io):
     (dec.shared_step if kind == "shared" else dec.weighed_step)(q[None], out)
     assert torch.equal(dec.weights["mass"], once) and torch.equal(dec.weights["pos"], where)
     assert torch.equal(step.out, out) and dec.device_status() == 0
+
+
+def test_begin_token_advances_the_weights_of_every_captured_step():
+    """An old capture goes on with its own weights, so the positions it writes must go on too."""
+    from dynamic_sparse_kv_gb300 import CapturedStep
+    dec, q = tracked()
+    step = CapturedStep(dec, "shared")
+    old = dec.weights
+    dec.track_weights(64, 20)
+    new = dec.weights
+    first, second = old["seen"].tolist(), new["seen"].tolist()
+    for t in range(1, 4):
+        dec.begin_token()
+        assert old["seen"].tolist() == [x + t for x in first]
+        assert new["seen"].tolist() == [x + t for x in second]
+        step.q.copy_(q[None])
+        step.replay()
+        for b, n in enumerate(dec.seq_len.tolist()):
+            assert (old["pos"][0, b, :, n - 1 - 20] == first[b] + t - 1).all()
+    # one counter given to both is advanced once, and weights that no step holds not at all
+    del step
+    loose = old["seen"]
+    del old
+    shared = new["seen"]
+    keep = CapturedStep(dec, "weighed")
+    dec.track_weights(64, 20, seen=shared)
+    was, out_of_use = shared.tolist(), loose.tolist()
+    dec.begin_token()
+    assert shared.tolist() == [x + 1 for x in was] and loose.tolist() == out_of_use
+    assert keep.launches == 1 and dec.device_status() == 0
