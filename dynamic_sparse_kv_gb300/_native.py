@@ -124,6 +124,14 @@ def _check(fn: str, status: int) -> None:
         raise FastOCRError(fn, status)
 
 
+def check_tensor(t, name, shape, dtype, device) -> None:
+    """Refuse a tensor that the library would read or write wrongly: it gets the bare address."""
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                         f"{device}, not {t.dtype} {tuple(t.shape)} on {t.device}"
+                         + ("" if t.is_contiguous() else f" with strides {t.stride()}"))
+
+
 def _ptr(t):
     if t is None:
         return None

@@ -53,18 +53,14 @@ class CrossAttention:
             pass
 
     def attend(self, l, q, q_start, out, stream=None):
-        """Layer l: q, out [rows, H_q, d] contiguous; q_start [B + 1] int32 on the
-        device, query tokens q_start[b] .. q_start[b+1]-1 are sequence b's."""
-        rows = q.shape[0]
-        if tuple(q.shape[1:]) != (self.q_heads, self.head_dim) or out.shape != q.shape:
-            raise ValueError(f"q and out must be [rows, {self.q_heads}, {self.head_dim}]")
-        if not (q.is_contiguous() and out.is_contiguous()):
-            raise ValueError("q and out must be contiguous")
-        if q.dtype != self.k_cache.dtype or out.dtype != q.dtype:
-            raise ValueError(f"q and out must be {self.k_cache.dtype}")
-        if tuple(q_start.shape) != (self.batch + 1,) or q_start.dtype != torch.int32 \
-                or not q_start.is_cuda:
-            raise ValueError(f"q_start must be int32 [{self.batch + 1}] on the device")
+        """Layer l: q, out [rows, H_q, d]; q_start [B + 1] int32, query tokens
+        q_start[b] .. q_start[b+1]-1 are sequence b's. All contiguous and on the
+        caches' device."""
+        rows, dev = q.shape[0], self.k_cache.device
+        shape = (rows, self.q_heads, self.head_dim)
+        N.check_tensor(q, "q", shape, self.k_cache.dtype, dev)
+        N.check_tensor(out, "out", shape, self.k_cache.dtype, dev)
+        N.check_tensor(q_start, "q_start", (self.batch + 1,), torch.int32, dev)
         if rows == 0:
             return
         N.fastocr_cross_attend(self.handle, q, self.kv[l], q_start, rows, out, self.ws,

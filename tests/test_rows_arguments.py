@@ -1,0 +1,51 @@
+"""Tensors that the library would read or write wrongly are refused before any call of it:
+wrong shape, type, strides or device. The library itself is replaced, so no GPU is needed."""
+import pytest
+import torch
+
+BF = torch.bfloat16
+
+
+@pytest.fixture()
+def calls(monkeypatch):
+    """Names of the library calls made."""
+    from conftest import build_library
+    build_library()
+    from dynamic_sparse_kv_gb300 import _native
+    made = []
+    for name in ("cross_attend", "shared_attend", "weigh_attend", "evict"):
+        monkeypatch.setattr(_native, "fastocr_" + name, lambda *args, name=name, **kw: made.append(name))
+    return made
+
+
+def spread(t):
+    """The same values at other strides."""
+    return torch.stack([t, t + 1], dim=-1)[..., 0]
+
+
+def cross():
+    from dynamic_sparse_kv_gb300 import CrossAttention
+    ca = object.__new__(CrossAttention)
+    ca.k_cache = ca.v_cache = torch.zeros(1, 4, 2, 16, 64, dtype=BF)
+    ca.batch, ca.q_heads, ca.head_dim, ca.kv = 3, 4, 64, [None]
+    ca.handle, ca.ws = None, torch.zeros(1, dtype=torch.uint8)
+    return ca
+
+
+def test_cross_attention_refuses_what_it_would_read_wrongly(calls):
+    ca = cross()
+    q = torch.zeros(5, 4, 64, dtype=BF)
+    start = torch.tensor([0, 2, 2, 5], dtype=torch.int32)
+    ca.attend(0, q, start, torch.empty_like(q))
+    assert calls == ["cross_attend"]
+    for bad in (spread(start), torch.zeros(1, dtype=torch.int32).expand(4), start.long(), start[:3],
+                start.view(2, 2), start.to("meta")):
+        with pytest.raises(ValueError, match="q_start"):
+            ca.attend(0, q, bad, torch.empty_like(q))
+    for bad in (spread(q), q.float(), q[:, :3], q.to("meta"), q[:, :1].expand(5, 4, 64), q.transpose(0, 1)):
+        with pytest.raises(ValueError, match="q must"):
+            ca.attend(0, bad, start, torch.empty(bad.shape, dtype=BF))
+    for bad in (spread(q), q.float(), q[:4], q.to("meta"), q[:1].expand(5, 4, 64)):
+        with pytest.raises(ValueError, match="out must"):
+            ca.attend(0, q, start, bad)
+    assert calls == ["cross_attend"]
