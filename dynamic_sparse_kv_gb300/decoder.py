@@ -489,6 +489,8 @@ class DecodeAttention:
         (evict_step copies new_len) must run before the layer attends again."""
         if self.weights is None:
             raise RuntimeError("track_weights has not been called")
+        if new_len is not None:
+            N.check_tensor(new_len, "new_len", (self.batch,), torch.int32, self.k_cache.device)
         N.fastocr_evict(self.handle, self.kv[l], self.weights["c"][l], budget, recent, new_len,
                         stream)
 

@@ -49,3 +49,26 @@ def test_cross_attention_refuses_what_it_would_read_wrongly(calls):
         with pytest.raises(ValueError, match="out must"):
             ca.attend(0, q, start, bad)
     assert calls == ["cross_attend"]
+
+
+def decoder():
+    from dynamic_sparse_kv_gb300 import DecodeAttention
+    dec = object.__new__(DecodeAttention)
+    dec.k_cache = dec.v_cache = torch.zeros(1, 4, 2, 16, 64, dtype=BF)
+    dec.layers, dec.batch, dec.q_heads, dec.head_dim, dec.kv = 1, 3, 4, 64, [None]
+    dec.handle = None
+    dec.groups = {"c": None, "ws": torch.zeros(1, dtype=torch.uint8)}
+    dec.weights = {"c": [None]}
+    return dec
+
+
+def test_evict_refuses_lengths_it_would_write_wrongly(calls):
+    dec = decoder()
+    good = torch.zeros(3, dtype=torch.int32)
+    dec.evict_layer(0, 2, 1)
+    dec.evict_layer(0, 2, 1, good)
+    assert calls == ["evict"] * 2
+    for bad in (good.long(), good[:2], spread(good), good[:1].expand(3), good.to("meta"), good.view(3, 1)):
+        with pytest.raises(ValueError, match="new_len"):
+            dec.evict_layer(0, 2, 1, bad)
+    assert calls == ["evict"] * 2
