@@ -449,12 +449,18 @@ class DecodeAttention:
             if hook:
                 hook(l, False)
 
+    def _check_layer(self, q_l, out_l):
+        shape = (self.batch, self.q_heads, self.head_dim)
+        N.check_tensor(q_l, "q", shape, self.k_cache.dtype, self.k_cache.device)
+        N.check_tensor(out_l, "out", shape, self.k_cache.dtype, self.k_cache.device)
+
     def shared_layer(self, l, q_l, out_l, stream=None):
         """Layer l of a step over shared prefixes (share_prefix); adds the rows'
-        weights if they are tracked."""
+        weights if they are tracked. q_l, out_l: [B, H_q, d], contiguous."""
         g = self.groups
         if g is None:
             raise RuntimeError("share_prefix has not been called")
+        self._check_layer(q_l, out_l)
         N.fastocr_shared_attend(self.handle, q_l, self.kv[l], g["c"], out_l, g["ws"],
                                 g["ws"].numel(), self.weights["c"][l] if self.weights else None,
                                 stream)
@@ -469,9 +475,11 @@ class DecodeAttention:
                 hook(l, False)
 
     def weigh_layer(self, l, q_l, out_l, stream=None):
-        """Layer l of a step that adds every row's attention weight."""
+        """Layer l of a step that adds every row's attention weight. q_l, out_l:
+        [B, H_q, d], contiguous."""
         if self.weights is None:
             raise RuntimeError("track_weights has not been called")
+        self._check_layer(q_l, out_l)
         N.fastocr_weigh_attend(self.handle, q_l, self.kv[l], self.weights["c"][l], out_l, stream)
 
     def weighed_step(self, q, out, stream=None, hook=None):

@@ -72,3 +72,24 @@ def test_evict_refuses_lengths_it_would_write_wrongly(calls):
         with pytest.raises(ValueError, match="new_len"):
             dec.evict_layer(0, 2, 1, bad)
     assert calls == ["evict"] * 2
+
+
+@pytest.mark.parametrize("kind", ["shared", "weigh"])
+def test_shared_and_weighed_layers_refuse_what_they_would_read_wrongly(calls, kind):
+    dec = decoder()
+    layer = dec.shared_layer if kind == "shared" else dec.weigh_layer
+    step = dec.shared_step if kind == "shared" else dec.weighed_step
+    good = torch.zeros(3, 4, 64, dtype=BF)
+    layer(0, good, torch.empty_like(good))
+    step(good[None], torch.empty_like(good)[None])
+    assert calls == [kind + "_attend"] * 2
+    of_all = torch.zeros(3, 2, 4, 64, dtype=BF)          # [B, L, H_q, d]: a layer of it is strided
+    for bad in (of_all[:, 0], good.float(), good[:2], good[:, :3], good.to("meta"), good.view(3, 256),
+                good[:1].expand(3, 4, 64), good.transpose(0, 1)):
+        with pytest.raises(ValueError, match="q must"):
+            layer(0, bad, good)
+        with pytest.raises(ValueError, match="out must"):
+            layer(0, good, bad)
+    with pytest.raises(ValueError):
+        step(of_all.transpose(0, 1), torch.empty(2, 3, 4, 64, dtype=BF))
+    assert calls == [kind + "_attend"] * 2
