@@ -93,3 +93,14 @@ def test_shared_and_weighed_layers_refuse_what_they_would_read_wrongly(calls, ki
     with pytest.raises(ValueError):
         step(of_all.transpose(0, 1), torch.empty(2, 3, 4, 64, dtype=BF))
     assert calls == [kind + "_attend"] * 2
+
+
+def test_cross_attention_refuses_lengths_of_another_batch(calls):
+    from dynamic_sparse_kv_gb300 import CrossAttention
+    k = torch.zeros(1, 4, 2, 16, 64, dtype=BF)
+    table = torch.zeros(3, 2, dtype=torch.int32)
+    for lengths in (torch.zeros(2), torch.zeros(1), torch.zeros(4), torch.zeros(3, 1), torch.tensor(5)):
+        with pytest.raises(ValueError, match="state_len"):       # fewer were read past their end
+            CrossAttention(k, k, table, lengths, q_heads=4)
+    with pytest.raises(ValueError, match="block_table"):
+        CrossAttention(k, k, table[0], torch.zeros(2), q_heads=4)
