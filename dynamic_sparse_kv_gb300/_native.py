@@ -132,6 +132,18 @@ def check_tensor(t, name, shape, dtype, device) -> None:
                          + ("" if t.is_contiguous() else f" with strides {t.stride()}"))
 
 
+def check_caches(k, v) -> int:
+    """The dtype code of a stack's caches [layers, pages, H_kv, page, d]; refuses what the
+    kernels would read wrongly. Layers may lie apart, each must be contiguous."""
+    if k.dim() != 5 or k.shape != v.shape or k.dtype != v.dtype or k.device != v.device:
+        raise ValueError("k_cache and v_cache must be alike, [layers, pages, H_kv, page_size, d]")
+    if k.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"caches must be bfloat16 or float32, not {k.dtype}")
+    if not (k[0].is_contiguous() and v[0].is_contiguous()):
+        raise ValueError("a layer's cache must be contiguous")
+    return FASTOCR_DTYPE_BF16 if k.dtype == torch.bfloat16 else FASTOCR_DTYPE_F32
+
+
 def _ptr(t):
     if t is None:
         return None

@@ -28,14 +28,14 @@ class CrossAttention:
         if block_table.dim() != 2 or tuple(state_len.shape) != (self.batch,):
             raise ValueError(f"block_table must be [B, pages], state_len an int or [B], not "
                              f"{tuple(block_table.shape)} and {tuple(state_len.shape)}")
-        assert k_cache.is_cuda and k_cache.shape == v_cache.shape
+        dtype = N.check_caches(k_cache, v_cache)
+        assert k_cache.is_cuda
         self.k_cache, self.v_cache = k_cache, v_cache
         self.layers, _, self.kv_heads, self.page_size, self.head_dim = k_cache.shape
         self.q_heads = q_heads
         dev = k_cache.device
         self.block_table = block_table.to(device=dev, dtype=torch.int32).contiguous()
         self.state_len = state_len.to(device=dev, dtype=torch.int32).contiguous()
-        dtype = N.FASTOCR_DTYPE_BF16 if k_cache.dtype == torch.bfloat16 else N.FASTOCR_DTYPE_F32
         self.handle = N.fastocr_create(self.batch, q_heads, self.kv_heads, self.head_dim, dtype,
                                        self.page_size, self.block_table.shape[1], 0, self.layers)
         self.kv = [N.make_kv(k_cache[l], v_cache[l], self.block_table, self.state_len)

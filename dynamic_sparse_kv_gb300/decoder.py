@@ -110,7 +110,8 @@ class DecodeAttention:
                  max_img: int = 0, tau: float = 1.0, mode: str = "fastocr",
                  rswa_prefix: int = 0, rswa_window: int = 0, splits=None, variants=None,
                  score_reduce=None):
-        assert k_cache.is_cuda and k_cache.shape == v_cache.shape
+        dtype = N.check_caches(k_cache, v_cache)
+        assert k_cache.is_cuda
         self.k_cache, self.v_cache = k_cache, v_cache
         self.layers, self.num_pages, self.kv_heads, self.page_size, self.head_dim = k_cache.shape
         self.batch = block_table.shape[0]
@@ -123,7 +124,6 @@ class DecodeAttention:
         self.img_range = (img_range.to(device=dev, dtype=torch.int32).contiguous()
                           if img_range is not None else None)
         self.max_img = int(max_img)
-        dtype = N.FASTOCR_DTYPE_BF16 if k_cache.dtype == torch.bfloat16 else N.FASTOCR_DTYPE_F32
         self.handle = N.fastocr_create(self.batch, q_heads, self.kv_heads, self.head_dim, dtype,
                                        self.page_size, self.block_table.shape[1], self.max_img,
                                        self.layers)

@@ -104,3 +104,22 @@ def test_cross_attention_refuses_lengths_of_another_batch(calls):
             CrossAttention(k, k, table, lengths, q_heads=4)
     with pytest.raises(ValueError, match="block_table"):
         CrossAttention(k, k, table[0], torch.zeros(2), q_heads=4)
+
+
+def test_caches_of_other_types_and_strides_are_refused(calls):
+    from dynamic_sparse_kv_gb300 import CrossAttention, DecodeAttention
+    k = torch.zeros(2, 4, 2, 16, 64, dtype=BF)
+    table = torch.zeros(3, 2, dtype=torch.int32)
+    half = k.half()                              # was read as fp32, past its end
+    for kk, vv in ((half, half), (k, k.float()), (k.float(), k), (k, k[:, :3]), (k[0], k[0]),
+                   (k.transpose(1, 2), k.transpose(1, 2)), (k, spread(k)),
+                   (k[:, :1].expand(2, 4, 2, 16, 64), k), (k, k.to("meta"))):
+        with pytest.raises(ValueError):
+            CrossAttention(kk, vv, table, 5, q_heads=4)
+        with pytest.raises(ValueError):
+            DecodeAttention(kk, vv, table, q_heads=4)
+    for good in (k, k.float(), torch.zeros(2, 6, 2, 16, 64, dtype=BF)[:, :4]):
+        with pytest.raises(AssertionError):      # only for want of a GPU
+            CrossAttention(good, good, table, 5, q_heads=4)
+        with pytest.raises(AssertionError):
+            DecodeAttention(good, good, table, q_heads=4)
