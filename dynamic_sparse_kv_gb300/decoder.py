@@ -348,13 +348,18 @@ class DecodeAttention:
         return st
 
     def load_state_dict(self, st: dict, stream=None) -> None:
-        """Resume from state_dict() of a decoder over the same shapes and tau.
+        """Resume from state_dict() of a decoder over the same shapes and tau, and
+        with as many weighed rows if it has any (ValueError, and nothing changes).
         With the same focal set the selection buffers keep their addresses
         (a CapturedStep of this decoder stays valid); another focal set gets
         new buffers, so a step must then be captured anew."""
         for key in ("batch", "layers", "stride", "tau", "max_img"):
             if st[key] != getattr(self, key):
                 raise ValueError(f"checkpoint {key}={st[key]!r}, decoder has {getattr(self, key)!r}")
+        weights = st.get("weights")   # looked at before anything is changed
+        if weights is not None and (self.weights is None or any(self.weights[x].shape != t.shape
+                                                                for x, t in weights.items())):
+            raise ValueError("checkpoint has weights: call track_weights with as many rows first")
         if tuple(st["focal"]) != tuple(self.focal):
             if st["focal"]:
                 self.set_focal_layers(st["focal"])
@@ -363,12 +368,8 @@ class DecodeAttention:
         for l, (idx, k) in st["sel"].items():
             self.sel[l][0].copy_(idx)
             self.sel[l][1].copy_(k)
-        weights = st.get("weights")
-        if weights is not None:
-            if self.weights is None or self.weights["mass"].shape != weights["mass"].shape:
-                raise ValueError("checkpoint has weights: call track_weights with as many rows first")
-            for x, t in weights.items():
-                self.weights[x].copy_(t)
+        for x, t in (weights or {}).items():
+            self.weights[x].copy_(t)
         self.has_f_last = bool(st["has_f_last"])
         if st["warm"] is None:
             self.warm_idx = self.warm_k = None

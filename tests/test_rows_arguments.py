@@ -123,3 +123,20 @@ def test_caches_of_other_types_and_strides_are_refused(calls):
             CrossAttention(good, good, table, 5, q_heads=4)
         with pytest.raises(AssertionError):
             DecodeAttention(good, good, table, q_heads=4)
+
+
+def test_a_refused_checkpoint_changes_nothing(calls):
+    dec = decoder()
+    dec.stride, dec.tau, dec.max_img, dec.has_f_last = 4, 1.0, 8, False
+    dec.focal, dec.sel = (0,), {0: (torch.zeros(3, 4, dtype=torch.int32), torch.zeros(3, dtype=torch.int32))}
+    st = {"batch": 3, "layers": 1, "stride": 4, "tau": 1.0, "max_img": 8, "focal": (0,), "has_f_last": True,
+          "sel": {0: (torch.ones(3, 4, dtype=torch.int32), torch.ones(3, dtype=torch.int32))}, "warm": None,
+          "weights": {"mass": torch.ones(1, 3, 2, 5), "pos": torch.ones(1, 3, 2, 5, dtype=torch.int32)}}
+    small = {"mass": torch.zeros(1, 3, 2, 5), "pos": torch.zeros(1, 3, 2, 4, dtype=torch.int32)}
+    for have in (None, small):
+        dec.weights = have
+        for focal in ((0,), ()):
+            with pytest.raises(ValueError, match="track_weights"):
+                dec.load_state_dict({**st, "focal": focal, "sel": st["sel"] if focal else {}})
+            assert dec.focal == (0,) and not dec.sel[0][0].any() and not dec.has_f_last
+    assert not small["mass"].any()
