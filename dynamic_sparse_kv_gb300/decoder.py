@@ -510,11 +510,11 @@ class DecodeAttention:
         new_len = self.weights["new_len"]
         for l in range(self.layers):
             self.evict_layer(l, budget, recent, new_len if l == self.layers - 1 else None, stream)
-        if stream is None:
+        if isinstance(stream, int):   # 0 is the default stream, which ExternalStream does not know
+            dev = self.k_cache.device
+            stream = torch.cuda.ExternalStream(stream, dev) if stream else torch.cuda.default_stream(dev)
+        with torch.cuda.stream(stream):   # None: the current one
             self.seq_len.copy_(new_len)
-        else:
-            with torch.cuda.stream(stream):
-                self.seq_len.copy_(new_len)
 
     def launches_per_step(self, kind: str) -> int:
         """Kernels one step of `kind` launches: one attend kernel per layer,
