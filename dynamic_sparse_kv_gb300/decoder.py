@@ -149,6 +149,7 @@ class DecodeAttention:
         self.score_reduce = score_reduce
         self.sigma = (torch.zeros(self.batch, max(self.max_img, 1), dtype=torch.float32,
                                   device=dev) if score_reduce is not None else None)
+        self.hint = 0          # length the split choices assume (0: the cache's capacity)
         self.groups = None     # share_prefix
         self.weights = None    # track_weights
         self._tracked = []     # weak references to all weights still in use, captured steps' among them
@@ -165,12 +166,17 @@ class DecodeAttention:
             pass
 
     # ------------------------------------------------------------ set-up
+    def _set_hint(self, n):
+        self.hint = n
+        N.fastocr_set_length_hint(self.handle, n)
+
     def set_seq_len(self, n_t):
         """N_t of the current step, int (all sequences) or [B] tensor. An int
-        also becomes the handle's length hint (split choice only)."""
+        also becomes the handle's length hint (split choice only), which
+        begin_token and evict_step carry on."""
         if isinstance(n_t, int):
             self.seq_len.fill_(n_t)
-            N.fastocr_set_length_hint(self.handle, n_t)
+            self._set_hint(n_t)
         else:
             self.seq_len.copy_(n_t, non_blocking=True)
 
@@ -217,12 +223,14 @@ class DecodeAttention:
         no weight, every row at its own position, and the tokens of seq_len
         (a prompt that is already in the cache). begin_token advances seen. A
         CapturedStep goes on with the weights it was captured with, whose seen
-        begin_token advances too."""
+        begin_token advances too. A protect on the device is read back once."""
         if rows < 1:
             raise ValueError("rows must be at least 1")
         dev = self.k_cache.device
         shape = (self.layers, self.batch, self.kv_heads, rows)
+        given = protect
         protect = self._per_sequence(protect, "protect")
+        most = given if isinstance(given, int) else int(torch.as_tensor(given).max())
         if mass is None:
             mass = torch.zeros(shape, dtype=torch.float32, device=dev)
         if pos is None:
@@ -236,7 +244,7 @@ class DecodeAttention:
                 raise ValueError(f"need a contiguous {dt} tensor of shape {want} on {dev}")
         logits = torch.empty((self.batch, self.kv_heads, rows, 8), dtype=torch.float32, device=dev)
         self.weights = _Weights(mass=mass, pos=pos, seen=seen, protect=protect, logits=logits,
-                                new_len=torch.zeros_like(self.seq_len),
+                                new_len=torch.zeros_like(self.seq_len), most_protect=most,
                                 c=[N.make_weights(mass[l], pos[l], protect, seen, logits)
                                    for l in range(self.layers)])
         self._tracked = [r for r in self._tracked if r() is not None] + [weakref.ref(self.weights)]
@@ -245,6 +253,8 @@ class DecodeAttention:
         """One more token in every sequence: N_t and, with weights, seen go up by
         one (on the device; write its K/V to row N_t - 1)."""
         self.seq_len.add_(1)
+        if self.hint > 0:
+            self._set_hint(self.hint + 1)
         seen = [w["seen"] for w in (r() for r in self._tracked) if w is not None]
         for x in {t.data_ptr(): t for t in seen}.values():   # one counter may serve several
             x.add_(1)
@@ -515,6 +525,9 @@ class DecodeAttention:
             stream = torch.cuda.ExternalStream(stream, dev) if stream else torch.cuda.default_stream(dev)
         with torch.cuda.stream(stream):   # None: the current one
             self.seq_len.copy_(new_len)
+        left = max(1, self.weights["most_protect"] + budget)   # rows of the longest sequence, at most
+        if self.hint > left:
+            self._set_hint(left)
 
     def launches_per_step(self, kind: str) -> int:
         """Kernels one step of `kind` launches: one attend kernel per layer,
