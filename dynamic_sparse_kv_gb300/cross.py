@@ -18,10 +18,13 @@ class CrossAttention:
     block_table: [B, pages_per_seq] int32; state_len: int or [B] int32, states a
     sequence has (a device int32 tensor is taken as it is and may change).
     max_rows: query tokens of the largest call, for the workspace (None: any).
+    max_states: about the longest sequence's states, for the split choices only;
+    None takes it from state_len, or, where that is on the device, the capacity
+    of block_table.
     """
 
     def __init__(self, k_cache, v_cache, block_table, state_len, *, q_heads: int,
-                 max_rows: int | None = None):
+                 max_rows: int | None = None, max_states: int | None = None):
         self.batch = block_table.shape[0]
         if isinstance(state_len, int):
             state_len = torch.full((self.batch,), state_len, dtype=torch.int32)
@@ -40,6 +43,10 @@ class CrossAttention:
                                        self.page_size, self.block_table.shape[1], 0, self.layers)
         self.kv = [N.make_kv(k_cache[l], v_cache[l], self.block_table, self.state_len)
                    for l in range(self.layers)]
+        if max_states is None and not state_len.is_cuda:
+            max_states = int(state_len.max())
+        capacity = self.block_table.shape[1] * self.page_size
+        N.fastocr_set_length_hint(self.handle, min(max(0, max_states or 0), capacity))
         # the workspace stops growing where the rows of a sequence fill a row tile
         n = N.fastocr_rows_workspace(self.handle, max(1, 256 if max_rows is None else max_rows))
         self.ws = torch.empty(n, dtype=torch.uint8, device=dev)

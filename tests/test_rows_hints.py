@@ -39,3 +39,22 @@ def test_the_hint_of_a_decoder_follows_its_tokens(hints):
     dec.track_weights(64, 0)
     dec.evict_step(1, 0)
     assert hints[8:] == [1]
+
+
+def test_the_hint_of_cross_attention(hints, monkeypatch):
+    """From lengths on the host, or given; none for lengths on the device, which may change."""
+    from dynamic_sparse_kv_gb300 import CrossAttention, _native
+
+    class OnDevice(torch.Tensor):        # a host tensor that says it is on the device
+        is_cuda = True
+
+    monkeypatch.setattr(_native, "fastocr_create", lambda *args: 0)
+    monkeypatch.setattr(_native, "fastocr_rows_workspace", lambda *args: 16)
+    k = torch.zeros(1, 4, 2, 16, 64, dtype=BF).as_subclass(OnDevice)
+    table = torch.zeros(3, 2, dtype=torch.int32)
+    on_device = torch.tensor([5, 0, 9], dtype=torch.int32).as_subclass(OnDevice)
+    for state_len, most, want in ((7, None, 7), (0, None, 0), (torch.tensor([5, 0, 9]), None, 9), (on_device, None, 0),
+                                  (on_device, 12, 12), (torch.tensor([5, 0, 9]), 30, 30),
+                                  (torch.tensor([5, 1 << 40, -1]), None, 32)):
+        CrossAttention(k, k, table, state_len, q_heads=4, max_states=most)
+        assert hints[-1] == want
