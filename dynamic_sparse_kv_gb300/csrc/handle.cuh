@@ -56,10 +56,11 @@ inline int ilog2_exact(int x) {
 inline int slot_of(int mode) { return mode == kSparse ? 1 : (mode == kRswa ? 2 : 0); }
 
 // Kernel variant and split count of a launch whose attend lists hold about
-// `len` entries per (sequence, KV head) unit; caller overrides win.
+// `len` entries per (sequence, KV head) unit -- (query token, KV head) in cross
+// mode, which has p.q_rows of them; caller overrides win.
 inline void plan_launch(const fastocr_handle* h, int mode, long len, Params& p) {
   const int slot = slot_of(mode);
-  const long units = (long)h->dims.batch * h->dims.num_kv_heads;
+  const long units = (long)(mode == kCross ? p.q_rows : h->dims.batch) * h->dims.num_kv_heads;
   if (len < 1) len = 1;
   int v = h->variant_override[slot] - 1;   // -1: automatic
   int s = h->split_override[slot];         // 0: automatic
