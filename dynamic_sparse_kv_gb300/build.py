@@ -23,7 +23,8 @@ LIB = os.path.join(HERE, "libfastocr.so")
 
 SOURCES = ["abi.cu", "abi_rows.cu", "evict.cu", "kernels_bf16.cu", "kernels_f32.cu", "noalloc.cu",
            "probe.cu", "rows_bf16.cu", "rows_f32.cu"]
-HEADERS = ["attend_kernels.cuh", "attend_impl.cuh", "evict.cuh", "handle.cuh", "rows.cuh"]
+HEADERS = ["attend_kernels.cuh", "attend_impl.cuh", "evict.cuh", "handle.cuh", "rows.cuh",
+           "rows_plan.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -5,6 +5,7 @@
 #include "evict.cuh"
 #include "handle.cuh"
 #include "rows.cuh"
+#include "rows_plan.cuh"
 
 using namespace fastocr;
 
@@ -53,48 +54,6 @@ RowsParams rows_params(const fastocr_handle* h, const void* q, const fastocr_kv*
   return p;
 }
 
-// Most rows of a row tile, in whole tokens.
-int tile_rows(const fastocr_handle* h) {
-  const int bm = h->dims.dtype == FASTOCR_DTYPE_BF16 ? kRowsBf16 : kRowsF32;
-  const int g = h->dims.num_q_heads / h->dims.num_kv_heads;
-  return bm / g * g;
-}
-int64_t slot_rows(const fastocr_handle* h, int64_t rows) {
-  return std::min<int64_t>(tile_rows(h), rows * (h->dims.num_q_heads / h->dims.num_kv_heads));
-}
-
-// Tokens of a row tile. A bf16 tile of 256 rows reads each key once for all of
-// them, one of 128 twice, but its parts are half as large: where the keys of
-// few tiles are spread over all SMs, writing and joining the parts takes longer than
-// reading the keys (4 key tiles an SM or fewer: 896 rows on 8320 keys 27 us with
-// 256 rows, 22 us with 128). An fp32 tile of 64 rows reads shared memory less
-// for a product; one of 16 is done sooner, where groups have few rows or all tiles
-// of 16 still find an SM each (12 rows on 272 keys: 17.5 us and 13.6 us).
-int choose_tile_tokens(const fastocr_handle* h, int64_t rows, int64_t groups, long keys) {
-  const int64_t g = h->dims.num_q_heads / h->dims.num_kv_heads;
-  auto units = [&](int bm) {   // about
-    return std::max(groups, (rows * g + bm - 1) / bm) * h->dims.num_kv_heads * ((keys + kKeyTile - 1) / kKeyTile);
-  };
-  int bm;
-  if (h->dims.dtype == FASTOCR_DTYPE_BF16)
-    bm = units(kRowsBf16) <= 4 * h->num_sms ? kRowsBf16 / 2 : kRowsBf16;
-  else
-    bm = rows * g <= 16 * groups || units(16) <= h->num_sms ? 16 : kRowsF32;
-  return bm / (int)g;
-}
-
-// Key tiles of a share, where few items are shared by all CTAs: a part of an item
-// costs its rows' partials written and read (about 1 KB a row), a key tile of a
-// share costs every CTA 1 to 2 us. The sum is least near sqrt(key tiles * rows /
-// 1600): measured at 2, 6, 3 and 8 for 33 tiles and 224 rows (17.3 us), 65 and
-// 896 (22.4 us), 16 and 896 (17.7 us), 65 and 1792 (30.3 us); within 1 us of
-// the best share on nine shapes. fp32 tiles cost far more than their parts.
-int choose_share(const fastocr_handle* h, int64_t rows, long keys) {
-  if (h->dims.dtype != FASTOCR_DTYPE_BF16) return 1;
-  const double tiles = (double)((keys + kKeyTile - 1) / kKeyTile);
-  return (int)std::max(2.0, sqrt(tiles * (double)rows * h->dims.num_q_heads / 1600.0) + 0.5);
-}
-
 // Lays the workspace out for `rows` query tokens from `base` on and returns its
 // size: the slots, then what the readers of the parts need (see rows.cuh).
 int64_t place_workspace(const fastocr_handle* h, int64_t rows, bool shared, char* base, RowsParams& p) {
@@ -117,14 +76,6 @@ int64_t place_workspace(const fastocr_handle* h, int64_t rows, bool shared, char
     p.item_part = reinterpret_cast<int4*>(take((int64_t)h->num_sms * 32));
   }
   return (int64_t)at;
-}
-
-// The kernels count units of work in 32 bits.
-bool units_fit(const fastocr_handle* h, int64_t rows, int64_t groups) {
-  const int64_t g = h->dims.num_q_heads / h->dims.num_kv_heads;
-  const int64_t least = (h->dims.dtype == FASTOCR_DTYPE_BF16 ? kRowsBf16 / 2 : 16) / g;   // tokens of a row tile
-  const int64_t tiles = rows / least + std::min(rows, groups);
-  return (double)tiles * h->dims.num_kv_heads * (max_tokens(h) / kKeyTile + 1) < 2147483647.0;
 }
 
 fastocr_status launch_rows(const fastocr_handle* h, const RowsParams& p, cudaStream_t s) {
@@ -262,13 +213,7 @@ fastocr_status fastocr_cross_attend(fastocr_handle* h, const void* q, const fast
   if (!units_fit(h, rows, h->dims.batch)) return FASTOCR_ERR_UNSUPPORTED;
   if ((st = check_device(h)) != FASTOCR_OK) return st;
   if (rows == 0) return FASTOCR_OK;
-  // A decode step has one query token a sequence, or none. Those go to the split-K
-  // attend kernel, a token a unit, whose small tiles keep more of the states in
-  // flight (16 sequences, 10 heads, up to 2624 states: 32 us, row kernel and merge
-  // 46; two tokens in every other sequence 26 us and 32). Only the number of rows
-  // is known here, so tokens of one sequence may come this way too and read its
-  // states from L2 again: all 16 in one sequence, 8320 states, 23 us and 18.
-  if (rows <= h->dims.batch) {
+  if (cross_by_token(h, rows)) {
     Params a = base_params(h, q, kv, out);
     a.q_start = q_start;
     a.q_rows = (int)rows;

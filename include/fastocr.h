@@ -358,7 +358,8 @@ fastocr_status fastocr_evict(fastocr_handle* h, const fastocr_kv* kv, const fast
  * rows * H_q < 2^31.
  * ws: as fastocr_shared_attend, fastocr_rows_workspace(h, rows) bytes. Overlap:
  * as the other calls; q_start and the states' K/V rows are read before the
- * preceding kernel completes. Two kernels, or one where rows <= B.
+ * preceding kernel completes. Two kernels, or one where rows <= B (in bf16 as long
+ * as `rows` times a sequence's expected states come to at most 1 GB).
  * Errors: NULL, INVALID (rows, ws_bytes, another device current),
  * UNSUPPORTED, ALIGN, CUDA. */
 fastocr_status fastocr_cross_attend(fastocr_handle* h, const void* q, const fastocr_kv* kv,

@@ -1,12 +1,13 @@
 // Host-side probe of the row operators' plans, run without a GPU by
 // tests/test_rows_plan.py. Reads commands from stdin, one result per line:
 //   p <mode> <q_rows> <len>   -> splits and whether the next kernel is let go early
+//   c <rows>                  -> whether a cross attention goes a token a unit
 // for the handle that the arguments describe:
 //   rows_probe <batch> <H_q> <H_kv> <d> <dtype> <max_pages> <page> <SMs> <active[1..16]>
 #include <stdio.h>
 #include <stdlib.h>
 
-#include "handle.cuh"
+#include "rows_plan.cuh"
 
 using namespace fastocr;
 
@@ -39,6 +40,10 @@ int main(int argc, char** argv) {
       p.q_rows = q_rows;
       plan_launch(&h, mode, len, p);
       printf("%d %d\n", p.splits, (int)p.pdl_early);
+    } else if (cmd[0] == 'c') {
+      long rows;
+      if (scanf("%ld", &rows) != 1) return 2;
+      printf("%d\n", (int)cross_by_token(&h, rows));
     } else {
       return 2;
     }

@@ -41,3 +41,20 @@ def test_cross_attention_is_split_by_its_tokens_not_by_the_batch(plan):
                 assert own[0] == own[1] == large[0], (heads, n, rows, own, large)
     # a handful of tokens spreads its states over the GPU
     assert plan((256, 28, 4, 128, BF16, 1024, 16), [f"p {CROSS} 1 8320"])[0] == [16, 1]
+
+
+def test_cross_attention_goes_by_token_only_as_far_as_its_worst_case_allows(plan):
+    """As many tokens as sequences may be one prompt: its states are then read once a token."""
+    def by_token(batch, rows, heads, pages, dtype=BF16):
+        return plan((batch, *heads, dtype, pages, 16), [f"c {rows}"])[0][0]
+    big = (28, 4, 128)
+    assert by_token(16, 16, (10, 10, 128), 164) == 1          # a decode step
+    assert by_token(256, 1, big, 520) == 1                    # one token on a large handle
+    assert by_token(256, 256, big, 520) == 0                  # 4.4 GB if it is one prompt
+    assert by_token(256, 256, (10, 10, 128), 520) == 0
+    assert by_token(256, 256, big, 38) == 1                   # short states
+    assert by_token(16, 17, big, 10) == 0                     # more tokens than sequences
+    assert by_token(256, 256, big, 520, F32) == 1             # the fp32 row kernel takes longer for single tokens
+    assert by_token(70000, 70000, (4, 2, 64), 1) == 0         # a grid has 65535 blocks in z
+    assert by_token(70000, 70000, (4, 2, 64), 1, F32) == 0
+    assert by_token(70000, 65535, (4, 2, 64), 1) == by_token(70000, 65535, (4, 2, 64), 1, F32) == 1
