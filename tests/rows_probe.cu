@@ -2,6 +2,7 @@
 // tests/test_rows_plan.py. Reads commands from stdin, one result per line:
 //   p <mode> <q_rows> <len>   -> splits and whether the next kernel is let go early
 //   c <rows>                  -> whether a cross attention goes a token a unit
+//   t <rows> <groups> <keys>  -> query tokens of a row tile; keys 0: the expected length
 // for the handle that the arguments describe:
 //   rows_probe <batch> <H_q> <H_kv> <d> <dtype> <max_pages> <page> <SMs> <active[1..16]>
 #include <stdio.h>
@@ -44,6 +45,10 @@ int main(int argc, char** argv) {
       long rows;
       if (scanf("%ld", &rows) != 1) return 2;
       printf("%d\n", (int)cross_by_token(&h, rows));
+    } else if (cmd[0] == 't') {
+      long rows, groups, keys;
+      if (scanf("%ld %ld %ld", &rows, &groups, &keys) != 3) return 2;
+      printf("%d\n", choose_tile_tokens(&h, rows, groups, keys > 0 ? keys : expected_tokens(&h)));
     } else {
       return 2;
     }
