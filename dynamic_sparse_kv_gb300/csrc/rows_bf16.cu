@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsParams p) {
   enum { kSFull = 0, kPReady = 1, kPReady2 = 2, kPvDone = 3, kODone = 4 };
   if (tid == 0) {
     for (int s = 0; s < kSt; ++s) {
-      mbar_init(full(s), kLoadThreads);
+      mbar_init(full(s), kLoadThreads + kLoadThreads / 32);
       mbar_init(empty(s), 1);
     }
     mbar_init(q_full, 8);
@@ -650,6 +650,9 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsParams p) {
           // MMA's side: fence.proxy.async here would wait for every copy in
           // flight, so that one tile at a time was loaded.
           mbar_arrive_copies(full(st));
+          // The copies' arrival does not order this warp's key mask before the softmax's
+          // reading, which follows from this barrier by way of the MMA; a plain one does.
+          if (lane == 0) mbar_arrive(full(st));
         }
       }
     }
