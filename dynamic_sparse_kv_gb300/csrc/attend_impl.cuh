@@ -415,6 +415,13 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
   constexpr int kSliceMax = slice_for(V);
   using E = EpiSmem<D, kWarps>;
   constexpr bool kMma = sizeof(T) == 2;
+  // These modes give the second product their probabilities in two bf16 parts, the
+  // rounded value and the rounded remainder (together within 2^-16), against the same V
+  // fragments: as close to 64 bits as fp32 probabilities (relative error 0.0016 to
+  // 0.0017, the output's own rounding; one part 0.0020 to 0.0025) for 1 to 2 % of the
+  // time (8.0 us and 8.2, 15.4 and 15.5, 32.2 and 32.7; a tail behind a prefix 89.1 and
+  // 90.4). The others keep one part, and with it the results they had.
+  constexpr bool kTwoPart = kMma && (MODE == kTail || MODE == kWeigh || MODE == kCross);
   constexpr int ROWB = SM::kRowBytes;
   constexpr int CH = ROWB / 16;                 // 16-byte chunks per row
   const float kNegInf = -CUDART_INF_F;
@@ -911,12 +918,13 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
     // The P.V product takes the probabilities rounded to bf16. Outside focal
     // layers the softmax sum adds those same rounded values, so the weights
     // that multiply V sum to exactly 1 after normalisation (rounding moves a
-    // weight by at most 2^-9 relative, never the total). A focal layer's sum
+    // weight by at most 2^-8 relative, never the total). A focal layer's sum
     // also turns its logits into the image scores, which must be the
     // probabilities themselves, so there it adds the unrounded values; so does
-    // a profiling layer, whose image mass is a ratio of such sums.
+    // a profiling layer, whose image mass is a ratio of such sums, and so do the
+    // modes with two parts, whose products take all but 2^-16 of them.
     const uint32_t pk01 = pack_bf16(p0, p1), pk23 = pack_bf16(p2, p3);
-    if (stores_logits(MODE) || MODE == kProfile) {
+    if (kTwoPart || stores_logits(MODE) || MODE == kProfile) {
       sm_.l[0] += p0 + p2;
       sm_.l[1] += p1 + p3;
       if constexpr (MODE == kProfile) {
@@ -932,12 +940,18 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
     // P^T[16 keys x 8 heads] as the B operand: transpose the two 8x8 blocks
     const uint32_t bb0 = movmatrix_trans(pk01);
     const uint32_t bb1 = movmatrix_trans(pk23);
+    uint32_t bl0 = 0u, bl1 = 0u;   // what the rounding left
+    if constexpr (kTwoPart) {
+      bl0 = movmatrix_trans(pack_bf16(p0 - __uint_as_float(pk01 << 16), p1 - __uint_as_float(pk01 & 0xffff0000u)));
+      bl1 = movmatrix_trans(pack_bf16(p2 - __uint_as_float(pk23 << 16), p3 - __uint_as_float(pk23 & 0xffff0000u)));
+    }
 #pragma unroll
     for (int mt = 0; mt < D / 16; ++mt) {
       uint32_t a[4];
       ldmatrix_x4_trans(a, vA + voff[mt & 3] + (mt >> 2) * 128);
       // O^T[16 dims x 8 heads] += V^T[16 dims x 16 keys] . P^T[16 keys x 8 heads]
       mma_bf16(sm_.acc[mt], a, bb0, bb1);
+      if constexpr (kTwoPart) mma_bf16(sm_.acc[mt], a, bl0, bl1);
     }
   };
 
