@@ -19,17 +19,21 @@
 // gathered rows an instruction 7 (1190 us); K by TMA next to V by cp.async 380 us;
 // cp.async alone 370 us, all before the work was dealt out evenly.
 //
-// Many rows (4 x 1024 queries, 28 heads, up to 8320 states: 275 us, 1.18
-// PFLOP/s): the products of a key tile of two row tiles take 2048 cycles, alone and
-// at full rate as measured, a tile here 3200. What bounds it is a turn's chain:
-// S = QK^T, 1400 cycles of softmax behind TMEM loads, PV, and about 250 cycles
-// each time a commit or a P has to be seen through a barrier; a sixth of a CTA's
-// cycles are the starts and ends of its three or four segments. It is not the
-// copies: without any, 284 us became 273. Against those 284 us, sixteen softmax
-// warps with half a row each took 283 (the issuing warp is the slowest link
-// then), an issuing warp a turn 309 (the turns' products interleave and both end
-// late), a warp apart for the block table 283, and S loaded in blocks of 32 columns
-// under the exponentials 351 (spills).
+// Many rows (4 x 1024 queries, 28 heads, up to 8320 states): 275 us back to back (1.18
+// PFLOP/s), 290 to 299 us as a call among others (1.09 to 1.12). The products of a key
+// tile of two row tiles take 2048 cycles, alone and at full rate as measured, a tile
+// here 3200. What bounds it is a turn's chain: S = QK^T, 1400 cycles of softmax
+// behind TMEM loads, PV, and about 250 cycles each time a commit or a P has to be seen
+// through a barrier. The turn's next S is issued behind its PV, which reads P from
+// columns 0-63 of S's 128; the other 64 are free once the scores are in registers, and
+// with D = 64 another 128 of TMEM's 512 are, so half an S could start earlier (not
+// tried). A sixth of a CTA's cycles are the starts and ends of its three or four
+// segments. The compiler spills 168 bytes of stores and 228 of loads at D = 128 (148
+// and 208 at 64). It is not the copies: without any, 284 us became 273. Against those
+// 284 us, sixteen softmax warps with half a row each took 283 (the issuing warp is the
+// slowest link then), an issuing warp a turn 309 (the turns' products interleave and
+// both end late), a warp apart for the block table 283, and S loaded in blocks of 32
+// columns under the exponentials 351 (far more spills). D = 64: 213 us.
 // Few rows: the chain of a start, one or two tiles and the output, 9 us in all (8
 // sequences on 4160 keys), and the parts' way through the L2.
 #include <math_constants.h>
@@ -414,6 +418,11 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsParams p) {
             unpack2(fma2(pack2(x[64 * half + 2 * e], x[64 * half + 2 * e + 1]), scale2, base2), a, b);
             a = fast_exp2(a);
             b = fast_exp2(b);
+            // P is rounded to bf16, each value by 2^-8 at most, which the products take;
+            // l adds the values themselves, since a weighed step makes the rows' weights
+            // of it. A second bf16 part (as in the attend kernel's tail mode) would make
+            // the products of a tile 3072 cycles for 2048; the relative error against 64
+            // bits is 0.0022 to 0.0023 so, with fp32 probabilities 0.0017.
             sum[e & 1] = add2(sum[e & 1], pack2(__float_as_uint(a), __float_as_uint(b)));
             pk[e] = pack_bf16(a, b);
             if (!half) max_of(4 * e, 4 * e + 4, mx);
