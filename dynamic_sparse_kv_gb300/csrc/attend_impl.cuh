@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
   using E = EpiSmem<D, kWarps>;
   constexpr bool kMma = sizeof(T) == 2;
   // These modes give the second product their probabilities in two bf16 parts, the
-  // rounded value and the rounded remainder (together within 2^-16), against the same V
+  // value cut off and its rounded remainder (together within 2^-15), against the same V
   // fragments: as close to 64 bits as fp32 probabilities (relative error 0.0016 to
   // 0.0017, the output's own rounding; one part 0.0020 to 0.0025) for 1 to 2 % of the
   // time (8.0 us and 8.2, 15.4 and 15.5, 32.2 and 32.7; a tail behind a prefix 89.1 and
@@ -922,8 +922,15 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
     // also turns its logits into the image scores, which must be the
     // probabilities themselves, so there it adds the unrounded values; so does
     // a profiling layer, whose image mass is a ratio of such sums, and so do the
-    // modes with two parts, whose products take all but 2^-16 of them.
-    const uint32_t pk01 = pack_bf16(p0, p1), pk23 = pack_bf16(p2, p3);
+    // modes with two parts, whose products take all but 2^-15 of them.
+    uint32_t pk01, pk23;
+    if constexpr (kTwoPart) {   // cut off, not rounded: the remainder is then positive
+      pk01 = __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
+      pk23 = __byte_perm(__float_as_uint(p2), __float_as_uint(p3), 0x7632);
+    } else {
+      pk01 = pack_bf16(p0, p1);
+      pk23 = pack_bf16(p2, p3);
+    }
     if (kTwoPart || stores_logits(MODE) || MODE == kProfile) {
       sm_.l[0] += p0 + p2;
       sm_.l[1] += p1 + p3;
@@ -940,10 +947,12 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
     // P^T[16 keys x 8 heads] as the B operand: transpose the two 8x8 blocks
     const uint32_t bb0 = movmatrix_trans(pk01);
     const uint32_t bb1 = movmatrix_trans(pk23);
-    uint32_t bl0 = 0u, bl1 = 0u;   // what the rounding left
+    uint32_t bl0 = 0u, bl1 = 0u;
     if constexpr (kTwoPart) {
-      bl0 = movmatrix_trans(pack_bf16(p0 - __uint_as_float(pk01 << 16), p1 - __uint_as_float(pk01 & 0xffff0000u)));
-      bl1 = movmatrix_trans(pack_bf16(p2 - __uint_as_float(pk23 << 16), p3 - __uint_as_float(pk23 & 0xffff0000u)));
+      // what the cut left, below 2^-7 of p; never 0, so that an infinite V stays infinite
+      auto rest = [](float x) { return fmaxf(x - __uint_as_float(__float_as_uint(x) & 0xffff0000u), x * 0x1p-24f); };
+      bl0 = movmatrix_trans(pack_bf16(rest(p0), rest(p1)));
+      bl1 = movmatrix_trans(pack_bf16(rest(p2), rest(p3)));
     }
 #pragma unroll
     for (int mt = 0; mt < D / 16; ++mt) {
