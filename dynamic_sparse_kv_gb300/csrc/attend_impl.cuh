@@ -419,9 +419,10 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
   // value cut off and its rounded remainder (together within 2^-15), against the same V
   // fragments: as close to 64 bits as fp32 probabilities (relative error 0.0016 to
   // 0.0017, the output's own rounding; one part 0.0020 to 0.0025) for 1 to 2 % of the
-  // time (8.0 us and 8.2, 15.4 and 15.5, 32.2 and 32.7; a tail behind a prefix 89.1 and
-  // 90.4). The others keep one part, and with it the results they had.
-  constexpr bool kTwoPart = kMma && (MODE == kTail || MODE == kWeigh || MODE == kCross);
+  // time (8.0 us and 8.2, 15.4 and 15.5, 32.2 and 32.6). The others keep one part, and
+  // with it the results they had: a tail joins prefix parts that are rounded as much
+  // (64 sequences, 16448 + 4096 keys: 89.0 us and 90.8, error 0.0023 both).
+  constexpr bool kTwoPart = kMma && (MODE == kWeigh || MODE == kCross);
   constexpr int ROWB = SM::kRowBytes;
   constexpr int CH = ROWB / 16;                 // 16-byte chunks per row
   const float kNegInf = -CUDART_INF_F;

@@ -1,4 +1,4 @@
-"""Outputs of the split-K forms of the row operators in bf16: their probabilities reach the second
+"""Outputs of weighed attention and of single-token cross attention in bf16: their probabilities reach the second
 product within 2^-15, so an output is off by its own rounding and fp32 arithmetic only."""
 import numpy as np
 import pytest
@@ -43,19 +43,6 @@ def test_weighed_attention(heads, splits):
     dec.track_weights(2100, 0)
     out = torch.empty_like(q)
     dec.weigh_layer(0, q, out)
-    for b in range(3):
-        check_fine(out[b:b + 1], np64(q[b:b + 1]), *c.rows(b, 0, n[b]), f"sequence {b}")
-    dec.close()
-
-
-@pytest.mark.parametrize("heads", HEADS)
-def test_own_rows_of_a_shared_prefix_call(heads):
-    """Without a prefix all rows are the tail kernel's."""
-    c, start, prefix, n, q = shared_case([2, 1], [0, 0], [700, 33, 2100], heads, 16, BF, 4)
-    dec = decoder(c, n, heads[0])
-    dec.share_prefix(start, torch.tensor(prefix))
-    out = torch.empty_like(q)
-    dec.shared_layer(0, q, out)
     for b in range(3):
         check_fine(out[b:b + 1], np64(q[b:b + 1]), *c.rows(b, 0, n[b]), f"sequence {b}")
     dec.close()
