@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsParams p) {
             // probabilities 0.0017. Adding the rounded values, so that a row's weights sum
             // to 1, leaves 0.0019 to 0.0022 for 3 % more time (8 % with few rows); a second
             // bf16 part (as in the attend kernel's weigh mode) would make the products of a
-            // tile 3072 cycles for 2048.
+            // tile half as long again.
             sum[e & 1] = add2(sum[e & 1], pack2(__float_as_uint(a), __float_as_uint(b)));
             pk[e] = pack_bf16(a, b);
             if (!half) max_of(4 * e, 4 * e + 4, mx);

@@ -340,7 +340,8 @@ fastocr_status fastocr_weigh_attend(fastocr_handle* h, const void* q, const fast
  * must not be in two sequences' tables, nor twice in one. Only prefix positions keep their
  * meaning after it: rows are no longer in text order, so fastocr_rswa_attend's
  * window and an image behind protect do not apply.
- * 1 <= budget, 0 <= recent <= budget, stride <= 262144 (UNSUPPORTED). One
+ * 1 <= budget, 0 <= recent <= budget; the smaller of stride and the capacity
+ * <= 262144 (UNSUPPORTED). One
  * kernel; protect, seen and seq_len are read before the preceding kernel
  * completes, mass and pos after it. A call that attends to the moved rows
  * reads them before the kernel preceding it completes (see Overlap above), so
