@@ -25,8 +25,10 @@ FASTOCR_ERR_NO_DEVICE = -5
 FASTOCR_ERR_ALIGN = -6
 FASTOCR_DTYPE_F32 = 0
 FASTOCR_DTYPE_BF16 = 1
+FASTOCR_DTYPE_FP4 = 2
 DEV_BAD_PAGE, DEV_BAD_SEQLEN, DEV_BAD_IMG, DEV_BAD_SELECTION, DEV_INTERNAL = 1, 2, 4, 8, 16
 DEV_BAD_GROUP, DEV_BAD_WEIGHTS = 32, 64
+DEV_BAD_POSITION, DEV_NO_PAGES, DEV_BAD_POOL = 128, 256, 512
 
 
 class fastocr_dims(ctypes.Structure):
@@ -40,7 +42,32 @@ class fastocr_dims(ctypes.Structure):
 class fastocr_kv(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
                 ("block_table", ctypes.c_void_p), ("seq_len", ctypes.c_void_p),
-                ("num_pages", ctypes.c_int32)]
+                ("num_pages", ctypes.c_int32),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("k_gain", ctypes.c_void_p), ("v_gain", ctypes.c_void_p)]
+
+
+class fastocr_rotary(ctypes.Structure):
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("axis", ctypes.c_void_p),
+                ("positions", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
+                ("axes", ctypes.c_int32), ("adjacent", ctypes.c_int32)]
+
+
+class fastocr_tokens(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("q_out", ctypes.c_void_p), ("pos", ctypes.c_void_p), ("start", ctypes.c_void_p),
+                ("tokens", ctypes.c_int32)]
+
+
+class fastocr_pool(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.c_void_p), ("seq_len", ctypes.c_void_p),
+                ("held", ctypes.c_void_p), ("refs", ctypes.c_void_p), ("num_pages", ctypes.c_int32),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("k_layer", ctypes.c_int64), ("v_layer", ctypes.c_int64),
+                ("k_scale_layer", ctypes.c_int64), ("v_scale_layer", ctypes.c_int64),
+                ("ws", ctypes.c_void_p), ("ws_bytes", ctypes.c_int64)]
 
 
 class fastocr_groups(ctypes.Structure):
@@ -91,6 +118,16 @@ def _load() -> ctypes.CDLL:
         "fastocr_evict": ([P, ctypes.POINTER(fastocr_kv), ctypes.POINTER(fastocr_weights), I32,
                            I32, P, P], I32),
         "fastocr_cross_attend": ([P, P, ctypes.POINTER(fastocr_kv), P, I64, P, P, I64, P], I32),
+        "fastocr_write_rows": ([P, ctypes.POINTER(fastocr_kv), ctypes.POINTER(fastocr_tokens),
+                                ctypes.POINTER(fastocr_rotary), P], I32),
+        "fastocr_read_rows": ([P, ctypes.POINTER(fastocr_kv), P, I32, P, P, I32, P], I32),
+        "fastocr_pool_workspace": ([P, I64], I64),
+        "fastocr_pool_reserve": ([P, ctypes.POINTER(fastocr_pool), P, I32, P, P], I32),
+        "fastocr_pool_fork": ([P, ctypes.POINTER(fastocr_pool), P, P, I32, P], I32),
+        "fastocr_pool_release": ([P, ctypes.POINTER(fastocr_pool), P, I32, P], I32),
+        "fastocr_pool_trim": ([P, ctypes.POINTER(fastocr_pool), P], I32),
+        "fastocr_pool_compact": ([P, ctypes.POINTER(fastocr_pool), P, P], I32),
+        "fastocr_pool_copy": ([P, ctypes.POINTER(fastocr_pool), P, P, I32, P], I32),
         "fastocr_profiler_reset": ([P, P], I32),
         "fastocr_profiler_select": ([P, I32, ctypes.POINTER(I32), ctypes.POINTER(F64), P], I32),
         "fastocr_profiler_read": ([P, ctypes.POINTER(F64), P], I32),
@@ -133,8 +170,15 @@ def check_tensor(t, name, shape, dtype, device) -> None:
 
 
 def check_caches(k, v) -> int:
-    """The dtype code of a stack's caches [layers, pages, H_kv, page, d]; refuses what the
-    kernels would read wrongly. Layers may lie apart, each must be contiguous."""
+    """The dtype code of a stack's caches [layers, pages, H_kv, page, d] (two tensors or two
+    Fp4Cache); refuses what the kernels would read wrongly. Layers may lie apart, each must
+    be contiguous."""
+    if getattr(k, "fp4", False) or getattr(v, "fp4", False):
+        if not (getattr(k, "fp4", False) and getattr(v, "fp4", False)) or k.shape != v.shape or k.device != v.device:
+            raise ValueError("k_cache and v_cache must be alike: two Fp4Cache of one shape and device")
+        k.check()
+        v.check()
+        return FASTOCR_DTYPE_FP4
     if k.dim() != 5 or k.shape != v.shape or k.dtype != v.dtype or k.device != v.device:
         raise ValueError("k_cache and v_cache must be alike, [layers, pages, H_kv, page_size, d]")
     if k.dtype not in (torch.bfloat16, torch.float32):
@@ -178,7 +222,11 @@ def fastocr_destroy(handle: int) -> None:
 
 
 def make_kv(k, v, block_table, seq_len) -> fastocr_kv:
-    """One layer's cache descriptor; keeps no reference to the tensors."""
+    """One layer's cache descriptor; keeps no reference to the tensors. k, v: two tensors,
+    or what an Fp4Cache gives for a layer."""
+    if isinstance(k, tuple):   # codes, scales, gain
+        return fastocr_kv(_ptr(k[0]), _ptr(v[0]), _ptr(block_table), _ptr(seq_len), int(k[0].shape[0]),
+                          _ptr(k[1]), _ptr(v[1]), _ptr(k[2]), _ptr(v[2]))
     return fastocr_kv(_ptr(k), _ptr(v), _ptr(block_table), _ptr(seq_len), int(k.shape[0]))
 
 
@@ -297,6 +345,64 @@ def fastocr_cross_attend(handle, q, kv: fastocr_kv, q_start, rows, out, ws, ws_b
     _check("fastocr_cross_attend",
            lib.fastocr_cross_attend(handle, _ptr(q), ctypes.byref(kv), _ptr(q_start), int(rows),
                                     _ptr(out), _ptr(ws), int(ws_bytes), _stream(stream)))
+
+
+def fastocr_write_rows(handle, kv: fastocr_kv, tokens: fastocr_tokens, rotary: fastocr_rotary | None = None,
+                       stream=None) -> None:
+    """Tokens to their rows of one layer's cache, with rotary positions for queries and keys."""
+    r = ctypes.byref(rotary) if rotary is not None else None
+    _check("fastocr_write_rows",
+           lib.fastocr_write_rows(handle, ctypes.byref(kv), ctypes.byref(tokens), r, _stream(stream)))
+
+
+def fastocr_read_rows(handle, kv: fastocr_kv, start, tokens, k_out, v_out, out_dtype, stream=None) -> None:
+    """The last rows of every sequence, packed, as bf16 or fp32 values."""
+    _check("fastocr_read_rows",
+           lib.fastocr_read_rows(handle, ctypes.byref(kv), _ptr(start), int(tokens), _ptr(k_out),
+                                 _ptr(v_out), int(out_dtype), _stream(stream)))
+
+
+def fastocr_pool_workspace(handle, num_pages) -> int:
+    n = lib.fastocr_pool_workspace(handle, int(num_pages))
+    if n < 0:
+        raise FastOCRError("fastocr_pool_workspace", int(n))
+    return n
+
+
+def fastocr_pool_reserve(handle, pool: fastocr_pool, rows, extra, missing=None, stream=None) -> None:
+    """Pages for every sequence's next rows, shared ones copied before they are written."""
+    _check("fastocr_pool_reserve",
+           lib.fastocr_pool_reserve(handle, ctypes.byref(pool), _ptr(rows), int(extra), _ptr(missing),
+                                    _stream(stream)))
+
+
+def fastocr_pool_fork(handle, pool: fastocr_pool, src, dst, n, stream=None) -> None:
+    """Sequences dst become copies of src that share their pages."""
+    _check("fastocr_pool_fork",
+           lib.fastocr_pool_fork(handle, ctypes.byref(pool), _ptr(src), _ptr(dst), int(n), _stream(stream)))
+
+
+def fastocr_pool_release(handle, pool: fastocr_pool, seqs, n, stream=None) -> None:
+    """Sequences give up their pages."""
+    _check("fastocr_pool_release",
+           lib.fastocr_pool_release(handle, ctypes.byref(pool), _ptr(seqs), int(n), _stream(stream)))
+
+
+def fastocr_pool_trim(handle, pool: fastocr_pool, stream=None) -> None:
+    """Every sequence gives up the pages behind its rows."""
+    _check("fastocr_pool_trim", lib.fastocr_pool_trim(handle, ctypes.byref(pool), _stream(stream)))
+
+
+def fastocr_pool_compact(handle, pool: fastocr_pool, used=None, stream=None) -> None:
+    """The pages in use move together at the pool's start."""
+    _check("fastocr_pool_compact",
+           lib.fastocr_pool_compact(handle, ctypes.byref(pool), _ptr(used), _stream(stream)))
+
+
+def fastocr_pool_copy(handle, pool: fastocr_pool, src, dst, n, stream=None) -> None:
+    """Pages src to pages dst, in every layer."""
+    _check("fastocr_pool_copy",
+           lib.fastocr_pool_copy(handle, ctypes.byref(pool), _ptr(src), _ptr(dst), int(n), _stream(stream)))
 
 
 def fastocr_profiler_reset(handle, stream=None) -> None:

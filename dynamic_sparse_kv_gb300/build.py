@@ -21,9 +21,10 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfastocr.so")
 
-SOURCES = ["abi.cu", "abi_rows.cu", "evict.cu", "kernels_bf16.cu", "kernels_f32.cu", "noalloc.cu",
-           "probe.cu", "rows_bf16.cu", "rows_f32.cu"]
-HEADERS = ["attend_kernels.cuh", "attend_impl.cuh", "evict.cuh", "handle.cuh", "rows.cuh",
+SOURCES = ["abi.cu", "abi_cache.cu", "abi_rows.cu", "cache_rows.cu", "evict.cu", "kernels_bf16.cu",
+           "kernels_f32.cu", "kernels_fp4.cu", "noalloc.cu", "pages.cu", "probe.cu", "rows_bf16.cu", "rows_f32.cu"]
+HEADERS = ["attend_kernels.cuh", "attend_impl.cuh", "cache_rows.cuh", "evict.cuh", "fp4.cuh",
+           "handle.cuh", "pages.cuh", "rows.cuh",
            "rows_plan.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -32,6 +32,8 @@ class CrossAttention:
             raise ValueError(f"block_table must be [B, pages], state_len an int or [B], not "
                              f"{tuple(block_table.shape)} and {tuple(state_len.shape)}")
         dtype = N.check_caches(k_cache, v_cache)
+        if dtype == N.FASTOCR_DTYPE_FP4:
+            raise ValueError("cross attention needs states in bf16 or fp32, not in 4 bits")
         assert k_cache.is_cuda
         self.k_cache, self.v_cache = k_cache, v_cache
         self.layers, _, self.kv_heads, self.page_size, self.head_dim = k_cache.shape

@@ -36,7 +36,8 @@ fastocr_status fastocr_create(const fastocr_dims* dims, fastocr_handle** out) {
       d.num_layers < 1 || d.max_img_tokens < 0 || d.page_size < 1 || d.page_size > 256)
     return FASTOCR_ERR_INVALID;
   if (d.num_q_heads % d.num_kv_heads != 0) return FASTOCR_ERR_INVALID;
-  if (d.dtype != FASTOCR_DTYPE_F32 && d.dtype != FASTOCR_DTYPE_BF16) return FASTOCR_ERR_INVALID;
+  if (d.dtype != FASTOCR_DTYPE_F32 && d.dtype != FASTOCR_DTYPE_BF16 && d.dtype != FASTOCR_DTYPE_FP4)
+    return FASTOCR_ERR_INVALID;
   const int log2_page = ilog2_exact(d.page_size);
   if (log2_page < 0) return FASTOCR_ERR_INVALID;
   if (d.num_q_heads / d.num_kv_heads > kSlots) return FASTOCR_ERR_UNSUPPORTED;
@@ -49,7 +50,7 @@ fastocr_status fastocr_create(const fastocr_dims* dims, fastocr_handle** out) {
   cudaDeviceProp prop;
   if (cudaGetDeviceProperties(&prop, dev) != cudaSuccess) return FASTOCR_ERR_NO_DEVICE;
   if (prop.major != 10 || prop.minor != 3) return FASTOCR_ERR_NO_DEVICE;
-  if (prepare_bf16() != cudaSuccess || prepare_f32() != cudaSuccess ||
+  if (prepare_bf16() != cudaSuccess || prepare_f32() != cudaSuccess || prepare_fp4() != cudaSuccess ||
       prepare_rows_f32() != cudaSuccess || prepare_rows_bf16() != cudaSuccess ||
       prepare_evict() != cudaSuccess)
     return FASTOCR_ERR_CUDA;
@@ -75,11 +76,13 @@ fastocr_status fastocr_create(const fastocr_dims* dims, fastocr_handle** out) {
   h->log2_page = log2_page;
   for (int v = 0; v < kNumVariants; ++v)
     h->max_splits_v[v] = d.dtype == FASTOCR_DTYPE_BF16 ? max_cluster_bf16(d.head_dim, v)
-                                                       : max_cluster_f32(d.head_dim, v);
+                         : d.dtype == FASTOCR_DTYPE_FP4 ? max_cluster_fp4(d.head_dim, v)
+                                                        : max_cluster_f32(d.head_dim, v);
   h->max_splits = h->max_splits_v[kGeneral];
   for (int c = 1; c <= h->max_splits; ++c)
     h->active[c] = d.dtype == FASTOCR_DTYPE_BF16 ? active_clusters_bf16(d.head_dim, c)
-                                                 : active_clusters_f32(d.head_dim, c);
+                   : d.dtype == FASTOCR_DTYPE_FP4 ? active_clusters_fp4(d.head_dim, c)
+                                                  : active_clusters_f32(d.head_dim, c);
   h->ws_bytes = off;
   if (cudaMalloc(&h->ws, off) != cudaSuccess) {
     free(h);

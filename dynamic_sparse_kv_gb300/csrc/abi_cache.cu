@@ -1,0 +1,225 @@
+// C ABI of the calls that write, read and hand around the rows and pages of a cache
+// (declared in include/fastocr.h): argument checks and launches.
+#include <stdint.h>
+
+#include "cache_rows.cuh"
+#include "handle.cuh"
+#include "pages.cuh"
+
+using namespace fastocr;
+
+namespace {
+
+fastocr_status status_of(cudaError_t e) { return e == cudaSuccess ? FASTOCR_OK : FASTOCR_ERR_CUDA; }
+
+int q_bytes(const fastocr_handle* h) { return h->dims.dtype == FASTOCR_DTYPE_F32 ? 4 : 2; }
+
+CacheRows cache_rows(const fastocr_handle* h, const fastocr_kv* kv, const int32_t* start, int32_t tokens) {
+  CacheRows c;
+  memset(&c, 0, sizeof(c));
+  c.k = static_cast<char*>(const_cast<void*>(kv->k));
+  c.v = static_cast<char*>(const_cast<void*>(kv->v));
+  if (h->dims.dtype == FASTOCR_DTYPE_FP4) {
+    c.k_scale = static_cast<uint8_t*>(const_cast<void*>(kv->k_scale));
+    c.v_scale = static_cast<uint8_t*>(const_cast<void*>(kv->v_scale));
+    c.k_gain = kv->k_gain;
+    c.v_gain = kv->v_gain;
+  }
+  c.block_table = kv->block_table;
+  c.seq_len = kv->seq_len;
+  c.start = start;
+  c.num_pages = kv->num_pages;
+  c.max_pages = h->dims.max_pages_per_seq;
+  c.log2_page = h->log2_page;
+  c.B = h->dims.batch;
+  c.Hkv = h->dims.num_kv_heads;
+  c.tokens = tokens;
+  c.status = h->status;
+  return c;
+}
+
+// a grid of threads of 16 elements each stays below 2^31 CTAs of 256
+bool too_many(const fastocr_handle* h, int64_t tokens) {
+  return tokens * (h->dims.num_q_heads + 2LL * h->dims.num_kv_heads) * h->dims.head_dim >= (1LL << 34);
+}
+
+fastocr_status pool_params(const fastocr_handle* h, const fastocr_pool* pool, PoolParams& p) {
+  if (!h || !pool || !pool->block_table || !pool->seq_len || !pool->held || !pool->refs || !pool->k || !pool->v ||
+      !pool->ws)
+    return FASTOCR_ERR_NULL;
+  const fastocr_dims& d = h->dims;
+  const bool fp4 = d.dtype == FASTOCR_DTYPE_FP4;
+  if (fp4 && (!pool->k_scale || !pool->v_scale)) return FASTOCR_ERR_NULL;
+  if (pool->num_pages < 1) return FASTOCR_ERR_INVALID;
+  memset(&p, 0, sizeof(p));
+  void* bases[kPoolArrays] = {pool->k, pool->v, pool->k_scale, pool->v_scale};
+  const int64_t layers[kPoolArrays] = {pool->k_layer, pool->v_layer, pool->k_scale_layer, pool->v_scale_layer};
+  const int64_t rows = (int64_t)d.num_kv_heads * d.page_size;
+  const int64_t row = fp4 ? d.head_dim / 2 : (int64_t)d.head_dim * (d.dtype == FASTOCR_DTYPE_F32 ? 4 : 2);
+  const int64_t row_bytes[kPoolArrays] = {row, row, d.head_dim / 16, d.head_dim / 16};
+  p.arrays = fp4 ? 4 : 2;
+  p.layers = d.num_layers;
+  if (!aligned16(pool->ws)) return FASTOCR_ERR_ALIGN;
+  for (int a = 0; a < p.arrays; ++a) {
+    if (a < 2 ? !aligned16(bases[a]) || (p.layers > 1 && layers[a] & 15)
+              : !aligned_scales(h, bases[a]) || (p.layers > 1 && !aligned_scales(h, (const void*)layers[a])))
+      return FASTOCR_ERR_ALIGN;
+    if (rows * row_bytes[a] >= (1LL << 30)) return FASTOCR_ERR_UNSUPPORTED;
+    // layers apart by less than a cache would overlap; one layer needs no stride
+    if (p.layers > 1 && layers[a] < rows * row_bytes[a] * pool->num_pages) return FASTOCR_ERR_INVALID;
+    p.base[a] = static_cast<char*>(bases[a]);
+    p.layer[a] = p.layers > 1 ? (long)layers[a] : 0;
+    p.chunk[a] = (int)(rows * row_bytes[a]);
+    p.wide[a] = ((reinterpret_cast<uintptr_t>(bases[a]) | (uintptr_t)p.layer[a] | (uintptr_t)p.chunk[a]) & 15) == 0;
+  }
+  if (rows * pool->num_pages >= (1LL << 31) || (int64_t)d.batch * d.max_pages_per_seq >= (1LL << 31))
+    return FASTOCR_ERR_UNSUPPORTED;
+  if (pool->ws_bytes < pool_workspace(pool->num_pages, d.batch)) return FASTOCR_ERR_INVALID;
+  p.table = pool->block_table;
+  p.seq_len = pool->seq_len;
+  p.held = pool->held;
+  p.refs = pool->refs;
+  p.B = d.batch;
+  p.max_pages = d.max_pages_per_seq;
+  p.log2_page = h->log2_page;
+  p.num_pages = pool->num_pages;
+  p.status = h->status;
+  p.num_sms = h->num_sms;
+  place_pool_workspace(p, pool->ws);
+  return check_device(h);
+}
+
+}  // namespace
+
+extern "C" {
+
+fastocr_status fastocr_write_rows(fastocr_handle* h, const fastocr_kv* kv, const fastocr_tokens* t,
+                                  const fastocr_rotary* rotary, fastocr_stream stream) {
+  if (!h || !t || !t->k || !t->v || !t->q != !t->q_out) return FASTOCR_ERR_NULL;
+  fastocr_status st = check_kv(h, kv);
+  if (st != FASTOCR_OK) return st;
+  const fastocr_dims& d = h->dims;
+  const int64_t e = q_bytes(h), D = d.head_dim;
+  if (!aligned16(t->q) || !aligned16(t->k) || !aligned16(t->v) || !aligned16(t->q_out)) return FASTOCR_ERR_ALIGN;
+  if ((t->q_stride * e | t->k_stride * e | t->v_stride * e) & 15) return FASTOCR_ERR_ALIGN;
+  if (t->tokens < 0 || (!t->start && t->tokens != d.batch)) return FASTOCR_ERR_INVALID;
+  if (t->tokens > 1 && ((t->q && t->q_stride < d.num_q_heads * D) || t->k_stride < d.num_kv_heads * D ||
+                        t->v_stride < d.num_kv_heads * D))
+    return FASTOCR_ERR_INVALID;
+  if (too_many(h, t->tokens)) return FASTOCR_ERR_UNSUPPORTED;
+  WriteParams p;
+  memset(&p, 0, sizeof(p));
+  if (rotary) {
+    if (!rotary->cos_sin || !rotary->axis || !t->pos) return FASTOCR_ERR_NULL;
+    if (rotary->positions < 1 || rotary->axes < 1 || rotary->axes > 4 || rotary->rotary_dim < 2 ||
+        rotary->rotary_dim > D)
+      return FASTOCR_ERR_INVALID;
+    if (rotary->rotary_dim % 32) return FASTOCR_ERR_UNSUPPORTED;
+    if (!aligned16(rotary->cos_sin)) return FASTOCR_ERR_ALIGN;
+    p.cos_sin = rotary->cos_sin;
+    p.axis = rotary->axis;
+    p.pos = t->pos;
+    p.positions = rotary->positions;
+    p.rotary = rotary->rotary_dim;
+    p.axes = rotary->axes;
+    p.adjacent = rotary->adjacent != 0;
+  }
+  // q_out is written where it is read, or somewhere else altogether
+  if (t->q && t->tokens > 0) {
+    const char *a = static_cast<const char*>(t->q), *b = static_cast<const char*>(t->q_out);
+    const int64_t row = d.num_q_heads * D * e;
+    const char *a_end = a + (t->tokens - 1) * t->q_stride * e + row, *b_end = b + t->tokens * row;
+    const bool same = a == b && (t->q_stride * e == row || t->tokens == 1);
+    if (!same && a < b_end && b < a_end) return FASTOCR_ERR_INVALID;
+  }
+  if ((st = check_device(h)) != FASTOCR_OK) return st;
+  if (t->tokens == 0) return FASTOCR_OK;
+  p.c = cache_rows(h, kv, t->start, t->tokens);
+  p.q = static_cast<const char*>(t->q);
+  p.k = static_cast<const char*>(t->k);
+  p.v = static_cast<const char*>(t->v);
+  p.q_out = static_cast<char*>(t->q_out);
+  p.q_stride = t->q_stride * e;
+  p.k_stride = t->k_stride * e;
+  p.v_stride = t->v_stride * e;
+  p.Hq = d.num_q_heads;
+  p.single = !t->start;
+  return status_of(launch_write_rows(d.dtype, d.head_dim, h->num_sms, p, static_cast<cudaStream_t>(stream)));
+}
+
+fastocr_status fastocr_read_rows(fastocr_handle* h, const fastocr_kv* kv, const int32_t* start, int32_t tokens,
+                                 void* k_out, void* v_out, int32_t out_dtype, fastocr_stream stream) {
+  if (!h || !start || !k_out || !v_out) return FASTOCR_ERR_NULL;
+  fastocr_status st = check_kv(h, kv);
+  if (st != FASTOCR_OK) return st;
+  if (!aligned16(k_out) || !aligned16(v_out)) return FASTOCR_ERR_ALIGN;
+  if (tokens < 0 || (out_dtype != FASTOCR_DTYPE_F32 && out_dtype != FASTOCR_DTYPE_BF16)) return FASTOCR_ERR_INVALID;
+  if (too_many(h, tokens)) return FASTOCR_ERR_UNSUPPORTED;
+  if ((st = check_device(h)) != FASTOCR_OK) return st;
+  if (tokens == 0) return FASTOCR_OK;
+  ReadParams p;
+  p.c = cache_rows(h, kv, start, tokens);
+  p.k_out = static_cast<char*>(k_out);
+  p.v_out = static_cast<char*>(v_out);
+  p.out_f32 = out_dtype == FASTOCR_DTYPE_F32;
+  return status_of(launch_read_rows(h->dims.dtype, h->dims.head_dim, p, static_cast<cudaStream_t>(stream)));
+}
+
+int64_t fastocr_pool_workspace(const fastocr_handle* h, int64_t num_pages) {
+  if (!h) return FASTOCR_ERR_NULL;
+  if (num_pages < 1 || num_pages >= (1LL << 31)) return FASTOCR_ERR_INVALID;
+  return pool_workspace(num_pages, h->dims.batch);
+}
+
+fastocr_status fastocr_pool_reserve(fastocr_handle* h, const fastocr_pool* pool, const int32_t* rows, int32_t extra,
+                                    int32_t* missing, fastocr_stream stream) {
+  PoolParams p;
+  const fastocr_status st = pool_params(h, pool, p);
+  if (st != FASTOCR_OK) return st;
+  if (!rows && extra < 0) return FASTOCR_ERR_INVALID;
+  return status_of(launch_reserve(p, rows, extra, missing, static_cast<cudaStream_t>(stream)));
+}
+
+fastocr_status fastocr_pool_fork(fastocr_handle* h, const fastocr_pool* pool, const int32_t* src, const int32_t* dst,
+                                 int32_t n, fastocr_stream stream) {
+  PoolParams p;
+  const fastocr_status st = pool_params(h, pool, p);
+  if (st != FASTOCR_OK) return st;
+  if (!src || !dst) return FASTOCR_ERR_NULL;
+  if (n < 0 || n > p.B) return FASTOCR_ERR_INVALID;
+  return n == 0 ? FASTOCR_OK : status_of(launch_fork(p, src, dst, n, static_cast<cudaStream_t>(stream)));
+}
+
+fastocr_status fastocr_pool_release(fastocr_handle* h, const fastocr_pool* pool, const int32_t* seqs, int32_t n,
+                                    fastocr_stream stream) {
+  PoolParams p;
+  const fastocr_status st = pool_params(h, pool, p);
+  if (st != FASTOCR_OK) return st;
+  if (!seqs) return FASTOCR_ERR_NULL;
+  if (n < 0 || n > p.B) return FASTOCR_ERR_INVALID;
+  return n == 0 ? FASTOCR_OK : status_of(launch_release(p, seqs, n, static_cast<cudaStream_t>(stream)));
+}
+
+fastocr_status fastocr_pool_trim(fastocr_handle* h, const fastocr_pool* pool, fastocr_stream stream) {
+  PoolParams p;
+  const fastocr_status st = pool_params(h, pool, p);
+  return st != FASTOCR_OK ? st : status_of(launch_trim(p, static_cast<cudaStream_t>(stream)));
+}
+
+fastocr_status fastocr_pool_compact(fastocr_handle* h, const fastocr_pool* pool, int32_t* used, fastocr_stream stream) {
+  PoolParams p;
+  const fastocr_status st = pool_params(h, pool, p);
+  return st != FASTOCR_OK ? st : status_of(launch_compact(p, used, static_cast<cudaStream_t>(stream)));
+}
+
+fastocr_status fastocr_pool_copy(fastocr_handle* h, const fastocr_pool* pool, const int32_t* src, const int32_t* dst,
+                                 int32_t n, fastocr_stream stream) {
+  PoolParams p;
+  const fastocr_status st = pool_params(h, pool, p);
+  if (st != FASTOCR_OK) return st;
+  if (!src || !dst) return FASTOCR_ERR_NULL;
+  if (n < 0 || n > p.num_pages) return FASTOCR_ERR_INVALID;
+  return n == 0 ? FASTOCR_OK : status_of(launch_copy_pages(p, src, dst, n, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -11,12 +11,6 @@ using namespace fastocr;
 
 namespace {
 
-fastocr_status check_device(const fastocr_handle* h) {
-  int dev = -1;
-  if (cudaGetDevice(&dev) != cudaSuccess) return FASTOCR_ERR_NO_DEVICE;
-  return dev == h->device ? FASTOCR_OK : FASTOCR_ERR_INVALID;
-}
-
 fastocr_status check_weights(const fastocr_weights* w, bool attend) {
   if (!w || !w->mass || !w->pos || !w->protect || !w->seen || (attend && !w->logits))
     return FASTOCR_ERR_NULL;
@@ -100,6 +94,7 @@ fastocr_status fastocr_shared_attend(fastocr_handle* h, const void* q, const fas
                                      void* out, void* ws, int64_t ws_bytes, fastocr_stream stream) {
   if (!h || !q || !out || !groups || !groups->start || !groups->prefix_len || !ws)
     return FASTOCR_ERR_NULL;
+  if (h->dims.dtype == FASTOCR_DTYPE_FP4) return FASTOCR_ERR_UNSUPPORTED;
   fastocr_status st = check_kv(h, kv);
   if (st != FASTOCR_OK) return st;
   if (!aligned16(q) || !aligned16(out) || !aligned16(ws)) return FASTOCR_ERR_ALIGN;
@@ -140,6 +135,7 @@ fastocr_status fastocr_weigh_attend(fastocr_handle* h, const void* q, const fast
                                     const fastocr_weights* weights, void* out,
                                     fastocr_stream stream) {
   if (!h || !q || !out) return FASTOCR_ERR_NULL;
+  if (h->dims.dtype == FASTOCR_DTYPE_FP4) return FASTOCR_ERR_UNSUPPORTED;
   fastocr_status st = check_kv(h, kv);
   if (st != FASTOCR_OK) return st;
   if (!aligned16(q) || !aligned16(out)) return FASTOCR_ERR_ALIGN;
@@ -154,6 +150,7 @@ fastocr_status fastocr_evict(fastocr_handle* h, const fastocr_kv* kv, const fast
                              int32_t budget, int32_t recent, int32_t* new_len,
                              fastocr_stream stream) {
   if (!h) return FASTOCR_ERR_NULL;
+  if (h->dims.dtype == FASTOCR_DTYPE_FP4) return FASTOCR_ERR_UNSUPPORTED;
   fastocr_status st = check_kv(h, kv);
   if (st != FASTOCR_OK) return st;
   if ((st = check_weights(weights, false)) != FASTOCR_OK) return st;
@@ -203,6 +200,7 @@ fastocr_status fastocr_cross_attend(fastocr_handle* h, const void* q, const fast
                                     const int32_t* q_start, int64_t rows, void* out, void* ws,
                                     int64_t ws_bytes, fastocr_stream stream) {
   if (!h || !q || !out || !q_start || !ws) return FASTOCR_ERR_NULL;
+  if (h->dims.dtype == FASTOCR_DTYPE_FP4) return FASTOCR_ERR_UNSUPPORTED;
   fastocr_status st = check_kv(h, kv);
   if (st != FASTOCR_OK) return st;
   if (!aligned16(q) || !aligned16(out) || !aligned16(ws)) return FASTOCR_ERR_ALIGN;

@@ -5,6 +5,7 @@
 #include <math_constants.h>
 
 #include "attend_kernels.cuh"
+#include "fp4.cuh"
 
 namespace fastocr {
 
@@ -414,7 +415,8 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
   constexpr int kThreads = 32 * kWarps;
   constexpr int kSliceMax = slice_for(V);
   using E = EpiSmem<D, kWarps>;
-  constexpr bool kMma = sizeof(T) == 2;
+  constexpr bool kMma = Held<T>::kMma, kFp4 = Held<T>::kFp4;
+  using TQ = typename Held<T>::Q;
   // These modes give the second product their probabilities in two bf16 parts, the
   // value cut off and its rounded remainder (together within 2^-15), against the same V
   // fragments: as close to 64 bits as fp32 probabilities (relative error 0.0016 to
@@ -437,8 +439,8 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
       return;
     }
   }
-  const T* __restrict__ kg = static_cast<const T*>(p.k);
-  const T* __restrict__ vg = static_cast<const T*>(p.v);
+  const char* __restrict__ kg = static_cast<const char*>(p.k);
+  const char* __restrict__ vg = static_cast<const char*>(p.v);
   const int32_t* __restrict__ bt = p.block_table + (size_t)b * p.max_pages;
   const int page_mask = (1 << p.log2_page) - 1;
   unsigned char* pipe = smem + warp * ST * SM::kStageBytes;
@@ -455,7 +457,7 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
   // it. Only the general variant does so: its pipeline holds a few of a
   // CTA's tiles, so a stale guess costs a drain and a full restart, while the
   // deep variant's small grids stage whole lists and measured faster guessing.
-  const bool sel_pending = MODE == kSparse && V == kGeneral && p.sel_pending;
+  const bool sel_pending = MODE == kSparse && V != kDeep && p.sel_pending;
   // Otherwise k and this CTA's share of the selection are read before the
   // wait (checked after it unless the caller declared them final), issued
   // together with the lengths' loads. The share is guessed from the keep
@@ -547,13 +549,13 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
   const int ch_lane = lane % CH, row_lane = lane / CH;
   // lane constants of the copies: this lane's chunk of K and V rows, and its
   // swizzled destination offset in each of its kIss rows of a stage
-  const char* kg_lane = reinterpret_cast<const char*>(kg) + ch_lane * 16;
-  const char* vg_lane = reinterpret_cast<const char*>(vg) + ch_lane * 16;
+  const char* kg_lane = kg + ch_lane * 16;
+  const char* vg_lane = vg + ch_lane * 16;
   uint32_t doff[kIss];
 #pragma unroll
   for (int i = 0; i < kIss; ++i) {
     const int r = i * kRowsPerInst + row_lane;
-    doff[i] = r * ROWB + ((ch_lane ^ (r & 7)) << 4);
+    doff[i] = kFp4 ? fp4_place<D>(r, ch_lane) : r * ROWB + ((ch_lane ^ (r & 7)) << 4);
   }
   const uint64_t pol_stream = l2_policy_evict_first();   // K/V rows are read once
   auto issue = [&](int j, int n_round) {
@@ -576,6 +578,23 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
       const int bytes = rows[i] >= 0 ? 16 : 0;
       cp_async16(sb + doff[i], kg_lane + off, bytes, pol_stream);
       cp_async16(sb + doff[i] + kTile * ROWB, vg_lane + off, bytes, pol_stream);
+    }
+    if constexpr (kFp4) {   // the scales of 16 K rows and 16 V rows, a row a lane
+      const int r = lane & (kTile - 1);
+      int row = base + r < n_round ? srow[base + r] : -1;
+      if (row >= n_rows) row = -1;
+      const uint8_t* src = (lane < kTile ? p.k_scale : p.v_scale) + (size_t)max(row, 0) * SM::kScaleBytes;
+      cp_async_small<SM::kScaleBytes>(sb + 2 * kTile * ROWB + lane * SM::kScaleBytes, src,
+                                      row >= 0 ? SM::kScaleBytes : 0, pol_stream);
+    }
+  };
+  // pull a row's K and V into L2
+  auto prefetch_row = [&](int row) {
+    prefetch_l2(kg + (size_t)row * ROWB, ROWB);
+    prefetch_l2(vg + (size_t)row * ROWB, ROWB);
+    if constexpr (kFp4) {
+      prefetch_l2_line(p.k_scale + (size_t)row * SM::kScaleBytes);
+      prefetch_l2_line(p.v_scale + (size_t)row * SM::kScaleBytes);
     }
   };
 
@@ -657,11 +676,8 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
           // variant (large grids) does: there it shortens the post-wait stream,
           // while the deep variant's small grids measured faster without the
           // extra traffic next to the running layer.
-          if constexpr (V == kGeneral) {
-            if (u >= u_staged) {
-              prefetch_l2(kg + (size_t)row * D, ROWB);
-              prefetch_l2(vg + (size_t)row * D, ROWB);
-            }
+          if constexpr (V != kDeep) {
+            if (u >= u_staged) prefetch_row(row);
           }
         } else {
           ps = -1;
@@ -674,8 +690,7 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
       int row = -1, ps = c.cur_pos;
       if (cpage >= 0 && cpage < p.num_pages) {
         row = ((cpage * p.Hkv + hkv) << p.log2_page) | (ps & page_mask);
-        prefetch_l2(kg + (size_t)row * D, ROWB);
-        prefetch_l2(vg + (size_t)row * D, ROWB);
+        prefetch_row(row);
       } else {
         bad |= kDevBadPage;
         ps = masked<MODE>(ps);
@@ -688,8 +703,8 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
   // kernel, so they are read only after the wait; pulling their lines into L2
   // now is safe (L2 is where those writes land) and shortens that read.
   if (tid == 0)
-    prefetch_l2(static_cast<const T*>(p.q) + ((size_t)q_row * p.Hq + (size_t)hkv * p.g) * D,
-                p.g * D * (uint32_t)sizeof(T));
+    prefetch_l2(static_cast<const TQ*>(p.q) + ((size_t)q_row * p.Hq + (size_t)hkv * p.g) * D,
+                p.g * D * (uint32_t)sizeof(TQ));
   __syncthreads();
 #pragma unroll 1
   for (int j = 0; j < ST; ++j) {
@@ -722,7 +737,17 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
   WarpStateMma<D> sm_;
   WarpStateF32<D> sf_;
   const int gid = lane >> 2, tig = lane & 3;
-  if constexpr (kMma) {
+  float sl0 = p.scale_log2, sl1 = p.scale_log2;   // logit scale of this lane's two heads
+  float v_gain = 1.f;
+  if constexpr (kFp4) {
+    v_gain = __ldg(p.v_gain + hkv);
+    const float k_scale = p.scale_log2 * __ldg(p.k_gain + hkv);
+    const bool have = gid < p.g;
+    const float unit = fp4_query<D>(
+        static_cast<const TQ*>(p.q) + ((size_t)q_row * p.Hq + hkv * p.g + (have ? gid : 0)) * D, have, sm_.qf);
+    sl0 = k_scale * __shfl_sync(0xffffffffu, unit, 8 * tig);       // heads 2 tig and 2 tig + 1
+    sl1 = k_scale * __shfl_sync(0xffffffffu, unit, 8 * tig + 4);
+  } else if constexpr (kMma) {
     const bool have = gid < p.g;
     const T* qrow = static_cast<const T*>(p.q) + ((size_t)q_row * p.Hq + hkv * p.g + (have ? gid : 0)) * D;
 #pragma unroll
@@ -850,8 +875,9 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
     float cc[kChains][4];
 #pragma unroll
     for (int q = 0; q < kChains; ++q) cc[q][0] = cc[q][1] = cc[q][2] = cc[q][3] = 0.f;
+    if constexpr (kFp4) fp4_keys<D, kChains>(kA, kA + 2 * kTile * ROWB, lane, sm_.qf, cc);
 #pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks) {
+    for (int ks = 0; ks < (kFp4 ? 0 : D / 16); ++ks) {
       // chunk 2ks + (lane >> 4) of row `lane & 15`, swizzled: a lane
       // constant for ks % 4 plus 8 chunks per 4 ks
       uint32_t a[4];
@@ -870,12 +896,13 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
   // of work-list entries [tbase, tbase + 16) whose V rows start at vA.
   auto tile_rest = [&](const float cfr[4], uint32_t vA, int tbase, int n_round) {
     // cache positions of keys gid and gid+8 (-1: masked or past the end)
-    const int posA = tbase + gid < n_round ? spos[tbase + gid] : -1;
-    const int posB = tbase + gid + 8 < n_round ? spos[tbase + gid + 8] : -1;
-    const float s0 = posA >= 0 ? cfr[0] * p.scale_log2 : kNegInf;
-    const float s1 = posA >= 0 ? cfr[1] * p.scale_log2 : kNegInf;
-    const float s2 = posB >= 0 ? cfr[2] * p.scale_log2 : kNegInf;
-    const float s3 = posB >= 0 ? cfr[3] * p.scale_log2 : kNegInf;
+    const int uA = tbase + (kFp4 ? fp4_key(gid) : gid);   // row gid of the fragments
+    const int posA = uA < n_round ? spos[uA] : -1;
+    const int posB = uA + 8 < n_round ? spos[uA + 8] : -1;
+    const float s0 = posA >= 0 ? cfr[0] * sl0 : kNegInf;
+    const float s1 = posA >= 0 ? cfr[1] * sl1 : kNegInf;
+    const float s2 = posB >= 0 ? cfr[2] * sl0 : kNegInf;
+    const float s3 = posB >= 0 ? cfr[3] * sl1 : kNegInf;
     if (stores_logits(MODE)) {
       const int atA = logit_pos(posA), atB = logit_pos(posB);
       if (atA >= c.img_start && atA < c.img_start + c.n_img)
@@ -889,11 +916,15 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
     // max and the output scale are updated only when a score exceeds the
     // running max by more than kLazyMax, so most tiles need neither the
     // cross-lane max nor a rescale; probabilities stay below 2^kLazyMax.
-    if (__any_sync(0xffffffffu, s0 > sm_.m[0] + kLazyMax || s2 > sm_.m[0] + kLazyMax ||
-                                    s1 > sm_.m[1] + kLazyMax || s3 > sm_.m[1] + kLazyMax)) {
+    // 4 bits: the running max is kept kHeadroom below the true one, so that the
+    // probabilities use fp16's range (up to 2^(kLazyMax + kHeadroom), and 2^-24 of
+    // the range below is 2^-31 of the largest).
+    constexpr float kHeadroom = kFp4 ? 7.f : 0.f, kLimit = kLazyMax + kHeadroom;
+    if (__any_sync(0xffffffffu, s0 > sm_.m[0] + kLimit || s2 > sm_.m[0] + kLimit ||
+                                    s1 > sm_.m[1] + kLimit || s3 > sm_.m[1] + kLimit)) {
       const float mx0 = warp_max_gid(fmaxf(s0, s2));
       const float mx1 = warp_max_gid(fmaxf(s1, s3));
-      const float mn0 = fmaxf(sm_.m[0], mx0), mn1 = fmaxf(sm_.m[1], mx1);
+      const float mn0 = fmaxf(sm_.m[0], mx0 - kHeadroom), mn1 = fmaxf(sm_.m[1], mx1 - kHeadroom);
       const float al0 = fast_exp2(sm_.m[0] - (mn0 == kNegInf ? 0.f : mn0));
       const float al1 = fast_exp2(sm_.m[1] - (mn1 == kNegInf ? 0.f : mn1));
       sm_.l[0] *= al0;
@@ -928,6 +959,9 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
     if constexpr (kTwoPart) {   // cut off, not rounded: the remainder is then positive
       pk01 = __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
       pk23 = __byte_perm(__float_as_uint(p2), __float_as_uint(p3), 0x7632);
+    } else if constexpr (kFp4) {   // fp16: within 2^-11, and V's values are whole in it
+      pk01 = pack_f16(p0, p1);
+      pk23 = pack_f16(p2, p3);
     } else {
       pk01 = pack_bf16(p0, p1);
       pk23 = pack_bf16(p2, p3);
@@ -941,6 +975,10 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
         sm_.il[0] += (iA ? p0 : 0.f) + (iB ? p2 : 0.f);
         sm_.il[1] += (iA ? p1 : 0.f) + (iB ? p3 : 0.f);
       }
+    } else if constexpr (kFp4) {
+      const float2 r01 = unpack_f16(pk01), r23 = unpack_f16(pk23);
+      sm_.l[0] += r01.x + r23.x;
+      sm_.l[1] += r01.y + r23.y;
     } else {
       sm_.l[0] += __uint_as_float(pk01 << 16) + __uint_as_float(pk23 << 16);
       sm_.l[1] += __uint_as_float(pk01 & 0xffff0000u) + __uint_as_float(pk23 & 0xffff0000u);
@@ -955,8 +993,9 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
       bl0 = movmatrix_trans(pack_bf16(rest(p0), rest(p1)));
       bl1 = movmatrix_trans(pack_bf16(rest(p2), rest(p3)));
     }
+    if constexpr (kFp4) fp4_values<D>(vA, vA + kTile * (ROWB + SM::kScaleBytes), lane, bb0, bb1, sm_.acc);
 #pragma unroll
-    for (int mt = 0; mt < D / 16; ++mt) {
+    for (int mt = 0; mt < (kFp4 ? 0 : D / 16); ++mt) {
       uint32_t a[4];
       ldmatrix_x4_trans(a, vA + voff[mt & 3] + (mt >> 2) * 128);
       // O^T[16 dims x 8 heads] += V^T[16 dims x 16 keys] . P^T[16 keys x 8 heads]
@@ -1191,8 +1230,18 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
         wil[h1] = il1;
       }
     }
+    if constexpr (kFp4) {   // dims D/8 gid + 2 mt and the one after it
 #pragma unroll
-    for (int mt = 0; mt < D / 16; ++mt) {
+      for (int mt = 0; mt < D / 16; mt += 2) {
+        const int at = D / 8 * gid + 2 * mt;
+        *reinterpret_cast<float4*>(wacc + h0 * D + at) = make_float4(
+            sm_.acc[mt][0] * v_gain, sm_.acc[mt][2] * v_gain, sm_.acc[mt + 1][0] * v_gain, sm_.acc[mt + 1][2] * v_gain);
+        *reinterpret_cast<float4*>(wacc + h1 * D + at) = make_float4(
+            sm_.acc[mt][1] * v_gain, sm_.acc[mt][3] * v_gain, sm_.acc[mt + 1][1] * v_gain, sm_.acc[mt + 1][3] * v_gain);
+      }
+    }
+#pragma unroll
+    for (int mt = 0; mt < (kFp4 ? 0 : D / 16); ++mt) {
       wacc[h0 * D + 16 * mt + gid] = sm_.acc[mt][0];
       wacc[h1 * D + 16 * mt + gid] = sm_.acc[mt][1];
       wacc[h0 * D + 16 * mt + 8 + gid] = sm_.acc[mt][2];
@@ -1274,9 +1323,9 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
     for (int w = 0; w < kWarps; ++w) sc[w] = fast_exp2(wm[w * kSlots + h] - base);
     return M;
   };
-  T* outp = static_cast<T*>(p.out) + ((size_t)q_row * p.Hq + (size_t)hkv * p.g) * D;
+  TQ* outp = static_cast<TQ*>(p.out) + ((size_t)q_row * p.Hq + (size_t)hkv * p.g) * D;
   auto store_pair = [&](int e, float4 acc) {   // output dims 4*(e % C4).. of head e / C4
-    T* o = outp + (e / C4) * D + 4 * (e % C4);
+    TQ* o = outp + (e / C4) * D + 4 * (e % C4);
     if constexpr (kMma) {
       uint2 w;
       w.x = pack_bf16(acc.x, acc.y);
@@ -1578,16 +1627,18 @@ cudaError_t prepare_modes() {
   if ((e = prepare_attend(attend_kernel<T, D, kFocal, V>, bytes))) return e;
   if ((e = prepare_attend(attend_kernel<T, D, kSparse, V>, bytes))) return e;
   if ((e = prepare_attend(attend_kernel<T, D, kProfile, V>, bytes))) return e;
-  if ((e = prepare_attend(attend_kernel<T, D, kTail, V>, bytes))) return e;
-  if ((e = prepare_attend(attend_kernel<T, D, kWeigh, V>, bytes))) return e;
-  if ((e = prepare_attend(attend_kernel<T, D, kCross, V>, bytes))) return e;
+  if constexpr (!Held<T>::kFp4) {
+    if ((e = prepare_attend(attend_kernel<T, D, kTail, V>, bytes))) return e;
+    if ((e = prepare_attend(attend_kernel<T, D, kWeigh, V>, bytes))) return e;
+    if ((e = prepare_attend(attend_kernel<T, D, kCross, V>, bytes))) return e;
+  }
   return prepare_attend(attend_kernel<T, D, kRswa, V>, bytes);
 }
 
 template <typename T, int D>
 cudaError_t prepare_all_modes() {
   cudaError_t e;
-  if ((e = prepare_modes<T, D, kGeneral>())) return e;
+  if ((e = prepare_modes<T, D, Held<T>::kGeneralVariant>())) return e;
   if constexpr (variant_fits<T, D, kDeep>())
     if ((e = prepare_modes<T, D, kDeep>())) return e;
   if ((e = cudaFuncSetAttribute(select_kernel<kSelectThreads>,
@@ -1605,7 +1656,7 @@ template <typename T, int D>
 int active_clusters(int c) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(c, 1, 1);
-  cfg.blockDim = dim3(32 * warps_for(kGeneral), 1, 1);
+  cfg.blockDim = dim3(32 * warps_for(Held<T>::kGeneralVariant), 1, 1);
   cfg.dynamicSmemBytes = attend_smem_bytes<T, D>();
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1615,7 +1666,7 @@ int active_clusters(int c) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, attend_kernel<T, D, kFull, kGeneral>, &cfg) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(&n, attend_kernel<T, D, kFull, Held<T>::kGeneralVariant>, &cfg) != cudaSuccess) {
     cudaGetLastError();
     return 0;
   }
@@ -1653,7 +1704,7 @@ int max_cluster_size() {
 template <typename T, int D>
 int max_cluster_of(int variant) {
   switch (variant) {
-    case kGeneral: return max_cluster_size<T, D, kGeneral>();
+    case kGeneral: return max_cluster_size<T, D, Held<T>::kGeneralVariant>();
     case kDeep: return max_cluster_size<T, D, kDeep>();
   }
   return 0;
@@ -1667,6 +1718,8 @@ cudaError_t dispatch_variant(int mode, const Params& p, cudaStream_t s) {
     case kSparse: return launch_attend<T, D, kSparse, V>(p, s);
     case kRswa: return launch_attend<T, D, kRswa, V>(p, s);
     case kProfile: return launch_attend<T, D, kProfile, V>(p, s);
+  }
+  if constexpr (!Held<T>::kFp4) switch (mode) {   // not for a cache in 4 bits: refused on the host
     case kTail: return launch_attend<T, D, kTail, V>(p, s);
     case kWeigh: return launch_attend<T, D, kWeigh, V>(p, s);
     case kCross: return launch_attend<T, D, kCross, V>(p, s);
@@ -1679,7 +1732,7 @@ cudaError_t dispatch_mode(int mode, const Params& p, cudaStream_t s) {
   if constexpr (variant_fits<T, D, kDeep>())
     if (p.variant == kDeep) return dispatch_variant<T, D, kDeep>(mode, p, s);
   if (p.variant != kGeneral) return cudaErrorInvalidValue;
-  return dispatch_variant<T, D, kGeneral>(mode, p, s);
+  return dispatch_variant<T, D, Held<T>::kGeneralVariant>(mode, p, s);
 }
 
 }  // namespace fastocr

@@ -47,10 +47,13 @@ constexpr int kSlots = 8;      // query-head slots per KV head (g <= 8)
 //           more warps stream faster, and 12 stages still fit twice per SM.
 //  kDeep    4 x 6: one CTA per SM, for grids at most half the SM count; a
 //           batch-1 CTA stages its whole share before the wait.
-enum Variant : int { kGeneral = 0, kDeep = 1, kNumVariants = 2 };
-__host__ __device__ constexpr int stages_of(int v) { return v == kDeep ? 6 : 2; }
-__host__ __device__ constexpr int warps_for(int v) { return v == kDeep ? 4 : 6; }
-__host__ __device__ constexpr int ctas_per_sm(int v) { return v == kGeneral ? 2 : 1; }
+//  kPacked  8 x 4: the general variant of a cache in 4 bits, whose tiles hold 2.3 KB
+//           instead of 8: unpacking them, not the bytes in flight, is what more
+//           warps are for.
+enum Variant : int { kGeneral = 0, kDeep = 1, kNumVariants = 2, kPacked = 2 };
+__host__ __device__ constexpr int stages_of(int v) { return v == kDeep ? 6 : (v == kPacked ? 4 : 2); }
+__host__ __device__ constexpr int warps_for(int v) { return v == kDeep ? 4 : (v == kPacked ? 8 : 6); }
+__host__ __device__ constexpr int ctas_per_sm(int v) { return v == kDeep ? 1 : 2; }
 constexpr float kLazyMax = 8.f; // running-max slack (log2 units) before a rescale
 constexpr int kMaxSplits = 16;  // = the largest thread-block cluster used
 constexpr int kMaxImg = 16384; // image tokens whose scores fit in shared memory
@@ -73,12 +76,40 @@ constexpr int kDevBadSelection = 8;
 constexpr int kDevInternal = 16;   // a cache row outside the cache reached a copy
 constexpr int kDevBadGroup = 32;
 constexpr int kDevBadWeights = 64;
+constexpr int kDevBadPosition = 128;
+constexpr int kDevNoPages = 256;
+constexpr int kDevBadPool = 512;
+
+// How K and V are held: T is the type of their elements, or Fp4, whose q and out are bf16.
+struct Fp4 {};
+template <typename T>
+struct Held {
+  using Q = T;
+  static constexpr bool kFp4 = false;
+  static constexpr bool kMma = sizeof(T) == 2;       // tensor-core contraction
+  static constexpr int kGeneralVariant = kGeneral;
+  static constexpr int row_bytes(int d) { return d * (int)sizeof(T); }
+  static constexpr int scale_bytes(int) { return 0; }
+};
+template <>
+struct Held<Fp4> {
+  using Q = __nv_bfloat16;
+  static constexpr bool kFp4 = true;
+  static constexpr bool kMma = true;
+  static constexpr int kGeneralVariant = kPacked;
+  static constexpr int row_bytes(int d) { return d / 2; }       // two codes a byte
+  static constexpr int scale_bytes(int d) { return d / 16; }    // one e4m3 a group of 16
+};
 
 struct Params {
   const void* q;
   void* out;
   const void* k;
   const void* v;
+  const uint8_t* k_scale;    // 4 bits: e4m3 scales of the rows' groups
+  const uint8_t* v_scale;
+  const float* k_gain;       // 4 bits: [H_kv]
+  const float* v_gain;
   const int32_t* block_table;
   const int32_t* seq_len;
   int num_pages, max_pages, log2_page;
@@ -176,6 +207,13 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t r[4], uint32_t addr) 
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr));
 }
+// cp.async16 with 4 or 8 bytes.
+template <int BYTES>
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, int src_bytes, uint64_t pol) {
+  asm volatile("cp.async.ca.shared.global.L2::cache_hint [%0], [%1], %2, %3, %4;\n" ::"r"(dst), "l"(src),
+               "n"(BYTES), "r"(src_bytes), "l"(pol)
+               : "memory");
+}
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
   uint32_t y;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
@@ -188,6 +226,13 @@ __device__ __forceinline__ void mma_bf16(float c[4], const uint32_t a[4], uint32
                                          uint32_t b1) {
   asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, "
+      "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16(float c[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, "
       "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -224,6 +269,10 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
 // Bring `bytes` (multiple of 16) at `p` into L2; never faults on a valid address.
 __device__ __forceinline__ void prefetch_l2(const void* ptr, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;\n" ::"l"(ptr), "r"(bytes) : "memory");
+}
+// Bring the line at `p` into L2 (no alignment or size to keep).
+__device__ __forceinline__ void prefetch_l2_line(const void* ptr) {
+  asm volatile("prefetch.global.L2 [%0];\n" ::"l"(ptr) : "memory");
 }
 // 2^x on the special-function unit (x = -inf gives +0).
 __device__ __forceinline__ float fast_exp2(float x) {
@@ -302,16 +351,18 @@ __device__ __forceinline__ AttendList make_list(const Params& p, int b, int& bad
 
 // Work-list entries resolved to cache rows per round: a multiple of the CTA
 // size (every thread resolves the same number).
-__host__ __device__ constexpr int slice_for(int v) { return v == kDeep ? 1024 : 960; }
+__host__ __device__ constexpr int slice_for(int v) { return v == kGeneral ? 960 : 1024; }
 
-template <typename T, int D, int V = kGeneral>
+template <typename T, int D, int V = Held<T>::kGeneralVariant>
 struct Smem {
   static constexpr int ST = stages_of(V);
   static constexpr int kWarps = warps_for(V);
   static constexpr int kSliceMax = slice_for(V);
   static_assert(kSliceMax % (32 * kWarps) == 0 && kSliceMax % kTile == 0, "slice layout");
-  static constexpr int kRowBytes = D * (int)sizeof(T);
-  static constexpr int kStageBytes = 2 * kTile * kRowBytes;          // K rows then V rows
+  static constexpr int kRowBytes = Held<T>::row_bytes(D);
+  static constexpr int kScaleBytes = Held<T>::scale_bytes(D);
+  // K rows then V rows (4 bits: then K's scales, then V's)
+  static constexpr int kStageBytes = 2 * kTile * (kRowBytes + kScaleBytes);
   static constexpr int kPipeBytes = kWarps * ST * kStageBytes;
   static constexpr int kRowOffset = kPipeBytes;                      // int row[kSliceMax]
   static constexpr int kPosOffset = kRowOffset + kSliceMax * 4;      // int pos[kSliceMax]
@@ -323,7 +374,7 @@ struct Smem {
   // the CTA's one reading of k before the wait (sparse), shared by its threads
   static constexpr int kSpecK = kRecvAcc + kRecvAccFloats * 4;
   static constexpr int kQOffset = kSpecK + 16;                       // f32 path: q[8][D]
-  static constexpr int kMainBytes = kQOffset + (sizeof(T) == 4 ? kSlots * D * 4 : 0);
+  static constexpr int kMainBytes = kQOffset + (Held<T>::kMma ? 0 : kSlots * D * 4);
 };
 
 template <int D, int kWarps>
@@ -341,7 +392,7 @@ struct EpiSmem {
   static constexpr int kBytes = kExt + kSlots * kMaxExt * 8;
 };
 
-template <typename T, int D, int V = kGeneral>
+template <typename T, int D, int V = Held<T>::kGeneralVariant>
 inline int attend_smem_bytes() {
   static_assert(EpiSmem<D, warps_for(V)>::kBytes <= Smem<T, D, V>::kPipeBytes,
                 "epilogue must fit the pipeline area");
@@ -352,6 +403,7 @@ inline int attend_smem_bytes() {
 // always does; bf16 fits it twice an SM).
 template <typename T, int D, int V>
 constexpr bool variant_fits() {
+  if (Held<T>::kFp4) return V == Held<T>::kGeneralVariant;
   return Smem<T, D, V>::kMainBytes <= 227 * 1024;
 }
 

@@ -1,0 +1,56 @@
+// Rows of a paged cache written (with rotary positions) and read back: parameters and
+// launches of cache_rows.cu.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace fastocr {
+
+// What both kernels know of the cache and of whose the packed tokens are.
+struct CacheRows {
+  char* k;                 // codes, or elements
+  char* v;
+  uint8_t* k_scale;        // 4 bits only
+  uint8_t* v_scale;
+  const float* k_gain;
+  const float* v_gain;
+  const int32_t* block_table;
+  const int32_t* seq_len;
+  const int32_t* start;    // [B + 1]: tokens start[b] .. start[b+1]-1 are sequence b's; NULL: token b is
+  int num_pages, max_pages, log2_page, B, Hkv;
+  int tokens;
+  int32_t* status;
+};
+
+struct WriteParams {
+  CacheRows c;
+  const char* q;           // NULL: none
+  const char* k;
+  const char* v;
+  char* q_out;
+  long q_stride, k_stride, v_stride;   // bytes from token to token
+  int Hq;
+  const float* cos_sin;    // [positions, rotary / 2, 2]
+  const int8_t* axis;      // [rotary / 2]
+  const int32_t* pos;      // [axes, tokens]
+  int positions, rotary, axes, adjacent;
+  int slots;               // threads groups that share a token's heads
+  int single;              // one token a sequence
+};
+
+struct ReadParams {
+  CacheRows c;
+  char* k_out;             // [tokens, H_kv, d]
+  char* v_out;
+  int out_f32;
+};
+
+// dtype: FASTOCR_DTYPE_*; head_dim 64 or 128
+cudaError_t launch_write_rows(int dtype, int head_dim, int num_sms, WriteParams p, cudaStream_t s);
+cudaError_t launch_read_rows(int dtype, int head_dim, const ReadParams& p, cudaStream_t s);
+// An empty kernel that ends once everything before it on the stream is complete: the kernel
+// behind it may read, before its own wait, whatever was written before.
+cudaError_t launch_fence(cudaStream_t s);
+
+}  // namespace fastocr

@@ -1,0 +1,184 @@
+// Cache rows held in 4 bits: the format, and how the decode-attention kernel reads it.
+//
+// A row is d codes of 4 bits (e2m1; dimension 2i in the low half of byte i) and d / 16
+// scales of 8 bits (e4m3), one a group of 16 dimensions; an element stands for
+// e2m1 * e4m3 * gain of its KV head. The product e2m1 * e4m3 has at most 6 significant
+// bits and lies in [2^-10, 2688] or is 0, so it is whole in fp16: both contractions take
+// the values themselves, and only the probabilities are rounded.
+//
+// Tensor-core layout (mma m16n8k16, keys or dims on M, query heads on N). Neither the
+// order of the keys of a tile nor that of the dimensions inside a contraction matters,
+// so both are chosen for the loads: in S^T = K Q^T lane (gid, tig) takes a contiguous
+// quarter of rows fp4_key(gid) and fp4_key(gid) + 8 (one 16-byte load each at d = 128),
+// in O^T = V^T P^T the dims D/8 gid .. of keys tig, tig + 4, tig + 8, tig + 12.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "attend_kernels.cuh"
+
+namespace fastocr {
+
+// Byte offset of 16-byte chunk c of tile row r: 128-byte lines of 2 (d = 128) or 4 rows,
+// chunks exchanged so that neither access pattern meets a bank twice.
+template <int D>
+__device__ __forceinline__ uint32_t fp4_place(int r, int c) {
+  if constexpr (D == 128)
+    return (r >> 1) * 128 + (((((r & 1) << 2) | c) ^ (r & 6)) << 4);
+  else
+    return (r >> 2) * 128 + (((((r & 3) << 1) | c) ^ (((r >> 2) & 1) << 2)) << 4);
+}
+
+// Tile row that stands in row i < 8 of the first product (row i + 8: 8 further), so that
+// columns 2t, 2t + 1 of the second are keys t and t + 4.
+__device__ __forceinline__ int fp4_key(int i) { return (i >> 1) + ((i & 1) << 2); }
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float2 unpack_f16(uint32_t x) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&x));
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// The four bytes of w (two codes each, the low one first) as pairs of fp16.
+__device__ __forceinline__ void fp4_decode8(uint32_t w, uint32_t h[4]) {
+  asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %4;\n cvt.rn.f16x2.e2m1x2 %0, a;\n"
+      " cvt.rn.f16x2.e2m1x2 %1, b;\n cvt.rn.f16x2.e2m1x2 %2, c;\n cvt.rn.f16x2.e2m1x2 %3, d;\n}\n"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+// Two e4m3 in the low 16 bits as a pair of fp16.
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t x) {
+  uint32_t h;
+  asm("{\n .reg .b16 a;\n cvt.u16.u32 a, %1;\n cvt.rn.f16x2.e4m3x2 %0, a;\n}\n" : "=r"(h) : "r"(x));
+  return h;
+}
+
+// This lane's share of query row q (head gid) as fp16 fragments, divided by a power of
+// two that brings the row's largest element into [1, 2) (fp16 keeps every bf16 element
+// down to 2^-14 of it whole); returns that power.
+template <int D>
+__device__ __forceinline__ float fp4_query(const __nv_bfloat16* q, bool have, uint32_t (&qf)[D / 16][2]) {
+  constexpr int N = D / 4;   // dims a lane: its quarter of the row
+  const int tig = threadIdx.x & 3;
+  uint4 raw[N / 8];
+#pragma unroll
+  for (int i = 0; i < N / 8; ++i)
+    raw[i] = have ? __ldcg(reinterpret_cast<const uint4*>(q + N * tig) + i) : make_uint4(0, 0, 0, 0);
+  uint32_t w[N / 2];
+#pragma unroll
+  for (int i = 0; i < N / 8; ++i) {
+    w[4 * i] = raw[i].x;
+    w[4 * i + 1] = raw[i].y;
+    w[4 * i + 2] = raw[i].z;
+    w[4 * i + 3] = raw[i].w;
+  }
+  uint32_t top = 0;   // the largest magnitude's bits (bf16 in the upper half)
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) top = max(top, max((w[i] << 16) & 0x7fff0000u, w[i] & 0x7fff0000u));
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  const uint32_t e = min(max(top >> 23, 1u), 253u);
+  const float down = __uint_as_float((254u - e) << 23);
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i)
+    qf[i >> 1][i & 1] = pack_f16(__uint_as_float(w[i] << 16) * down, __uint_as_float(w[i] & 0xffff0000u) * down);
+  return __uint_as_float(e << 23);
+}
+
+// Partial S^T of a tile: K codes at shared address kA, their scales at sA.
+template <int D, int CHAINS>
+__device__ __forceinline__ void fp4_keys(uint32_t kA, uint32_t sA, int lane, const uint32_t (&qf)[D / 16][2],
+                                         float (&cc)[CHAINS][4]) {
+  const int gid = lane >> 2, tig = lane & 3;
+  const int r0 = fp4_key(gid);
+  constexpr int W = D / 32;   // 32-bit words of codes a row gives a lane
+  uint32_t w0[W], w1[W], s0[2], s1[2];
+  if constexpr (D == 128) {
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(w0[0]), "=r"(w0[1]), "=r"(w0[2]), "=r"(w0[3]) : "r"(kA + fp4_place<D>(r0, tig)));
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(w1[0]), "=r"(w1[1]), "=r"(w1[2]), "=r"(w1[3]) : "r"(kA + fp4_place<D>(r0 + 8, tig)));
+    uint16_t a, b;   // groups 2 tig and 2 tig + 1
+    asm volatile("ld.shared.u16 %0, [%1];\n" : "=h"(a) : "r"(sA + r0 * 8 + 2 * tig));
+    asm volatile("ld.shared.u16 %0, [%1];\n" : "=h"(b) : "r"(sA + (r0 + 8) * 8 + 2 * tig));
+    const uint32_t x = e4m3_pair(a), y = e4m3_pair(b);
+    s0[0] = __byte_perm(x, x, 0x1010);
+    s0[1] = __byte_perm(x, x, 0x3232);
+    s1[0] = __byte_perm(y, y, 0x1010);
+    s1[1] = __byte_perm(y, y, 0x3232);
+  } else {
+    const uint32_t half = (tig & 1) * 8;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];\n"
+                 : "=r"(w0[0]), "=r"(w0[1]) : "r"(kA + fp4_place<D>(r0, tig >> 1) + half));
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];\n"
+                 : "=r"(w1[0]), "=r"(w1[1]) : "r"(kA + fp4_place<D>(r0 + 8, tig >> 1) + half));
+    uint16_t a, b;   // group tig
+    asm volatile("{\n .reg .b8 t;\n ld.shared.u8 t, [%1];\n cvt.u16.u8 %0, t;\n}\n" : "=h"(a) : "r"(sA + r0 * 4 + tig));
+    asm volatile("{\n .reg .b8 t;\n ld.shared.u8 t, [%1];\n cvt.u16.u8 %0, t;\n}\n" : "=h"(b) : "r"(sA + (r0 + 8) * 4 + tig));
+    s0[0] = s0[1] = e4m3_pair(a | (a << 8));
+    s1[0] = s1[1] = e4m3_pair(b | (b << 8));
+  }
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    uint32_t h0[4], h1[4];
+    fp4_decode8(w0[i], h0);
+    fp4_decode8(w1[i], h1);
+    const int g = D == 128 ? i >> 1 : 0;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int ks = 2 * i + j;
+      const uint32_t a[4] = {mul_f16x2(h0[2 * j], s0[g]), mul_f16x2(h1[2 * j], s1[g]),
+                             mul_f16x2(h0[2 * j + 1], s0[g]), mul_f16x2(h1[2 * j + 1], s1[g])};
+      mma_f16(cc[ks % CHAINS], a, qf[ks][0], qf[ks][1]);
+    }
+  }
+}
+
+// O^T += V^T P^T of a tile: V codes at shared address vA, their scales at sA, the
+// probabilities' fragments in b0 (keys 2t, 2t + 1 of fp4_key's order) and b1 (8 further).
+// acc[mt]: dims D/8 gid + 2 mt (elements 0, 1) and the one after it (2, 3).
+template <int D>
+__device__ __forceinline__ void fp4_values(uint32_t vA, uint32_t sA, int lane, uint32_t b0, uint32_t b1,
+                                           float (&acc)[D / 16][4]) {
+  const int gid = lane >> 2, tig = lane & 3;
+  constexpr int W = D / 64;   // words a key gives a lane: D / 8 codes
+  uint32_t w[4][W];
+  uint32_t s[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int r = tig + 4 * j;
+    if constexpr (D == 128) {
+      asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];\n"
+                   : "=r"(w[j][0]), "=r"(w[j][1]) : "r"(vA + fp4_place<D>(r, gid >> 1) + (gid & 1) * 8));
+      asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(s[j]) : "r"(sA + r * 8 + gid));
+    } else {
+      asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(w[j][0]) : "r"(vA + fp4_place<D>(r, gid >> 2) + (gid & 3) * 4));
+      asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(s[j]) : "r"(sA + r * 4 + (gid >> 1)));
+    }
+  }
+  const uint32_t s01 = e4m3_pair(s[0] | (s[1] << 8)), s23 = e4m3_pair(s[2] | (s[3] << 8));
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    // codes of the same dim of two keys side by side: even dims, then odd ones
+    constexpr uint32_t M = 0x0f0f0f0fu;
+    uint32_t e01[4], o01[4], e23[4], o23[4];
+    fp4_decode8((w[0][i] & M) | ((w[1][i] << 4) & ~M), e01);
+    fp4_decode8(((w[0][i] >> 4) & M) | (w[1][i] & ~M), o01);
+    fp4_decode8((w[2][i] & M) | ((w[3][i] << 4) & ~M), e23);
+    fp4_decode8(((w[2][i] >> 4) & M) | (w[3][i] & ~M), o23);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t a[4] = {mul_f16x2(e01[j], s01), mul_f16x2(o01[j], s01), mul_f16x2(e23[j], s23),
+                             mul_f16x2(o23[j], s23)};
+      mma_f16(acc[4 * i + j], a, b0, b1);
+    }
+  }
+}
+
+}  // namespace fastocr

@@ -12,14 +12,18 @@
 
 namespace fastocr {
 cudaError_t launch_bf16(int head_dim, int mode, const Params& p, cudaStream_t s);
+cudaError_t launch_fp4(int head_dim, int mode, const Params& p, cudaStream_t s);
 cudaError_t launch_f32(int head_dim, int mode, const Params& p, cudaStream_t s);
 cudaError_t launch_select(const Params& p, cudaStream_t s);
 cudaError_t prepare_bf16();
 cudaError_t prepare_f32();
+cudaError_t prepare_fp4();
 int max_cluster_bf16(int head_dim, int variant);
 int max_cluster_f32(int head_dim, int variant);
+int max_cluster_fp4(int head_dim, int variant);
 int active_clusters_bf16(int head_dim, int cluster);
 int active_clusters_f32(int head_dim, int cluster);
+int active_clusters_fp4(int head_dim, int cluster);
 }  // namespace fastocr
 
 struct fastocr_handle {
@@ -86,14 +90,29 @@ inline long expected_tokens(const fastocr_handle* h) {
   return h->len_hint > 0 ? std::min(h->len_hint, max_tokens(h)) : max_tokens(h);
 }
 
+// scales of 4 bits: a row of them is read at once
+inline bool aligned_scales(const fastocr_handle* h, const void* p) {
+  return reinterpret_cast<uintptr_t>(p) % (h->dims.head_dim / 16) == 0;
+}
+
 inline fastocr_status check_kv(const fastocr_handle* h, const fastocr_kv* kv) {
   if (!kv || !kv->k || !kv->v || !kv->block_table || !kv->seq_len) return FASTOCR_ERR_NULL;
   if (kv->num_pages < 1) return FASTOCR_ERR_INVALID;
   if (!aligned16(kv->k) || !aligned16(kv->v)) return FASTOCR_ERR_ALIGN;
+  if (h->dims.dtype == FASTOCR_DTYPE_FP4) {
+    if (!kv->k_scale || !kv->v_scale || !kv->k_gain || !kv->v_gain) return FASTOCR_ERR_NULL;
+    if (!aligned_scales(h, kv->k_scale) || !aligned_scales(h, kv->v_scale)) return FASTOCR_ERR_ALIGN;
+  }
   // cache rows are indexed with 32-bit integers inside the kernels
   if ((long long)kv->num_pages * h->dims.num_kv_heads * h->dims.page_size >= (1LL << 31))
     return FASTOCR_ERR_UNSUPPORTED;
   return FASTOCR_OK;
+}
+
+inline fastocr_status check_device(const fastocr_handle* h) {
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return FASTOCR_ERR_NO_DEVICE;
+  return dev == h->device ? FASTOCR_OK : FASTOCR_ERR_INVALID;
 }
 
 inline Params base_params(const fastocr_handle* h, const void* q, const fastocr_kv* kv, void* out) {
@@ -104,6 +123,12 @@ inline Params base_params(const fastocr_handle* h, const void* q, const fastocr_
   p.out = out;
   p.k = kv->k;
   p.v = kv->v;
+  if (d.dtype == FASTOCR_DTYPE_FP4) {
+    p.k_scale = static_cast<const uint8_t*>(kv->k_scale);
+    p.v_scale = static_cast<const uint8_t*>(kv->v_scale);
+    p.k_gain = kv->k_gain;
+    p.v_gain = kv->v_gain;
+  }
   p.block_table = kv->block_table;
   p.seq_len = kv->seq_len;
   p.num_pages = kv->num_pages;
@@ -131,8 +156,10 @@ inline fastocr_status launch(const fastocr_handle* h, int mode, long len, Params
                       fastocr_stream stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   plan_launch(h, mode, len, p);
-  cudaError_t e = h->dims.dtype == FASTOCR_DTYPE_BF16 ? launch_bf16(h->dims.head_dim, mode, p, s)
-                                                       : launch_f32(h->dims.head_dim, mode, p, s);
+  const int D = h->dims.head_dim;
+  const cudaError_t e = h->dims.dtype == FASTOCR_DTYPE_BF16  ? launch_bf16(D, mode, p, s)
+                        : h->dims.dtype == FASTOCR_DTYPE_FP4 ? launch_fp4(D, mode, p, s)
+                                                             : launch_f32(D, mode, p, s);
   return e == cudaSuccess ? FASTOCR_OK : FASTOCR_ERR_CUDA;
 }
 

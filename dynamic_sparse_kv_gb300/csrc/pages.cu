@@ -1,0 +1,554 @@
+// Pages of a paged cache change hands: reserved, shared by forked sequences, released,
+// moved together. All state (block table, lengths, pages held, references) lives on the
+// device, and nothing is read back, so a decode loop whose lengths the host does not know
+// (eviction) and a captured step can use it.
+//
+// A call is one planning kernel over the table and the references, integers only and with
+// the lowest free page first, so that the result does not depend on any order of threads;
+// where pages move, a copy kernel over (page, layer, array) pieces follows. The plans of
+// reserve and compact are one CTA: their work is two or three dependent passes over the
+// references (64 KB for 16384 pages, 32 words a thread and pass), which a barrier between
+// CTAs would lengthen.
+#include <algorithm>
+
+#include "attend_kernels.cuh"
+#include "cache_rows.cuh"
+#include "pages.cuh"
+
+namespace fastocr {
+namespace {
+
+constexpr int kPlan = 1024;          // threads of the planning kernels
+constexpr int kWarps = kPlan / 32;
+constexpr int kPer = 16;             // references a lane looks at in one pass
+constexpr int kPass = kPlan * kPer;
+constexpr int kPiece = 4096;         // bytes a warp copies at once
+
+__device__ __forceinline__ void pool_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+__device__ __forceinline__ void pool_release_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+}
+
+__device__ __forceinline__ int pages_of(const PoolParams& p, int rows) {
+  return (int)(((long)rows + (1 << p.log2_page) - 1) >> p.log2_page);
+}
+
+// Length of sequence b and the pages it holds, inside their bounds.
+__device__ __forceinline__ int length_of(const PoolParams& p, int b, int& bad) {
+  const int n = __ldcg(p.seq_len + b), cap = p.max_pages << p.log2_page;
+  if (n >= 0 && n <= cap) return n;
+  bad |= kDevBadSeqLen;
+  return n < 0 ? 0 : cap;
+}
+__device__ __forceinline__ int held_of(const PoolParams& p, int b, int& bad) {
+  const int h = __ldcg(p.held + b);
+  if (h >= 0 && h <= p.max_pages) return h;
+  bad |= kDevBadPool;
+  return h < 0 ? 0 : p.max_pages;
+}
+
+// One reference to a page more or less; a page out of range, or one that nobody refers
+// to, is reported.
+__device__ __forceinline__ void add_ref(const PoolParams& p, int page, int& bad) {
+  if (page < 0 || page >= p.num_pages)
+    bad |= kDevBadPage;
+  else
+    atomicAdd(p.refs + page, 1);
+}
+__device__ __forceinline__ void drop_ref(const PoolParams& p, int page, int& bad) {
+  if (page < 0 || page >= p.num_pages) {
+    bad |= kDevBadPage;
+  } else if (atomicSub(p.refs + page, 1) <= 0) {
+    atomicAdd(p.refs + page, 1);
+    bad |= kDevBadPool;
+  }
+}
+
+// Exclusive prefix of x over the CTA's warps (x the same in all lanes of a warp), and the
+// total; two barriers.
+__device__ __forceinline__ int scan_warps(int x, int* s_warp, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (lane == 0) s_warp[warp] = x;
+  __syncthreads();
+  const int mine = s_warp[lane];   // kWarps == 32
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  total = __shfl_sync(0xffffffffu, incl, 31);
+  const int before = __shfl_sync(0xffffffffu, incl - mine, warp);
+  __syncthreads();
+  return before;
+}
+
+// The references of one pass, 32 * kPer consecutive ones a warp: bit `lane` of free[i] is
+// whether page base + 32 i + lane exists and is free.
+__device__ __forceinline__ int free_masks(const PoolParams& p, long base, uint32_t free[kPer]) {
+  const int lane = threadIdx.x & 31;
+  int r[kPer], n = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const long page = base + 32 * i + lane;
+    r[i] = page < p.num_pages ? __ldcg(p.refs + page) : 1;
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    free[i] = __ballot_sync(0xffffffffu, r[i] <= 0);
+    n += __popc(free[i]);
+  }
+  return n;
+}
+
+// Columns of sequence b's table that reserve looks at: [first, need), of which those below
+// `held` have a page. Pages that hold rows below the length only are not among them.
+struct Want {
+  int first, need, held, len;
+};
+__device__ __forceinline__ Want want_of(const PoolParams& p, const int32_t* rows, int extra, int b, int& bad) {
+  Want w;
+  w.len = length_of(p, b, bad);
+  w.held = held_of(p, b, bad);
+  const int cap = p.max_pages << p.log2_page;
+  long r = rows ? (long)__ldcg(rows + b) : (long)w.len + extra;
+  if (r > cap) {
+    bad |= kDevBadSeqLen;
+    r = cap;
+  }
+  w.need = pages_of(p, r < 0 ? 0 : (int)r);
+  w.first = min(w.len >> p.log2_page, w.held);
+  return w;
+}
+
+// Reserve. Every wanted column without a page gets one, and so does a wanted column whose
+// page is shared, for its rows are about to be written: of the pages' holders all but one
+// move to a fresh page, the one being the first of them where every holder is here, and
+// none where somebody else keeps the page. A page that holds rows below the length is
+// copied. Fresh pages go out in order of sequence and column.
+__global__ void __launch_bounds__(kPlan) reserve_kernel(const PoolParams p, const int32_t* rows, int extra,
+                                                        int32_t* missing) {
+  __shared__ int s_warp[32];
+  __shared__ int s_bad;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int bad = 0;
+  if (tid == 0) s_bad = 0;
+  pool_wait();
+  pool_release_dependents();   // the copy kernel waits for this grid
+  // how many wanted columns refer to a shared page, and the first of them; only the
+  // entries of pages looked at are cleared
+  auto each_shared = [&](auto&& f) {
+    for (int b = warp; b < p.B; b += kWarps) {
+      int ignored = 0;
+      const Want w = want_of(p, rows, extra, b, ignored);
+      const int32_t* row = p.table + (size_t)b * p.max_pages;
+      for (int c = w.first + lane; c < min(w.need, w.held); c += 32) {
+        const int page = __ldcg(row + c);
+        if (page >= 0 && page < p.num_pages && __ldcg(p.refs + page) > 1) f(page, b * p.max_pages + c);
+      }
+    }
+  };
+  each_shared([&](int page, int) {
+    __stcg(p.want + page, 0);
+    __stcg(p.lead + page, 0x7fffffff);
+  });
+  __syncthreads();
+  each_shared([&](int page, int at) {
+    atomicAdd(p.want + page, 1);
+    atomicMin(p.lead + page, at);
+  });
+  __syncthreads();
+  // whether column c of sequence b gets a fresh page; old: the page it gives up, or -1
+  auto fresh = [&](const Want& w, int b, int c, int& old, int& bad) -> bool {
+    old = -1;
+    if (c >= w.need) return false;
+    if (c >= w.held) return true;
+    const int page = __ldcg(p.table + (size_t)b * p.max_pages + c);
+    if (page < 0 || page >= p.num_pages) {
+      bad |= kDevBadPage;
+      return true;
+    }
+    const int refs = __ldcg(p.refs + page);
+    if (refs <= 1 || (__ldcg(p.want + page) == refs && __ldcg(p.lead + page) == b * p.max_pages + c)) return false;
+    old = page;
+    return true;
+  };
+  for (int b = warp; b < p.B; b += kWarps) {
+    const Want w = want_of(p, rows, extra, b, bad);
+    int n = 0;
+    for (int c0 = w.first; c0 < w.need; c0 += 32) {
+      int old;
+      n += __popc(__ballot_sync(0xffffffffu, fresh(w, b, c0 + lane, old, bad)));
+    }
+    if (lane == 0) __stcg(p.count + b, n);
+  }
+  __syncthreads();
+  // counts -> first indices, kPlan sequences a pass
+  int total = 0;
+  for (int b0 = 0; b0 < p.B; b0 += kPlan) {
+    const int b = b0 + tid;
+    const int n = b < p.B ? __ldcg(p.count + b) : 0;
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    int sum;
+    const int before = scan_warps(__shfl_sync(0xffffffffu, incl, 31), s_warp, sum);
+    if (b < p.B) __stcg(p.count + b, total + before + incl - n);
+    total += sum;
+  }
+  // the lowest `total` free pages
+  int found = 0;
+  for (long base = 0; base < p.num_pages && found < total; base += kPass) {
+    uint32_t free[kPer];
+    const long mine = base + (long)warp * 32 * kPer;
+    const int n = free_masks(p, mine, free);
+    int sum;
+    int at = found + scan_warps(n, s_warp, sum);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int r = at + __popc(free[i] & ((1u << lane) - 1));
+      if ((free[i] >> lane & 1) && r < total) __stcg(p.list + r, (int)(mine + 32 * i + lane));
+      at += __popc(free[i]);
+    }
+    found += sum;
+  }
+  if (bad) atomicOr(&s_bad, bad);
+  __syncthreads();
+  const int lacking = max(0, total - found);
+  if (tid == 0) {
+    __stcg(p.head, lacking ? 0 : p.B);
+    __stcg(p.head + 1, 0);
+    if (missing) __stcg(missing, lacking);
+    if (s_bad || lacking) atomicOr(p.status, s_bad | (lacking ? kDevNoPages : 0));
+  }
+  if (lacking) return;   // all or nothing
+  // Hand them out; the references change once every sequence has looked at them.
+  for (int b = warp; b < p.B; b += kWarps) {
+    int ignored = 0;
+    const Want w = want_of(p, rows, extra, b, ignored);
+    int at = __ldcg(p.count + b);
+    int32_t* row = p.table + (size_t)b * p.max_pages;
+    if (lane == 0) __stcg(p.src + b, -1);
+    __syncwarp();
+    for (int c0 = w.first; c0 < w.need; c0 += 32) {
+      const int c = c0 + lane;
+      int old;
+      const bool take = fresh(w, b, c, old, ignored);
+      const uint32_t mask = __ballot_sync(0xffffffffu, take);
+      if (take) {
+        const int r = at + __popc(mask & ((1u << lane) - 1));
+        const int page = __ldcg(p.list + r);
+        __stcg(p.old + r, old);
+        __stcg(row + c, page);
+        if (old >= 0 && ((long)c << p.log2_page) < w.len) {   // one column at most: that of row `len`
+          __stcg(p.src + b, old);
+          __stcg(p.dst + b, page);
+        }
+      }
+      at += __popc(mask);
+    }
+    if (lane == 0 && w.need > w.held) __stcg(p.held + b, w.need);
+  }
+  __syncthreads();
+  int late = 0;
+  for (int r = tid; r < total; r += kPlan) {
+    __stcg(p.refs + __ldcg(p.list + r), 1);
+    const int old = __ldcg(p.old + r);
+    if (old >= 0) drop_ref(p, old, late);
+  }
+  if (late) atomicOr(p.status, late);
+}
+
+// Fork: sequence dst[i] gets the pages of src[i] that hold rows, and its length. A pair out
+// of range, one whose target an earlier pair has, and one whose source or target is the
+// other side of any pair is reported and left out.
+__global__ void __launch_bounds__(256) fork_kernel(const PoolParams p, const int32_t* src, const int32_t* dst, int n) {
+  pool_wait();
+  pool_release_dependents();
+  const int i = blockIdx.x, tid = threadIdx.x;
+  const int from = __ldcg(src + i), to = __ldcg(dst + i);
+  int bad = 0;
+  bool no = from < 0 || from >= p.B || to < 0 || to >= p.B || from == to;
+  for (int x = tid; x < n; x += 256) {
+    const int fx = __ldcg(src + x), tx = __ldcg(dst + x);
+    no |= (x < i && tx == to) || (x != i && (tx == from || fx == to));
+  }
+  if (__syncthreads_or(no)) {
+    if (tid == 0) atomicOr(p.status, kDevBadGroup);
+    return;
+  }
+  const int len = length_of(p, from, bad), had = held_of(p, to, bad), has = held_of(p, from, bad);
+  int take = pages_of(p, len);
+  if (take > has) {
+    bad |= kDevBadPool;
+    take = has;
+  }
+  const int32_t* a = p.table + (size_t)from * p.max_pages;
+  int32_t* b = p.table + (size_t)to * p.max_pages;
+  for (int c = tid; c < p.max_pages; c += 256) {
+    const int page = c < take ? __ldcg(a + c) : -1;
+    if (c < had) drop_ref(p, __ldcg(b + c), bad);
+    if (c < take) add_ref(p, page, bad);
+    __stcg(b + c, page);
+  }
+  __syncthreads();   // every thread has read the lengths
+  if (tid == 0) {
+    __stcg(p.held + to, take);
+    __stcg(p.seq_len + to, len);
+  }
+  if (bad) atomicOr(p.status, bad);
+}
+
+// Release: the pages of sequences seqs[i] (NULL: none of them, but of every sequence the
+// pages behind its rows). A sequence named twice is released once.
+__global__ void __launch_bounds__(256) release_kernel(const PoolParams p, const int32_t* seqs) {
+  pool_wait();
+  pool_release_dependents();
+  const int i = blockIdx.x, tid = threadIdx.x;
+  int bad = 0;
+  const int b = seqs ? __ldcg(seqs + i) : i;
+  bool no = b < 0 || b >= p.B;
+  if (no && tid == 0) atomicOr(p.status, kDevBadGroup);
+  if (seqs)
+    for (int x = tid; x < i; x += 256) no |= __ldcg(seqs + x) == b;
+  if (__syncthreads_or(no)) return;
+  const int had = held_of(p, b, bad);
+  const int keep = seqs ? 0 : min(had, pages_of(p, length_of(p, b, bad)));
+  int32_t* row = p.table + (size_t)b * p.max_pages;
+  for (int c = keep + tid; c < had; c += 256) {
+    drop_ref(p, __ldcg(row + c), bad);
+    __stcg(row + c, -1);
+  }
+  __syncthreads();
+  if (tid == 0) {
+    __stcg(p.held + b, keep);
+    if (seqs) __stcg(p.seq_len + b, 0);
+  }
+  if (bad) atomicOr(p.status, bad);
+}
+
+// Compact: with U pages in use, the i-th used page at or behind U moves into the i-th free
+// page before it. Leaves the moves (list: the free pages before the border; src: the used
+// pages by their rank among all used ones) and swaps their references; the copy kernel
+// moves the rows and renames the pages in the table.
+__global__ void __launch_bounds__(kPlan) compact_kernel(const PoolParams p, int32_t* used_out) {
+  __shared__ int s_warp[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pool_wait();
+  pool_release_dependents();
+  int free_all = 0;
+  for (long base = 0; base < p.num_pages; base += kPass) {
+    uint32_t free[kPer];
+    const int n = free_masks(p, base + (long)warp * 32 * kPer, free);
+    int sum;
+    scan_warps(n, s_warp, sum);
+    free_all += sum;
+  }
+  const int border = p.num_pages - free_all;
+  int before = 0, holes_mine = 0;   // free pages of earlier passes; free pages below the border this lane saw
+  for (long base = 0; base < p.num_pages; base += kPass) {
+    uint32_t free[kPer];
+    const long mine = base + (long)warp * 32 * kPer;
+    const int n = free_masks(p, mine, free);
+    int sum;
+    int at = before + scan_warps(n, s_warp, sum);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const long page = mine + 32 * i + lane;
+      const int rank = at + __popc(free[i] & ((1u << lane) - 1));   // free pages before this one
+      const bool is_free = free[i] >> lane & 1;
+      if (page < p.num_pages) {
+        if (is_free && page < border) {
+          __stcg(p.list + rank, (int)page);
+          ++holes_mine;
+        } else if (!is_free && page >= border) {
+          __stcg(p.src + (page - rank), (int)page);
+          __stcg(p.lead + page, (int)(page - rank));
+        }
+      }
+      at += __popc(free[i]);
+    }
+    before += sum;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) holes_mine += __shfl_xor_sync(0xffffffffu, holes_mine, o);
+  int holes;
+  scan_warps(holes_mine, s_warp, holes);   // its barriers also order the lists before their reading
+  const int first = border - holes;   // rank of the first page that moves
+  for (int i = tid; i < holes; i += kPlan) {
+    const int from = __ldcg(p.src + first + i), to = __ldcg(p.list + i);
+    __stcg(p.refs + to, __ldcg(p.refs + from));
+    __stcg(p.refs + from, 0);
+  }
+  if (tid == 0) {
+    __stcg(p.head, holes);
+    __stcg(p.head + 1, first);
+    __stcg(p.head + 2, border);
+    if (used_out) __stcg(used_out, border);
+  }
+}
+
+template <typename U>
+__device__ __forceinline__ void copy_piece(char* dst, const char* src, int bytes) {
+  constexpr int N = kPiece / 32 / (int)sizeof(U) < 8 ? kPiece / 32 / (int)sizeof(U) : 8;
+  const int lane = threadIdx.x & 31, units = bytes / (int)sizeof(U);
+  for (int u0 = 0; u0 < units; u0 += 32 * N) {
+    U x[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (u0 + 32 * i + lane < units) x[i] = __ldcg(reinterpret_cast<const U*>(src) + u0 + 32 * i + lane);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (u0 + 32 * i + lane < units) __stcg(reinterpret_cast<U*>(dst) + u0 + 32 * i + lane, x[i]);
+  }
+}
+
+// The rows of the pages that move, in every layer and array: a warp takes pieces of up to
+// 4 KB (8 accesses of 16 bytes a lane in flight). src, dst: the moves, or the workspace's
+// (count and first source in head). rename: the table's entries behind the border too.
+__global__ void __launch_bounds__(256) copy_kernel(const PoolParams p, const int32_t* src, const int32_t* dst, int n,
+                                                   int rename) {
+  pool_wait();
+  const int lane = threadIdx.x & 31;
+  const long warps = (long)gridDim.x * 8, me = (long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  int bad = 0, first = 0;
+  if (n < 0) {
+    n = __ldcg(p.head);
+    first = __ldcg(p.head + 1);
+  }
+  int pieces = 0;   // of a page in one layer
+#pragma unroll
+  for (int a = 0; a < kPoolArrays; ++a)
+    if (a < p.arrays) pieces += (p.chunk[a] + kPiece - 1) / kPiece;
+  const long per_move = (long)pieces * p.layers, items = per_move * n;
+  for (long it = me; it < items; it += warps) {
+    const int m = (int)(it / per_move);
+    const int from = __ldcg(src + first + m);
+    if (from < 0) continue;   // a sequence whose page stays
+    const int to = __ldcg(dst + m);
+    if (from >= p.num_pages || to < 0 || to >= p.num_pages) {
+      bad |= kDevBadPage;
+      continue;
+    }
+    int rest = (int)(it % per_move);
+    const int layer = rest / pieces;
+    rest %= pieces;
+#pragma unroll
+    for (int a = 0; a < kPoolArrays; ++a) {
+      if (a >= p.arrays) break;
+      const int here = (p.chunk[a] + kPiece - 1) / kPiece;
+      if (rest >= 0 && rest < here) {
+        char* base = p.base[a] + layer * p.layer[a] + (long)rest * kPiece;
+        const int bytes = min(kPiece, p.chunk[a] - rest * kPiece);
+        char* d = base + (long)to * p.chunk[a];
+        const char* s = base + (long)from * p.chunk[a];
+        if (p.wide[a])
+          copy_piece<uint4>(d, s, bytes);
+        else
+          copy_piece<uint32_t>(d, s, bytes);
+      }
+      rest -= here;
+    }
+  }
+  if (rename && n > 0) {
+    const int border = __ldcg(p.head + 2);
+    for (long b = me; b < p.B; b += warps) {
+      const int held = held_of(p, (int)b, bad);
+      int32_t* row = p.table + b * p.max_pages;
+      for (int c = lane; c < held; c += 32) {
+        const int page = __ldcg(row + c);
+        if (page < border) continue;
+        // a page that its references do not know has no place among the moves
+        const int i = page < p.num_pages ? __ldcg(p.lead + page) - first : -1;
+        if (i >= 0 && i < n && __ldcg(src + first + i) == page)
+          __stcg(row + c, __ldcg(dst + i));
+        else
+          bad |= page < p.num_pages ? kDevBadPool : kDevBadPage;
+      }
+    }
+  }
+  if (bad) atomicOr(p.status, bad);
+}
+
+template <typename... P, typename... A>
+cudaError_t launch_pool(void (*kernel)(P...), long grid, int block, cudaStream_t s, A... args) {
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(block);
+  cfg.stream = s;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// CTAs of the copy kernel for up to n moves: pieces enough for a warp each, 8 CTAs an SM at most.
+long copy_grid(const PoolParams& p, long n) {
+  long pieces = 0;
+  for (int a = 0; a < p.arrays; ++a) pieces += (p.chunk[a] + kPiece - 1) / kPiece;
+  return std::max(1L, std::min(8L * p.num_sms, (n * pieces * p.layers + 7) / 8));
+}
+
+}  // namespace
+
+int64_t pool_workspace(int64_t pages, int64_t batch) {
+  return 4 * (16 + 4 * pages + 2 * std::max(pages, batch) + batch);
+}
+
+void place_pool_workspace(PoolParams& p, void* ws) {
+  int32_t* at = static_cast<int32_t*>(ws);
+  auto take = [&](int64_t n) {
+    int32_t* x = at;
+    at += n;
+    return x;
+  };
+  const int64_t most = std::max(p.num_pages, p.B);
+  p.head = take(16);
+  p.list = take(p.num_pages);
+  p.old = take(p.num_pages);
+  p.want = take(p.num_pages);
+  p.lead = take(p.num_pages);
+  p.src = take(most);
+  p.dst = take(most);
+  p.count = take(p.B);
+}
+
+cudaError_t launch_reserve(const PoolParams& p, const int32_t* rows, int extra, int32_t* missing, cudaStream_t s) {
+  cudaError_t e = launch_pool(reserve_kernel, 1, kPlan, s, p, rows, extra, missing);
+  if (e == cudaSuccess) e = launch_pool(copy_kernel, copy_grid(p, p.B), 256, s, p, p.src, p.dst, -1, 0);
+  return e == cudaSuccess ? launch_fence(s) : e;
+}
+
+cudaError_t launch_fork(const PoolParams& p, const int32_t* src, const int32_t* dst, int n, cudaStream_t s) {
+  const cudaError_t e = launch_pool(fork_kernel, n, 256, s, p, src, dst, n);
+  return e == cudaSuccess ? launch_fence(s) : e;
+}
+
+cudaError_t launch_release(const PoolParams& p, const int32_t* seqs, int n, cudaStream_t s) {
+  const cudaError_t e = launch_pool(release_kernel, n, 256, s, p, seqs);
+  return e == cudaSuccess ? launch_fence(s) : e;
+}
+
+cudaError_t launch_trim(const PoolParams& p, cudaStream_t s) {
+  const cudaError_t e = launch_pool(release_kernel, p.B, 256, s, p, (const int32_t*)nullptr);
+  return e == cudaSuccess ? launch_fence(s) : e;
+}
+
+cudaError_t launch_compact(const PoolParams& p, int32_t* used, cudaStream_t s) {
+  cudaError_t e = launch_pool(compact_kernel, 1, kPlan, s, p, used);
+  if (e == cudaSuccess)
+    e = launch_pool(copy_kernel, copy_grid(p, std::max(p.num_pages / 2, p.B)), 256, s, p, p.src, p.list, -1, 1);
+  return e == cudaSuccess ? launch_fence(s) : e;
+}
+
+cudaError_t launch_copy_pages(const PoolParams& p, const int32_t* src, const int32_t* dst, int n, cudaStream_t s) {
+  const cudaError_t e = launch_pool(copy_kernel, copy_grid(p, n), 256, s, p, src, dst, n, 0);
+  return e == cudaSuccess ? launch_fence(s) : e;
+}
+
+}  // namespace fastocr

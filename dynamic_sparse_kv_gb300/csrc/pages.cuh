@@ -1,0 +1,46 @@
+// Pages of a pool: parameters and launches of pages.cu.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace fastocr {
+
+constexpr int kPoolArrays = 4;   // K, V and, in 4 bits, their scales
+
+struct PoolParams {
+  int32_t* table;      // [B, max_pages]; -1: no page
+  int32_t* seq_len;    // [B]
+  int32_t* held;       // [B]
+  int32_t* refs;       // [num_pages]
+  int B, max_pages, log2_page, num_pages;
+  int32_t* status;
+  // workspace
+  int32_t* head;       // [0] moves; compact: [1] index of the first source, [2] border
+  int32_t* src;        // pages to move, negative: none
+  int32_t* dst;
+  int32_t *list, *old, *want, *lead;   // [num_pages]
+  int32_t* count;      // [B]
+  // the caches: page p of layer l of array a is at base[a] + l * layer[a] + p * chunk[a]
+  char* base[kPoolArrays];
+  long layer[kPoolArrays];
+  int chunk[kPoolArrays];
+  int wide[kPoolArrays];   // everything a multiple of 16 bytes (otherwise of 4)
+  int arrays, layers;
+  int num_sms;
+};
+
+// Bytes of workspace for a pool of `pages` pages and `batch` sequences.
+int64_t pool_workspace(int64_t pages, int64_t batch);
+void place_pool_workspace(PoolParams& p, void* ws);   // p.B and p.num_pages are set
+
+// Each ends with launch_fence: what follows may read the table, the lengths and the
+// cache before its own wait.
+cudaError_t launch_reserve(const PoolParams& p, const int32_t* rows, int extra, int32_t* missing, cudaStream_t s);
+cudaError_t launch_fork(const PoolParams& p, const int32_t* src, const int32_t* dst, int n, cudaStream_t s);
+cudaError_t launch_release(const PoolParams& p, const int32_t* seqs, int n, cudaStream_t s);
+cudaError_t launch_trim(const PoolParams& p, cudaStream_t s);
+cudaError_t launch_compact(const PoolParams& p, int32_t* used, cudaStream_t s);
+cudaError_t launch_copy_pages(const PoolParams& p, const int32_t* src, const int32_t* dst, int n, cudaStream_t s);
+
+}  // namespace fastocr

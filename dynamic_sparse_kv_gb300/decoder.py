@@ -18,7 +18,9 @@ window pages.
 Beside those, for generated text that grows long and for batches that read one
 document: share_prefix + shared_step (a prefix read once for a group of
 sequences) and track_weights + weighed_step + evict_step (every row's attention
-weight added up, the rows of least weight dropped), alone or together.
+weight added up, the rows of least weight dropped), alone or together. write_layer
+puts new tokens into the cache (rotary.Rotary positions), which may be held in 4
+bits (fp4.Fp4Cache), and pages.PagePool keeps the pages that the table names.
 
 The selection never leaves the GPU: every focal layer writes into its own
 fixed device buffer, and F_last *is* the deepest focal layer's buffer, which
@@ -102,7 +104,8 @@ class _Weights(dict):
 class DecodeAttention:
     """Decode attention of a stack of layers over a paged KV cache.
 
-    k_cache, v_cache: [layers, num_pages, H_kv, page_size, d] (bf16 or fp32)
+    k_cache, v_cache: [layers, num_pages, H_kv, page_size, d] (bf16 or fp32), or two
+    Fp4Cache (4 bits; q and out in bf16; not for shared prefixes and weights)
     block_table: [B, pages_per_seq] int32; img_range: [B, 2] int32 (focal modes).
     """
 
@@ -190,6 +193,10 @@ class DecodeAttention:
             raise ValueError(f"{name} must have one value a sequence, shape ({self.batch},)")
         return x
 
+    def _no_fp4(self, what):
+        if getattr(self.k_cache, "fp4", False):
+            raise ValueError(f"{what} need a cache in bf16 or fp32, not in 4 bits")
+
     def share_prefix(self, group_start, prefix_len, max_prefix: int | None = None):
         """Sequences group_start[i] .. group_start[i+1]-1 share rows [0, prefix_len)
         of group_start[i]'s pages (group_start from 0 to B; prefix_len int or
@@ -197,6 +204,7 @@ class DecodeAttention:
         split choice only; None takes it from prefix_len (which then
         synchronises, if it is on the device). Call it again when the groups
         change; a CapturedStep goes on with the groups it was captured with."""
+        self._no_fp4("shared prefixes")
         start = torch.as_tensor(group_start).to(torch.int32)
         if start.dim() != 1 or not 2 <= start.numel() <= self.batch + 1:
             raise ValueError("group_start must hold 2 .. B+1 offsets")
@@ -224,6 +232,7 @@ class DecodeAttention:
         (a prompt that is already in the cache). begin_token advances seen. A
         CapturedStep goes on with the weights it was captured with, whose seen
         begin_token advances too. A protect on the device is read back once."""
+        self._no_fp4("weights")
         if rows < 1:
             raise ValueError("rows must be at least 1")
         dev = self.k_cache.device
@@ -459,6 +468,76 @@ class DecodeAttention:
                                   self.rswa_window, out[l], stream)
             if hook:
                 hook(l, False)
+
+    # ------------------------------------------------------------ rows in and out
+    def _packed(self, t, name, heads, tokens=None):
+        """Tokens' heads as the library takes them: (tensor, elements from token to token)."""
+        dt, dev, d = self.k_cache.dtype, self.k_cache.device, self.head_dim
+        if (t.dim() != 3 or t.shape[1:] != (heads, d) or t.dtype != dt or t.device != dev
+                or (tokens is not None and t.shape[0] != tokens)):
+            n = "tokens" if tokens is None else tokens
+            raise ValueError(f"{name} must be a {dt} tensor of shape ({n}, {heads}, {d}) on {dev}, not {t.dtype} "
+                             f"{tuple(t.shape)} on {t.device}")
+        if t.shape[0] <= 1:
+            good, step = t.shape[0] == 0 or t[0].is_contiguous(), heads * d
+        else:
+            good, step = t[0].is_contiguous() and t.stride(0) >= heads * d, t.stride(0)
+        if not good or step * t.element_size() % 16:
+            raise ValueError(f"a token of {name} must be contiguous and tokens a multiple of 16 bytes apart, "
+                             f"not with strides {t.stride()}")
+        return step
+
+    def write_layer(self, l, k, v, *, q=None, out_q=None, rotary=None, pos=None, q_start=None, stream=None):
+        """New tokens of layer l: k, v [T, H_kv, d] go to the last rows of their sequences
+        (seq_len counts them already), k and q [T, H_q, d] turned by rotary positions.
+
+        One token a sequence (T = B), or with q_start [B + 1] int32 tokens q_start[b] ..
+        q_start[b+1]-1 of sequence b, rows N_b - T_b and on. q, k, v may be slices of one
+        projection's output (heads and dims contiguous). out_q, contiguous, may be q. rotary: a
+        Rotary, with pos [axes, T] int32; None: nothing turns. In a step, call it for a layer
+        before the layer attends, e.g. in step(hook=...)."""
+        dev, T = self.k_cache.device, k.shape[0]
+        ks = self._packed(k, "k", self.kv_heads)
+        vs = self._packed(v, "v", self.kv_heads, T)
+        qs = 0
+        if (q is None) != (out_q is None):
+            raise ValueError("q and out_q come together")
+        if q is not None:
+            qs = self._packed(q, "q", self.q_heads, T)
+            N.check_tensor(out_q, "out_q", (T, self.q_heads, self.head_dim), self.k_cache.dtype, dev)
+        if q_start is not None:
+            N.check_tensor(q_start, "q_start", (self.batch + 1,), torch.int32, dev)
+        elif T != self.batch:
+            raise ValueError(f"one token a sequence ({self.batch}), or q_start")
+        if rotary is not None:
+            if rotary.head_dim != self.head_dim or rotary.cos_sin.device != dev:
+                raise ValueError(f"rotary must be for head_dim {self.head_dim} on {dev}")
+            if pos is None:
+                raise ValueError("rotary needs pos")
+            N.check_tensor(pos, "pos", (rotary.axes, T), torch.int32, dev)
+        if T == 0:
+            return
+        tokens = N.fastocr_tokens(q.data_ptr() if q is not None else None, k.data_ptr(), v.data_ptr(), qs, ks, vs,
+                                  out_q.data_ptr() if q is not None else None,
+                                  pos.data_ptr() if rotary is not None else None,
+                                  q_start.data_ptr() if q_start is not None else None, T)
+        N.fastocr_write_rows(self.handle, self.kv[l], tokens, rotary.c if rotary is not None else None, stream)
+
+    def read_layer(self, l, row_start, out_k, out_v, stream=None):
+        """The last rows of every sequence of layer l as values: rows N_b - T_b .. N_b - 1 with
+        T_b = row_start[b+1] - row_start[b] (row_start [B + 1] int32), packed into out_k, out_v
+        [T, H_kv, d], both fp32 or both bf16."""
+        dev, T = self.k_cache.device, out_k.shape[0]
+        if out_k.dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError(f"out_k must be float32 or bfloat16, not {out_k.dtype}")
+        shape = (T, self.kv_heads, self.head_dim)
+        N.check_tensor(out_k, "out_k", shape, out_k.dtype, dev)
+        N.check_tensor(out_v, "out_v", shape, out_k.dtype, dev)
+        N.check_tensor(row_start, "row_start", (self.batch + 1,), torch.int32, dev)
+        if T == 0:
+            return
+        dtype = N.FASTOCR_DTYPE_F32 if out_k.dtype == torch.float32 else N.FASTOCR_DTYPE_BF16
+        N.fastocr_read_rows(self.handle, self.kv[l], row_start, T, out_k, out_v, dtype, stream)
 
     def _check_layer(self, q_l, out_l):
         shape = (self.batch, self.q_heads, self.head_dim)

@@ -1,0 +1,120 @@
+"""The pages of a paged cache and who holds them, over the C ABI (fastocr_pool).
+
+A pool serves one DecodeAttention: its block table, its lengths and, in every layer, its
+caches (bf16, fp32 or 4 bits). Nothing is read back to the host, so a captured step can
+reserve its next token's page, and lengths that only the device knows (after an eviction)
+are fine.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import _native as N
+
+
+class PagePool:
+    """Who holds the pages of dec's caches.
+
+    held [B] and refs [num_pages] int32, on the caches' device: how many leading entries of
+    a sequence's table row are pages, and how many entries name a page; taken as they are,
+    with dec's table and seq_len, if given. Otherwise the pool starts empty: every page
+    free, every table entry -1, every length 0.
+
+    Sequences are given as a list or a tensor; lists are checked on the host, int32 tensors
+    on the device are checked there (dec.device_status). Calls are asynchronous on `stream`
+    and have to be ordered among themselves and with what uses the table.
+    """
+
+    def __init__(self, dec, *, held=None, refs=None):
+        if (held is None) != (refs is None):
+            raise ValueError("held and refs come together")
+        dev = dec.k_cache.device
+        if held is None:
+            held = torch.zeros(dec.batch, dtype=torch.int32, device=dev)
+            refs = torch.zeros(dec.num_pages, dtype=torch.int32, device=dev)
+            dec.block_table.fill_(-1)
+            dec.seq_len.zero_()
+        N.check_tensor(held, "held", (dec.batch,), torch.int32, dev)
+        N.check_tensor(refs, "refs", (dec.num_pages,), torch.int32, dev)
+        self.dec, self.held, self.refs = dec, held, refs
+        self.used = torch.zeros(1, dtype=torch.int32, device=dev)      # of the last compact
+        self.missing = torch.zeros(1, dtype=torch.int32, device=dev)   # of the last reserve
+        n = N.fastocr_pool_workspace(dec.handle, dec.num_pages)
+        self.ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        arrays, steps = [], []
+        k, v = dec.k_cache, dec.v_cache
+        for t in ((k.codes, v.codes, k.scales, v.scales) if getattr(k, "fp4", False) else (k, v)):
+            arrays.append(t.data_ptr())
+            steps.append(t.stride(0) * t.element_size())
+        pad = [None] * (4 - len(arrays)), [0] * (4 - len(arrays))
+        self.c = N.fastocr_pool(dec.block_table.data_ptr(), dec.seq_len.data_ptr(), held.data_ptr(), refs.data_ptr(),
+                                dec.num_pages, *arrays, *pad[0], *steps, *pad[1], self.ws.data_ptr(), n)
+
+    def _indices(self, x, name, bound):
+        """[n] int32 on the device, and the host's copy if x was there."""
+        dev = self.dec.k_cache.device
+        if isinstance(x, torch.Tensor) and x.device == dev:
+            if x.dim() != 1 or x.dtype != torch.int32 or not x.is_contiguous() or x.numel() > bound:
+                raise ValueError(f"{name} must be a contiguous int32 tensor of up to {bound} entries")
+            return x, None
+        host = torch.as_tensor(x)
+        if host.numel() == 0:
+            host = host.to(torch.int64)
+        if host.dim() != 1 or host.is_floating_point() or host.dtype == torch.bool:
+            raise ValueError(f"{name} must be a list of whole numbers")
+        host = host.tolist()
+        if any(i < 0 or i >= bound for i in host) or len(host) > bound:
+            raise ValueError(f"{name} must lie in [0, {bound})")
+        return torch.tensor(host, dtype=torch.int32, device=dev), host
+
+    def _pairs(self, src, dst, bound):
+        (a, ha), (b, hb) = self._indices(src, "src", bound), self._indices(dst, "dst", bound)
+        if a.shape != b.shape:
+            raise ValueError("src and dst must have one length")
+        if hb is not None and len(set(hb)) != len(hb):
+            raise ValueError("dst must name each of its entries once")
+        if ha is not None and hb is not None and set(ha) & set(hb):
+            raise ValueError("src and dst must have nothing in common")
+        return a, b
+
+    def reserve(self, rows=None, *, extra: int | None = None, stream=None):
+        """Pages for rows [0, rows) (int or [B]) of every sequence, or for `extra` rows behind
+        its length; pages it shares with others, from the length on, become its own (the rows
+        in them are copied). All or nothing: self.missing [1] (on the device) tells how many
+        pages were too few, and dec.device_status has DEV_NO_PAGES."""
+        if (rows is None) == (extra is None):
+            raise ValueError("give rows or extra")
+        if rows is None:
+            if extra < 0:
+                raise ValueError("extra must not be negative")
+        else:
+            rows = self.dec._per_sequence(rows, "rows")
+        N.fastocr_pool_reserve(self.dec.handle, self.c, rows, extra or 0, self.missing, stream)
+
+    def fork(self, src, dst, stream=None):
+        """Sequences dst[i] become copies of src[i] that share its pages; what they held is
+        released. reserve copies a shared page before one of them writes to it."""
+        a, b = self._pairs(src, dst, self.dec.batch)
+        if a.numel():
+            N.fastocr_pool_fork(self.dec.handle, self.c, a, b, a.numel(), stream)
+
+    def release(self, seqs, stream=None):
+        """Sequences give up their pages; their length is 0."""
+        s, _ = self._indices(seqs, "seqs", self.dec.batch)
+        if s.numel():
+            N.fastocr_pool_release(self.dec.handle, self.c, s, s.numel(), stream)
+
+    def trim(self, stream=None):
+        """Every sequence gives up the pages behind its rows."""
+        N.fastocr_pool_trim(self.dec.handle, self.c, stream)
+
+    def compact(self, stream=None):
+        """The pages in use move to the pool's start, in every layer; self.used [1] (on the
+        device) is their number, and pages from there on are free."""
+        N.fastocr_pool_compact(self.dec.handle, self.c, self.used, stream)
+
+    def copy_pages(self, src, dst, stream=None):
+        """Page src[i] to dst[i] in every layer; tables and references stay."""
+        a, b = self._pairs(src, dst, self.dec.num_pages)
+        if a.numel():
+            N.fastocr_pool_copy(self.dec.handle, self.c, a, b, a.numel(), stream)

@@ -27,9 +27,18 @@
  *  g = H_q / H_kv <= 8), head dimension d (64 or 128). Query head h reads
  *  KV head h / g. Softmax scale 1/sqrt(d).
  *  dtype: FASTOCR_DTYPE_BF16 (q, K, V, out in bf16; fp32 accumulation) or
- *         FASTOCR_DTYPE_F32 (all fp32, CUDA-core arithmetic, no TF32).
+ *         FASTOCR_DTYPE_F32 (all fp32, CUDA-core arithmetic, no TF32) or
+ *         FASTOCR_DTYPE_FP4 (q, out in bf16; K, V held in 4 bits, below; not
+ *         for shared prefixes, weights, eviction and cross attention, which
+ *         answer FASTOCR_ERR_UNSUPPORTED, nor without a handle).
  *  q, out:        [B, H_q, d] contiguous, device memory, caller-owned.
  *  K, V caches:   [num_pages, H_kv, page_size, d] contiguous per layer, device.
+ *                 4 bits: k, v hold codes [num_pages, H_kv, page_size, d / 2] (e2m1,
+ *                 dimension 2i in the low half of byte i), k_scale, v_scale
+ *                 [num_pages, H_kv, page_size, d / 16] e4m3, one a group of 16
+ *                 dimensions, k_gain, v_gain [H_kv] fp32; an element stands for
+ *                 e2m1 * e4m3 * gain, 4.5 bits each. A scale of NaN makes its
+ *                 group NaN.
  *  block_table:   [B, max_pages_per_seq] int32, device; page of token p of
  *                 sequence b is block_table[b][p / page_size], row p % page_size.
  *  seq_len:       [B] int32, device; N_t = tokens in the cache, the current
@@ -86,7 +95,9 @@ extern "C" {
  * to version 1; no call of version 1 changed. fastocr_shared_attend,
  * fastocr_weigh_attend, fastocr_evict, fastocr_cross_attend and
  * fastocr_rows_workspace came later and changed nothing either, so the number
- * stayed: look for the symbols. */
+ * stayed: look for the symbols. So did FASTOCR_DTYPE_FP4 (with the trailing
+ * members of fastocr_kv, which other types do not read), fastocr_write_rows,
+ * fastocr_read_rows and the fastocr_pool calls. */
 #define FASTOCR_ABI_VERSION 2
 
 typedef struct fastocr_handle fastocr_handle;
@@ -102,7 +113,7 @@ typedef enum {
   FASTOCR_ERR_ALIGN = -6        /* a device pointer is not 16-byte aligned */
 } fastocr_status;
 
-typedef enum { FASTOCR_DTYPE_F32 = 0, FASTOCR_DTYPE_BF16 = 1 } fastocr_dtype;
+typedef enum { FASTOCR_DTYPE_F32 = 0, FASTOCR_DTYPE_BF16 = 1, FASTOCR_DTYPE_FP4 = 2 } fastocr_dtype;
 
 /* Device status bits (fastocr_device_status). */
 #define FASTOCR_DEV_BAD_PAGE 1      /* block_table entry outside [0, num_pages) */
@@ -112,6 +123,9 @@ typedef enum { FASTOCR_DTYPE_F32 = 0, FASTOCR_DTYPE_BF16 = 1 } fastocr_dtype;
 #define FASTOCR_DEV_INTERNAL 16     /* a kernel-internal consistency check failed (a library bug) */
 #define FASTOCR_DEV_BAD_GROUP 32    /* group or query offsets out of order, or a prefix past N_t */
 #define FASTOCR_DEV_BAD_WEIGHTS 64  /* protect < 0, below the prefix, or more rows than the stride */
+#define FASTOCR_DEV_BAD_POSITION 128 /* rotary position outside the table (the nearest one was taken) */
+#define FASTOCR_DEV_NO_PAGES 256    /* too few free pages: nothing was reserved */
+#define FASTOCR_DEV_BAD_POOL 512    /* pages held or references that do not fit the table */
 
 /* Shapes fixed for the life of a handle. */
 typedef struct {
@@ -133,7 +147,52 @@ typedef struct {
   const int32_t* block_table; /* [B, max_pages_per_seq] */
   const int32_t* seq_len;     /* [B] */
   int32_t num_pages;          /* pages in k and v (bounds check) */
+  /* FASTOCR_DTYPE_FP4 only (other types leave them unread) */
+  const void* k_scale;        /* [num_pages, H_kv, page_size, d / 16] e4m3, aligned to d / 16 bytes */
+  const void* v_scale;
+  const float* k_gain;        /* [H_kv], finite and above 0 */
+  const float* v_gain;
 } fastocr_kv;
+
+/* Rotary positions: the pairs of a head's first `rotary_dim` dimensions turn, pair i by
+ * the angle of its axis' position. Device memory, caller-owned. */
+typedef struct {
+  const float* cos_sin;   /* [positions, rotary_dim / 2, 2]: cos, sin of position p and pair i; 16-byte aligned */
+  const int8_t* axis;     /* [rotary_dim / 2]: axis of pair i (0 time, 1 height, ..., as the caller numbers them) */
+  int32_t positions;      /* >= 1 */
+  int32_t rotary_dim;     /* a multiple of 32, <= d */
+  int32_t axes;           /* 1 .. 4 */
+  int32_t adjacent;       /* 0: pair i is dimensions i and i + rotary_dim / 2; 1: 2i and 2i + 1 */
+} fastocr_rotary;
+
+/* Tokens for fastocr_write_rows, packed. Strides count elements from token to token; heads
+ * and dimensions are contiguous, so the parts of one projection's output serve as they are. */
+typedef struct {
+  const void* q;          /* [tokens, H_q, d], or NULL: keys and values only */
+  const void* k;          /* [tokens, H_kv, d] */
+  const void* v;          /* [tokens, H_kv, d] */
+  int64_t q_stride, k_stride, v_stride; /* multiples of 16 bytes */
+  void* q_out;            /* [tokens, H_q, d] contiguous; NULL with q. May be q, if that is contiguous */
+  const int32_t* pos;     /* [axes, tokens]; NULL without rotary positions */
+  const int32_t* start;   /* [B + 1]: tokens start[b] .. start[b+1]-1 are sequence b's; NULL: token b is, B of them */
+  int32_t tokens;         /* >= 0 */
+} fastocr_tokens;
+
+/* A pool of pages and who holds them (the fastocr_pool calls). Device memory, caller-owned. */
+typedef struct {
+  int32_t* block_table; /* [B, max_pages_per_seq]: held[b] pages, then -1 */
+  int32_t* seq_len;     /* [B]: rows written; 0: none */
+  int32_t* held;        /* [B] */
+  int32_t* refs;        /* [num_pages]: entries of block_table that name the page; 0: free */
+  int32_t num_pages;
+  void* k;              /* layer 0's cache, as fastocr_kv; num_layers of them */
+  void* v;
+  void* k_scale;        /* FASTOCR_DTYPE_FP4 only */
+  void* v_scale;
+  int64_t k_layer, v_layer, k_scale_layer, v_scale_layer; /* bytes from layer to layer, aligned as the pointers */
+  void* ws;             /* 16-byte aligned, fastocr_pool_workspace bytes; meaningless between calls */
+  int64_t ws_bytes;
+} fastocr_pool;
 
 /* Groups of sequences that share a prefix (fastocr_shared_attend). start and
  * prefix_len are device memory, caller-owned. */
@@ -366,6 +425,86 @@ fastocr_status fastocr_evict(fastocr_handle* h, const fastocr_kv* kv, const fast
 fastocr_status fastocr_cross_attend(fastocr_handle* h, const void* q, const fastocr_kv* kv,
                                     const int32_t* q_start, int64_t rows, void* out, void* ws,
                                     int64_t ws_bytes, fastocr_stream stream);
+
+/* Writes tokens to the cache of one layer, with rotary positions: q_out = turned q, and the
+ * turned k and the v of token t of sequence b's T_b tokens go to row N_b - T_b + t, N_b =
+ * seq_len[b], which counts them already. (x0, x1) becomes (x0 c - x1 s, x1 c + x0 s), each
+ * product and sum rounded to fp32, the result to the cache's type. FASTOCR_DTYPE_FP4 (from
+ * bf16): with y = x / gain and a the largest |y| of 16, the scale is a / 6 rounded to e4m3
+ * (at most 448) and a code is y / scale rounded to e2m1 (ties to even, at most 6); a group
+ * that has a NaN or an infinity becomes NaN. rotary NULL: nothing turns, q is copied.
+ * Tokens behind start[B], and their q_out, are left alone. A token of a sequence with fewer
+ * rows than tokens (FASTOCR_DEV_BAD_GROUP), a length out of range or a bad page gets no row;
+ * a position outside the table is clamped to it (FASTOCR_DEV_BAD_POSITION). A page must not
+ * be written through two sequences' tables at once. K and V are written although
+ * fastocr_kv has them const.
+ * Overlap: everything is read after the preceding kernel completes. With start NULL only
+ * rows N_b - 1 are written, as the attention calls expect of the kernel before them; with
+ * start a second, empty kernel follows, so that any call may come next.
+ * tokens * (H_q + 2 H_kv) * d < 2^34. Errors: NULL, INVALID (strides, rotary, tokens !=
+ * B without start, another device current), UNSUPPORTED (rotary_dim), ALIGN, CUDA. */
+fastocr_status fastocr_write_rows(fastocr_handle* h, const fastocr_kv* kv, const fastocr_tokens* tokens,
+                                  const fastocr_rotary* rotary, fastocr_stream stream);
+
+/* The way back: rows N_b - T_b .. N_b - 1 of every sequence, T_b = start[b+1] - start[b],
+ * packed into k_out, v_out [tokens, H_kv, d] (out_dtype FASTOCR_DTYPE_BF16 or _F32) -- as
+ * the values that 4 bits stand for, where the cache has those: a prompt's later chunks need
+ * the earlier ones' keys and values. A row that does not exist (as in fastocr_write_rows)
+ * reads as 0; rows behind start[B] are left alone. One kernel, which reads everything after
+ * the preceding one completes. Errors as fastocr_write_rows. */
+fastocr_status fastocr_read_rows(fastocr_handle* h, const fastocr_kv* kv, const int32_t* start, int32_t tokens,
+                                 void* k_out, void* v_out, int32_t out_dtype, fastocr_stream stream);
+
+/* Pages of a pool. Sequences hold pages of one pool, a page may be in several tables, and
+ * refs counts how often. The calls keep table, lengths, pages held and references in step;
+ * free pages go out lowest first, so the result is the same on every run. All of it happens
+ * on the device, in order on `stream`; an empty kernel ends each call, so that any call may
+ * follow. Calls on one pool must be ordered. State that does not fit (a page out of range, a
+ * reference too few) is reported as FASTOCR_DEV_BAD_PAGE or _BAD_POOL, and that entry left
+ * out. Errors of all: NULL, INVALID (sizes, ws_bytes, another device current),
+ * UNSUPPORTED (more than 2^31 rows or table entries), ALIGN, CUDA. */
+
+/* Bytes of workspace for a pool of num_pages pages. Negative (a fastocr_status): NULL, INVALID. */
+int64_t fastocr_pool_workspace(const fastocr_handle* h, int64_t num_pages);
+
+/* Pages for rows [0, rows[b]) of every sequence (rows NULL: [0, seq_len[b] + extra), extra
+ * >= 0), and pages of its own for those behind seq_len[b], which are about to be written:
+ * where such a page is in several tables, the sequence gets a fresh one and a copy of the
+ * rows in it -- except the first of the sequences that want it, where every holder does.
+ * seq_len stays. All or nothing: with too few free pages nothing changes and
+ * FASTOCR_DEV_NO_PAGES is set. missing (device, may be NULL): how many too few. rows above
+ * the capacity are clamped (FASTOCR_DEV_BAD_SEQLEN). Three kernels. */
+fastocr_status fastocr_pool_reserve(fastocr_handle* h, const fastocr_pool* pool, const int32_t* rows, int32_t extra,
+                                    int32_t* missing, fastocr_stream stream);
+
+/* Sequences dst[i] become copies of src[i] (i < n; device): length and pages, which are
+ * then shared (no rows move: fastocr_pool_reserve copies what one of them is about to
+ * write); what dst[i] held is released. A pair out of range, a dst named again, and a
+ * sequence that is both a src and a dst of different pairs are reported as
+ * FASTOCR_DEV_BAD_GROUP and the pair left out. 0 <= n <= B. Two kernels. */
+fastocr_status fastocr_pool_fork(fastocr_handle* h, const fastocr_pool* pool, const int32_t* src, const int32_t* dst,
+                                 int32_t n, fastocr_stream stream);
+
+/* Sequences seqs[i] (i < n; device) give up their pages and have no rows; one named twice
+ * does so once. 0 <= n <= B. Two kernels. */
+fastocr_status fastocr_pool_release(fastocr_handle* h, const fastocr_pool* pool, const int32_t* seqs, int32_t n,
+                                    fastocr_stream stream);
+
+/* Every sequence gives up the pages behind its rows (after an eviction, or when it was set
+ * back). Two kernels. */
+fastocr_status fastocr_pool_trim(fastocr_handle* h, const fastocr_pool* pool, fastocr_stream stream);
+
+/* With U pages in use, the i-th page in use at or behind U moves, in every layer, into the
+ * i-th free page before it, and the tables name it so: pages [U, num_pages) are then free.
+ * used (device, may be NULL) = U. Three kernels. */
+fastocr_status fastocr_pool_compact(fastocr_handle* h, const fastocr_pool* pool, int32_t* used, fastocr_stream stream);
+
+/* Page src[i] is copied to dst[i] (i < n; device) in every layer; the tables stay. A pair
+ * out of range is reported as FASTOCR_DEV_BAD_PAGE. No page may be dst of two pairs, or
+ * src of one and dst of another (its rows are then unspecified). 0 <= n <= num_pages.
+ * Two kernels. */
+fastocr_status fastocr_pool_copy(fastocr_handle* h, const fastocr_pool* pool, const int32_t* src, const int32_t* dst,
+                                 int32_t n, fastocr_stream stream);
 
 /* Zero the profiler accumulator of every layer (asynchronous on stream). */
 fastocr_status fastocr_profiler_reset(fastocr_handle* h, fastocr_stream stream);
