@@ -38,9 +38,9 @@ CacheRows cache_rows(const fastocr_handle* h, const fastocr_kv* kv, const int32_
   return c;
 }
 
-// a grid of threads of 16 elements each stays below 2^31 CTAs of 256
+// a thread takes 4 elements or more, and threads are counted in 32 bits
 bool too_many(const fastocr_handle* h, int64_t tokens) {
-  return tokens * (h->dims.num_q_heads + 2LL * h->dims.num_kv_heads) * h->dims.head_dim >= (1LL << 34);
+  return tokens * (h->dims.num_q_heads + 2LL * h->dims.num_kv_heads) * h->dims.head_dim >= (1LL << 33);
 }
 
 fastocr_status pool_params(const fastocr_handle* h, const fastocr_pool* pool, PoolParams& p) {
@@ -162,7 +162,7 @@ fastocr_status fastocr_read_rows(fastocr_handle* h, const fastocr_kv* kv, const 
   p.k_out = static_cast<char*>(k_out);
   p.v_out = static_cast<char*>(v_out);
   p.out_f32 = out_dtype == FASTOCR_DTYPE_F32;
-  return status_of(launch_read_rows(h->dims.dtype, h->dims.head_dim, p, static_cast<cudaStream_t>(stream)));
+  return status_of(launch_read_rows(h->dims.dtype, h->dims.head_dim, h->num_sms, p, static_cast<cudaStream_t>(stream)));
 }
 
 int64_t fastocr_pool_workspace(const fastocr_handle* h, int64_t num_pages) {

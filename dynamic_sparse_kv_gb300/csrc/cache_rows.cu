@@ -11,8 +11,9 @@
 // the heads of few tokens over the SMs (one token of 36 heads: 36 slots) and is 1 where
 // the tokens alone fill them.
 //
-// Read. A thread takes 16 dims (one group) of one row.
+// Read. The same split, 16 bytes of output a thread.
 #include <cuda_bf16.h>
+#include <algorithm>
 #include <float.h>
 #include <math_constants.h>
 
@@ -25,7 +26,13 @@ namespace fastocr {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kPerSm = 2048;
+constexpr int kReadTile = 8;   // tokens a CTA reads at most
 
+// What many threads look up at the same address (offsets, lengths, gains) is loaded through
+// L1: past it, one L2 slice would answer every warp of the grid in turn (reading 27 820
+// tokens from 4 bits back as fp32 took 62 us that way, 33 with it).
+//
 // Sequence of a packed token (the last that starts at or before it), or -1: none has it.
 __device__ __forceinline__ int sequence_of(const CacheRows& c, int token, int& first, int& end) {
   if (!c.start) {
@@ -36,20 +43,20 @@ __device__ __forceinline__ int sequence_of(const CacheRows& c, int token, int& f
   int lo = 0, hi = c.B;   // the answer is in [lo, hi)
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (__ldcg(c.start + mid) <= token)
+    if (c.start[mid] <= token)
       lo = mid;
     else
       hi = mid;
   }
-  first = __ldcg(c.start + lo);
-  end = __ldcg(c.start + lo + 1);
+  first = c.start[lo];
+  end = c.start[lo + 1];
   return token >= first && token < end ? lo : -1;
 }
 
 // Page slot of a token's row, as rows of one KV head are counted ((page * H_kv) << log2_page,
 // plus the slot), or -1 for none; the token is the last but (end - 1 - token) of sequence b.
 __device__ __forceinline__ long row_of(const CacheRows& c, int b, int token, int first, int end, int& bad) {
-  int n = __ldcg(c.seq_len + b);
+  int n = c.seq_len[b];
   if (n < 0 || n > (c.max_pages << c.log2_page)) {
     bad |= kDevBadSeqLen;
     return -1;
@@ -59,7 +66,7 @@ __device__ __forceinline__ long row_of(const CacheRows& c, int b, int token, int
     bad |= kDevBadGroup;
     return -1;
   }
-  const int page = __ldcg(c.block_table + (size_t)b * c.max_pages + (r >> c.log2_page));
+  const int page = c.block_table[(size_t)b * c.max_pages + (r >> c.log2_page)];
   if (page < 0 || page >= c.num_pages) {
     bad |= kDevBadPage;
     return -1;
@@ -67,19 +74,30 @@ __device__ __forceinline__ long row_of(const CacheRows& c, int b, int token, int
   return (((long)page * c.Hkv) << c.log2_page) + (r & ((1 << c.log2_page) - 1));
 }
 
-__device__ __forceinline__ void load8(const char* at, float x[8], const __nv_bfloat16*) {
-  const uint4 w = __ldcg(reinterpret_cast<const uint4*>(at));
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+// 8 elements as they lie, and as floats.
+template <typename Q>
+struct Raw8 {
+  uint4 w[sizeof(Q) / 2];
+  __device__ __forceinline__ void load(const char* at) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(u[i] << 16);
-    x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    for (int i = 0; i < (int)sizeof(Q) / 2; ++i) w[i] = __ldcg(reinterpret_cast<const uint4*>(at) + i);
   }
-}
-__device__ __forceinline__ void load8(const char* at, float x[8], const float*) {
-  const float4 a = __ldcg(reinterpret_cast<const float4*>(at)), b = __ldcg(reinterpret_cast<const float4*>(at) + 1);
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
+  __device__ __forceinline__ void get(float x[8]) const {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(Q) / 2; ++i) {
+      const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (sizeof(Q) == 2) {
+          x[2 * j] = __uint_as_float(u[j] << 16);
+          x[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
+        } else {
+          x[4 * i + j] = __uint_as_float(u[j]);
+        }
+      }
+    }
+  }
+};
 __device__ __forceinline__ void store8(char* at, const float x[8], const __nv_bfloat16*) {
   *reinterpret_cast<uint4*>(at) =
       make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
@@ -89,42 +107,67 @@ __device__ __forceinline__ void store8(char* at, const float x[8], const float*)
   reinterpret_cast<float4*>(at)[1] = make_float4(x[4], x[5], x[6], x[7]);
 }
 
+// a / b rounded to nearest, r = 1 / b rounded to nearest (Markstein: a quotient within an ulp
+// of a / b plus its remainder times r rounds correctly), where no product leaves the normal
+// range: b in [2^-30, 2^30], |a| below 2^60. A quotient below 2^-60 may be off by its last
+// bit, far below the smallest scale.
+__device__ __forceinline__ float quotient(float a, float b, float r) {
+  const float q = __fmul_rn(a, r);
+  return __fmaf_rn(__fmaf_rn(-q, b, a), r, q);
+}
+
 // 8 dims of a group of 16 whose other 8 the neighbouring lane holds, as codes; *scale is
 // the group's. Every lane of the warp takes part.
 __device__ __forceinline__ uint32_t pack_codes(const float x[8], float gain, uint32_t* scale) {
-  float y[8], top = 0.f;
-  bool finite = true;
+  float y[8], most = 0.f, poison = 0.f;   // poison: NaN if an element is not finite
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    y[i] = __fdiv_rn(x[i], gain);
-    top = fmaxf(top, fabsf(y[i]));
-    finite &= fabsf(y[i]) <= FLT_MAX;   // false for NaN
+    most = fmaxf(most, fabsf(x[i]));
+    poison = __fmaf_rn(x[i], 0.f, poison);
   }
-  top = finite ? top : CUDART_INF_F;
+  if (most < 0x1p60f && gain >= 0x1p-30f && gain <= 0x1p30f) {
+    const float r = __frcp_rn(gain);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = quotient(x[i], gain, r);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(x[i], gain);
+  }
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(y[i]));
+  top = poison == 0.f ? top : CUDART_INF_F;
   top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
   uint32_t s;
   asm("{\n .reg .b16 t;\n cvt.rn.satfinite.e4m3x2.f32 t, 0f00000000, %1;\n cvt.u32.u16 %0, t;\n}\n"
       : "=r"(s)
       : "f"(__fdiv_rn(top, 6.f)));
-  const uint32_t pair = e4m3_pair(s);
-  const float sf = unpack_f16(pair).x;
-  const bool live = top <= FLT_MAX && sf > 0.f;
-  *scale = top <= FLT_MAX ? s : 0x7fu;   // a NaN or an infinity makes the group NaN
+  const float sf = unpack_f16(e4m3_pair(s)).x;
+  if (top < 0x1p60f) {
+    const float rs = __frcp_rn(sf);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = live ? __fdiv_rn(y[i], sf) : 0.f;
+    for (int i = 0; i < 8; ++i) y[i] = quotient(y[i], sf, rs);   // a scale of 0: any value, see below
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(y[i], sf);
+  }
   uint32_t code;
   asm("{\n .reg .b8 a, b, c, d;\n cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
       " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n mov.b32 %0, {a, b, c, d};\n}\n"
       : "=r"(code)
       : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
-  return code;
+  *scale = top <= FLT_MAX ? s : 0x7fu;   // a NaN or an infinity makes the group NaN
+  return top <= FLT_MAX && sf > 0.f ? code : 0u;
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) write_kernel(const WriteParams p) {
+__global__ void __launch_bounds__(kThreads, Held<T>::kFp4 ? 3 : 2) write_kernel(const WriteParams p) {
   using Q = typename Held<T>::Q;
   constexpr int L = D / 16;   // threads a head
   constexpr int E = sizeof(Q);
+  // Query heads in flight. 27 820 tokens: bf16 100 us with 4 (a third CTA an SM and 2: 102),
+  // 4 bits, whose packing wants warps more, 108 with 2 and three CTAs (4 and two: 112).
+  constexpr int U = Held<T>::kFp4 ? 2 : 8 / E;
   const CacheRows& c = p.c;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   // One token a sequence: only row N_b - 1 is written, which an attention call reads
@@ -132,13 +175,13 @@ __global__ void __launch_bounds__(kThreads) write_kernel(const WriteParams p) {
   // without this, and followed by launch_fence.)
   if (p.single) asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 
-  const long f = (long)blockIdx.x * kThreads + threadIdx.x;
+  const uint32_t f = blockIdx.x * blockDim.x + threadIdx.x;   // below 2^31 (checked on the host)
   const int j = (int)(f % L);
-  const int slot = (int)(f / L % p.slots);
-  const int token = (int)min(f / L / p.slots, (long)c.tokens);
+  const uint32_t group = f / L, token_u = group / (uint32_t)p.slots;
+  const int slot = (int)(group - token_u * p.slots);
+  const int token = min((int)token_u, c.tokens);
   int first = 0, end = 0, bad = 0;
   const int b = token < c.tokens ? sequence_of(c, token, first, end) : -1;
-  const long row = b >= 0 ? row_of(c, b, token, first, end, bad) : -1;
 
   // this thread's dims: 8 from `lo`, 8 from `hi`
   const int turning = p.rotary / 16;   // threads whose dims turn
@@ -146,7 +189,40 @@ __global__ void __launch_bounds__(kThreads) write_kernel(const WriteParams p) {
   const int rest = D - p.rotary;
   const int lo = turns ? 8 * j : p.rotary + 8 * (j - turning);
   const int hi = lo + (turns ? p.rotary / 2 : rest / 2);
-  // their 8 pairs: rotate-halves takes dim lo + i with hi + i (pair lo + i), the adjacent
+
+  // Heads slot, slot + slots, ... of the queries, then of keys and values. The loads of the
+  // first ones go out before the chain of lookups that their angles and rows hang on.
+  const int Hq = p.q ? p.Hq : 0;
+  const char* q_lo = p.q + token * p.q_stride + lo * E;
+  const int to_hi = (hi - lo) * E;
+  Raw8<Q> x0[U], x1[U];
+  auto load_q = [&](int h) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (b >= 0 && h + u * p.slots < Hq) {
+        const char* src = q_lo + (long)(h + u * p.slots) * (D * E);
+        x0[u].load(src);
+        x1[u].load(src + to_hi);
+      }
+  };
+  // key and value head i
+  Raw8<Q> k0, k1, v0, v1;
+  auto load_kv = [&](int i) {
+    if (b >= 0 && i < c.Hkv) {
+      const long at = ((long)i * D + lo) * E;
+      k0.load(p.k + token * p.k_stride + at);
+      k1.load(p.k + token * p.k_stride + at + to_hi);
+      v0.load(p.v + token * p.v_stride + at);
+      v1.load(p.v + token * p.v_stride + at + to_hi);
+    }
+  };
+  const int kv_first = (slot + p.slots - Hq % p.slots) % p.slots;
+  const bool few = p.slots > Hq;   // few tokens: a query head or a KV head a thread
+  load_q(slot);
+  if (few) load_kv(kv_first);
+
+  const long row = b >= 0 ? row_of(c, b, token, first, end, bad) : -1;
+  // the pairs: rotate-halves takes dim lo + i with hi + i (pair lo + i), the adjacent
   // layout neighbouring dims (pairs lo / 2 .. and hi / 2 ..)
   float co[8], si[8];
   if (turns && b >= 0) {
@@ -154,7 +230,7 @@ __global__ void __launch_bounds__(kThreads) write_kernel(const WriteParams p) {
     for (int i = 0; i < 8; ++i) {
       const int pair = p.adjacent ? (i < 4 ? lo / 2 + i : hi / 2 + i - 4) : lo + i;
       const int a = min(max((int)__ldg(p.axis + pair), 0), p.axes - 1);
-      int at = __ldcg(p.pos + (size_t)a * c.tokens + token);
+      int at = p.pos[(size_t)a * c.tokens + token];
       if (at < 0 || at >= p.positions) {
         bad |= kDevBadPosition;
         at = at < 0 ? 0 : p.positions - 1;
@@ -167,65 +243,68 @@ __global__ void __launch_bounds__(kThreads) write_kernel(const WriteParams p) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) co[i] = 1.f, si[i] = 0.f;
   }
-
-  const int Hq = p.q ? p.Hq : 0, heads = Hq + 2 * c.Hkv;
-  const int page = 1 << c.log2_page;
-#pragma unroll 2
-  for (int h0 = 0; h0 < heads; h0 += p.slots) {   // the same number of turns for every thread
-    const int h = h0 + slot;
-    const bool is_q = h < Hq, is_v = h >= Hq + c.Hkv;
-    const int hk = h - Hq - (is_v ? c.Hkv : 0);
-    const bool on = b >= 0 && h < heads && (is_q || row >= 0);
-    float x[8], y[8];
-    if (on) {
-      const char* src = (is_q   ? p.q + token * p.q_stride + (long)h * (D * E)
-                         : is_v ? p.v + token * p.v_stride + (long)hk * (D * E)
-                                : p.k + token * p.k_stride + (long)hk * (D * E));
-      load8(src + lo * E, x, static_cast<const Q*>(nullptr));
-      load8(src + hi * E, y, static_cast<const Q*>(nullptr));
-      if (turns && !is_v) {
-        if (p.adjacent) {
+  auto turn = [&](float x[8], float y[8]) {
+    if (!turns) return;
+    if (p.adjacent) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float a0 = x[2 * i], a1 = x[2 * i + 1], b0 = y[2 * i], b1 = y[2 * i + 1];
-            x[2 * i] = __fsub_rn(__fmul_rn(a0, co[i]), __fmul_rn(a1, si[i]));
-            x[2 * i + 1] = __fadd_rn(__fmul_rn(a1, co[i]), __fmul_rn(a0, si[i]));
-            y[2 * i] = __fsub_rn(__fmul_rn(b0, co[4 + i]), __fmul_rn(b1, si[4 + i]));
-            y[2 * i + 1] = __fadd_rn(__fmul_rn(b1, co[4 + i]), __fmul_rn(b0, si[4 + i]));
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float a = x[i], e = y[i];
-            x[i] = __fsub_rn(__fmul_rn(a, co[i]), __fmul_rn(e, si[i]));
-            y[i] = __fadd_rn(__fmul_rn(e, co[i]), __fmul_rn(a, si[i]));
-          }
-        }
+      for (int i = 0; i < 4; ++i) {
+        const float a0 = x[2 * i], a1 = x[2 * i + 1], b0 = y[2 * i], b1 = y[2 * i + 1];
+        x[2 * i] = __fsub_rn(__fmul_rn(a0, co[i]), __fmul_rn(a1, si[i]));
+        x[2 * i + 1] = __fadd_rn(__fmul_rn(a1, co[i]), __fmul_rn(a0, si[i]));
+        y[2 * i] = __fsub_rn(__fmul_rn(b0, co[4 + i]), __fmul_rn(b1, si[4 + i]));
+        y[2 * i + 1] = __fadd_rn(__fmul_rn(b1, co[4 + i]), __fmul_rn(b0, si[4 + i]));
       }
-      if (is_q) {
-        char* dst = p.q_out + ((long)token * p.Hq + h) * (D * E);
-        store8(dst + lo * E, x, static_cast<const Q*>(nullptr));
-        store8(dst + hi * E, y, static_cast<const Q*>(nullptr));
-      } else if constexpr (!Held<T>::kFp4) {
-        char* dst = (is_v ? c.v : c.k) + (row + (long)hk * page) * (D * E);
-        store8(dst + lo * E, x, static_cast<const Q*>(nullptr));
-        store8(dst + hi * E, y, static_cast<const Q*>(nullptr));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float a = x[i], e = y[i];
+        x[i] = __fsub_rn(__fmul_rn(a, co[i]), __fmul_rn(e, si[i]));
+        y[i] = __fadd_rn(__fmul_rn(e, co[i]), __fmul_rn(a, si[i]));
       }
     }
-    if constexpr (Held<T>::kFp4) {
-      const bool mine = on && !is_q;
-      if (__any_sync(0xffffffffu, mine)) {   // the lanes of a group agree; the shuffles need all
-        if (!mine) {
+  };
+
+  for (int h = slot; h < Hq; h += U * p.slots) {
+    if (h != slot) load_q(h);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = y[i] = 0.f;
-        }
-        const float gain = mine ? __ldcg((is_v ? c.v_gain : c.k_gain) + hk) : 1.f;
+    for (int u = 0; u < U; ++u)
+      if (b >= 0 && h + u * p.slots < Hq) {
+        float x[8], y[8];
+        x0[u].get(x);
+        x1[u].get(y);
+        turn(x, y);
+        char* dst = p.q_out + ((long)token * p.Hq + h + u * p.slots) * (D * E) + lo * E;
+        store8(dst, x, static_cast<const Q*>(nullptr));
+        store8(dst + to_hi, y, static_cast<const Q*>(nullptr));
+      }
+  }
+
+  const int page = 1 << c.log2_page;
+#pragma unroll 1
+  for (int i0 = 0; i0 < c.Hkv; i0 += p.slots) {   // the same number of turns for every thread
+    const int i = i0 + kv_first;
+    const bool on = row >= 0 && i < c.Hkv;
+    if (i0 > 0 || !few) load_kv(i);
+    const long at = row + (long)i * page;
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {   // keys, then values
+      float x[8], y[8];
+      if (on) {
+        (which ? v0 : k0).get(x);
+        (which ? v1 : k1).get(y);
+        if (!which) turn(x, y);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = y[e] = 0.f;
+      }
+      if constexpr (Held<T>::kFp4) {
+        if (!__any_sync(0xffffffffu, on)) continue;   // the lanes of a group agree; the shuffles need all
+        const float gain = on ? __ldg((which ? c.v_gain : c.k_gain) + i) : 1.f;
         uint32_t sx, sy;
         const uint32_t cx = pack_codes(x, gain, &sx), cy = pack_codes(y, gain, &sy);
-        if (mine) {
-          const long at = row + (long)hk * page;
-          char* codes = (is_v ? c.v : c.k) + at * (D / 2);
-          uint8_t* scales = (is_v ? c.v_scale : c.k_scale) + at * (D / 16);
+        if (on) {
+          char* codes = (which ? c.v : c.k) + at * (D / 2);
+          uint8_t* scales = (which ? c.v_scale : c.k_scale) + at * (D / 16);
           *reinterpret_cast<uint32_t*>(codes + lo / 2) = cx;
           *reinterpret_cast<uint32_t*>(codes + hi / 2) = cy;
           if ((lo & 15) == 0) {
@@ -233,64 +312,106 @@ __global__ void __launch_bounds__(kThreads) write_kernel(const WriteParams p) {
             scales[hi / 16] = (uint8_t)sy;
           }
         }
+      } else if (on) {
+        char* dst = (which ? c.v : c.k) + at * (D * E) + lo * E;
+        store8(dst, x, static_cast<const Q*>(nullptr));
+        store8(dst + to_hi, y, static_cast<const Q*>(nullptr));
       }
     }
   }
   if (bad) atomicOr(c.status, bad);
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) read_kernel(const ReadParams p) {
-  constexpr int L = D / 16;
+// A CTA takes p.tile tokens, whose rows its first threads look up together (the lookups are
+// five loads that hang on one another, as long as all the rest). Lanes take 16 bytes of the
+// output, so that a row is written in whole lines, and a group of lanes goes through a
+// token's keys and values, four heads in flight.
+template <typename T, int D, typename O>
+__global__ void __launch_bounds__(kThreads, 6) read_kernel(const ReadParams p) {
+  constexpr int N = 16 / sizeof(O);   // dims a lane
+  constexpr int L = D / N;
+  constexpr int U = 4;
+  __shared__ long s_row[kReadTile];
   const CacheRows& c = p.c;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  const long f = (long)blockIdx.x * kThreads + threadIdx.x;
-  const int j = (int)(f % L);
-  const int h = (int)(f / L % c.Hkv);
-  const long token_l = f / L / c.Hkv;
-  if (token_l >= c.tokens) return;
-  const int token = (int)token_l;
-  int first = 0, end = 0, bad = 0;
-  const int b = sequence_of(c, token, first, end);
-  if (b < 0) return;   // behind the last sequence
-  const long row = row_of(c, b, token, first, end, bad);
-  const long at = row + ((long)h << c.log2_page);
-  const long out = ((long)token * c.Hkv + h) * D + 16 * j;
+  const int t0 = blockIdx.x * p.tile;
+  if ((int)threadIdx.x < p.tile) {
+    const int token = t0 + threadIdx.x;
+    int first = 0, end = 0, bad = 0;
+    const int b = token < c.tokens ? sequence_of(c, token, first, end) : -1;
+    s_row[threadIdx.x] = b >= 0 ? row_of(c, b, token, first, end, bad) : -2;   // -2: behind the last sequence
+    if (bad) atomicOr(c.status, bad);
+  }
+  __syncthreads();
+  const int j = threadIdx.x % L;
+  const int dim = N * j;
+  const int groups = kThreads / L, per = groups / p.share;   // p.share groups split a token's heads
+  const int part = threadIdx.x / L % p.share;
+  for (int k = threadIdx.x / L / p.share; k < p.tile; k += per) {
+    const int token = t0 + k;
+    const long row = s_row[k];
+    if (row < -1) continue;
+    for (int i0 = part; i0 < 2 * c.Hkv; i0 += U * p.share) {
+      uint32_t code[U], scale[U];
+      float gain[U];
+      float x[U][N];
 #pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    float x[16];
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * p.share;
+        const bool is_v = i >= c.Hkv, on = row >= 0 && i < 2 * c.Hkv;
+        const int h = i - (is_v ? c.Hkv : 0);
+        const long at = row + ((long)h << c.log2_page);
+        if constexpr (Held<T>::kFp4) {
+          code[u] = scale[u] = 0;
+          gain[u] = 0.f;
+          if (on) {
+            const char* src = (is_v ? c.v : c.k) + at * (D / 2) + dim / 2;
+            code[u] = N == 8 ? __ldcg(reinterpret_cast<const uint32_t*>(src)) : __ldcg(reinterpret_cast<const uint16_t*>(src));
+            scale[u] = __ldcg((is_v ? c.v_scale : c.k_scale) + at * (D / 16) + dim / 16);
+            gain[u] = __ldg((is_v ? c.v_gain : c.k_gain) + h);
+          }
+        } else {
+          const T* src = reinterpret_cast<const T*>(is_v ? c.v : c.k) + at * D + dim;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = 0.f;
-    if (row >= 0) {
-      if constexpr (Held<T>::kFp4) {
-        const uint2 w = __ldcg(reinterpret_cast<const uint2*>((which ? c.v : c.k) + at * (D / 2)) + j);
-        const float s = unpack_f16(e4m3_pair(__ldcg((which ? c.v_scale : c.k_scale) + at * (D / 16) + j))).x;
-        const float gain = __ldcg((which ? c.v_gain : c.k_gain) + h);
-        uint32_t v[8];
-        fp4_decode8(w.x, v);
-        fp4_decode8(w.y, v + 4);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 e = unpack_f16(v[i]);
-          x[2 * i] = __fmul_rn(__fmul_rn(e.x, s), gain);
-          x[2 * i + 1] = __fmul_rn(__fmul_rn(e.y, s), gain);
+          for (int e = 0; e < N; e += 4) {
+            float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (on) {
+              if constexpr (sizeof(T) == 4) {
+                q = __ldcg(reinterpret_cast<const float4*>(src + e));
+              } else {
+                const uint2 w = __ldcg(reinterpret_cast<const uint2*>(src + e));
+                q = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                                __uint_as_float(w.y & 0xffff0000u));
+              }
+            }
+            x[u][e] = q.x, x[u][e + 1] = q.y, x[u][e + 2] = q.z, x[u][e + 3] = q.w;
+          }
         }
-      } else {
-        const char* src = (which ? c.v : c.k) + (at * D + 16 * j) * (long)sizeof(T);
-        load8(src, x, static_cast<const T*>(nullptr));
-        load8(src + 8 * sizeof(T), x + 8, static_cast<const T*>(nullptr));
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * p.share;
+        if (i >= 2 * c.Hkv) break;
+        const bool is_v = i >= c.Hkv;
+        if constexpr (Held<T>::kFp4) {
+          const float s = unpack_f16(e4m3_pair(scale[u])).x;
+          uint32_t v[4];
+          fp4_decode8(code[u], v);
+#pragma unroll
+          for (int e = 0; e < N / 2; ++e) {
+            const float2 y = unpack_f16(v[e]);
+            x[u][2 * e] = __fmul_rn(__fmul_rn(y.x, s), gain[u]);
+            x[u][2 * e + 1] = __fmul_rn(__fmul_rn(y.y, s), gain[u]);
+          }
+        }
+        O* dst = reinterpret_cast<O*>(is_v ? p.v_out : p.k_out) + ((long)token * c.Hkv + i - (is_v ? c.Hkv : 0)) * D + dim;
+        if constexpr (sizeof(O) == 4)
+          __stcs(reinterpret_cast<float4*>(dst), make_float4(x[u][0], x[u][1], x[u][2], x[u][3]));
+        else
+          store8(reinterpret_cast<char*>(dst), x[u], static_cast<const __nv_bfloat16*>(nullptr));
       }
     }
-    char* dst = which ? p.v_out : p.k_out;
-    if (p.out_f32) {
-      store8(dst + out * 4, x, static_cast<const float*>(nullptr));
-      store8(dst + out * 4 + 32, x + 8, static_cast<const float*>(nullptr));
-    } else {
-      store8(dst + out * 2, x, static_cast<const __nv_bfloat16*>(nullptr));
-      store8(dst + out * 2 + 16, x + 8, static_cast<const __nv_bfloat16*>(nullptr));
-    }
   }
-  if (bad) atomicOr(c.status, bad);
 }
 
 __global__ void fence_kernel() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
@@ -310,6 +431,13 @@ cudaError_t launch_early(void (*kernel)(P...), long threads, cudaStream_t s, con
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// How many groups of `lanes` threads share a token's heads: as many as bring the grid to
+// kPerSm threads an SM, and no more than there are heads.
+int slots_for(int tokens, int lanes, int heads, int num_sms) {
+  const long groups = (long)num_sms * kPerSm / lanes, slots = (groups + tokens - 1) / tokens;
+  return (int)(slots < 1 ? 1 : slots > heads ? heads : slots);
+}
+
 template <typename T, int D>
 cudaError_t write_rows(const WriteParams& p, cudaStream_t s) {
   const cudaError_t e = launch_early(write_kernel<T, D>, (long)p.c.tokens * p.slots * (D / 16), s, p);
@@ -318,7 +446,9 @@ cudaError_t write_rows(const WriteParams& p, cudaStream_t s) {
 
 template <typename T, int D>
 cudaError_t read_rows(const ReadParams& p, cudaStream_t s) {
-  return launch_early(read_kernel<T, D>, (long)p.c.tokens * p.c.Hkv * (D / 16), s, p);
+  const long threads = (long)(p.c.tokens + p.tile - 1) / p.tile * kThreads;
+  return p.out_f32 ? launch_early(read_kernel<T, D, float>, threads, s, p)
+                   : launch_early(read_kernel<T, D, __nv_bfloat16>, threads, s, p);
 }
 
 }  // namespace
@@ -328,11 +458,7 @@ cudaError_t launch_fence(cudaStream_t s) {
 }
 
 cudaError_t launch_write_rows(int dtype, int head_dim, int num_sms, WriteParams p, cudaStream_t s) {
-  // as many threads as the SMs hold at a quarter of their registers, and no more slots than heads
-  const long groups = (long)num_sms * 1024 / (head_dim / 16);
-  const int heads = (p.q ? p.Hq : 0) + 2 * p.c.Hkv;
-  long slots = (groups + p.c.tokens - 1) / p.c.tokens;
-  p.slots = (int)(slots < 1 ? 1 : slots > heads ? heads : slots);
+  p.slots = slots_for(p.c.tokens, head_dim / 16, (p.q ? p.Hq : 0) + p.c.Hkv, num_sms);
   switch (dtype) {
     case FASTOCR_DTYPE_BF16:
       return head_dim == 64 ? write_rows<__nv_bfloat16, 64>(p, s) : write_rows<__nv_bfloat16, 128>(p, s);
@@ -341,7 +467,13 @@ cudaError_t launch_write_rows(int dtype, int head_dim, int num_sms, WriteParams 
   return head_dim == 64 ? write_rows<Fp4, 64>(p, s) : write_rows<Fp4, 128>(p, s);
 }
 
-cudaError_t launch_read_rows(int dtype, int head_dim, const ReadParams& p, cudaStream_t s) {
+cudaError_t launch_read_rows(int dtype, int head_dim, int num_sms, ReadParams p, cudaStream_t s) {
+  // tiles of up to kReadTile tokens, four CTAs an SM; a tile of fewer tokens than the CTA has
+  // groups of lanes splits their heads
+  p.tile = (int)std::max(1L, std::min((long)kReadTile, (long)p.c.tokens / (4L * num_sms)));
+  const int groups = kThreads / (head_dim / (p.out_f32 ? 4 : 8));
+  p.share = 1;
+  while (p.share * 2 * p.tile <= groups) p.share *= 2;
   switch (dtype) {
     case FASTOCR_DTYPE_BF16:
       return head_dim == 64 ? read_rows<__nv_bfloat16, 64>(p, s) : read_rows<__nv_bfloat16, 128>(p, s);

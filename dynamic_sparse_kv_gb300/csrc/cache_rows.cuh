@@ -35,7 +35,7 @@ struct WriteParams {
   const int8_t* axis;      // [rotary / 2]
   const int32_t* pos;      // [axes, tokens]
   int positions, rotary, axes, adjacent;
-  int slots;               // threads groups that share a token's heads
+  int slots;               // groups of threads that share a token's heads
   int single;              // one token a sequence
 };
 
@@ -44,11 +44,12 @@ struct ReadParams {
   char* k_out;             // [tokens, H_kv, d]
   char* v_out;
   int out_f32;
+  int tile, share;         // tokens a CTA takes; groups of lanes that split a token's heads
 };
 
 // dtype: FASTOCR_DTYPE_*; head_dim 64 or 128
 cudaError_t launch_write_rows(int dtype, int head_dim, int num_sms, WriteParams p, cudaStream_t s);
-cudaError_t launch_read_rows(int dtype, int head_dim, const ReadParams& p, cudaStream_t s);
+cudaError_t launch_read_rows(int dtype, int head_dim, int num_sms, ReadParams p, cudaStream_t s);
 // An empty kernel that ends once everything before it on the stream is complete: the kernel
 // behind it may read, before its own wait, whatever was written before.
 cudaError_t launch_fence(cudaStream_t s);

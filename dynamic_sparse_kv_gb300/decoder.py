@@ -470,22 +470,20 @@ class DecodeAttention:
                 hook(l, False)
 
     # ------------------------------------------------------------ rows in and out
-    def _packed(self, t, name, heads, tokens=None):
-        """Tokens' heads as the library takes them: (tensor, elements from token to token)."""
-        dt, dev, d = self.k_cache.dtype, self.k_cache.device, self.head_dim
-        if (t.dim() != 3 or t.shape[1:] != (heads, d) or t.dtype != dt or t.device != dev
-                or (tokens is not None and t.shape[0] != tokens)):
-            n = "tokens" if tokens is None else tokens
-            raise ValueError(f"{name} must be a {dt} tensor of shape ({n}, {heads}, {d}) on {dev}, not {t.dtype} "
-                             f"{tuple(t.shape)} on {t.device}")
-        if t.shape[0] <= 1:
-            good, step = t.shape[0] == 0 or t[0].is_contiguous(), heads * d
-        else:
-            good, step = t[0].is_contiguous() and t.stride(0) >= heads * d, t.stride(0)
-        if not good or step * t.element_size() % 16:
+    def _packed(self, t, name, heads, tokens):
+        """Elements from token to token of t [tokens, heads, d], as the library takes it."""
+        c, d = self.k_cache, self.head_dim
+        s = t.stride()
+        if t.shape == (tokens, heads, d) and t.dtype is c.dtype and t.device == c.device:
+            # a stride of a dimension of one says nothing
+            step = s[0] if tokens > 1 else heads * d
+            if (s[2] == 1 and (heads == 1 or s[1] == d) and step >= heads * d
+                    and step * t.element_size() % 16 == 0):
+                return step
             raise ValueError(f"a token of {name} must be contiguous and tokens a multiple of 16 bytes apart, "
-                             f"not with strides {t.stride()}")
-        return step
+                             f"not with strides {s}")
+        raise ValueError(f"{name} must be a {c.dtype} tensor of shape ({tokens}, {heads}, {d}) on {c.device}, not "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
 
     def write_layer(self, l, k, v, *, q=None, out_q=None, rotary=None, pos=None, q_start=None, stream=None):
         """New tokens of layer l: k, v [T, H_kv, d] go to the last rows of their sequences
@@ -497,16 +495,19 @@ class DecodeAttention:
         Rotary, with pos [axes, T] int32; None: nothing turns. In a step, call it for a layer
         before the layer attends, e.g. in step(hook=...)."""
         dev, T = self.k_cache.device, k.shape[0]
-        ks = self._packed(k, "k", self.kv_heads)
+        ks = self._packed(k, "k", self.kv_heads, T)
         vs = self._packed(v, "v", self.kv_heads, T)
+        q_at = o_at = pos_at = start_at = rot = None
         qs = 0
         if (q is None) != (out_q is None):
             raise ValueError("q and out_q come together")
         if q is not None:
             qs = self._packed(q, "q", self.q_heads, T)
             N.check_tensor(out_q, "out_q", (T, self.q_heads, self.head_dim), self.k_cache.dtype, dev)
+            q_at, o_at = q.data_ptr(), out_q.data_ptr()
         if q_start is not None:
             N.check_tensor(q_start, "q_start", (self.batch + 1,), torch.int32, dev)
+            start_at = q_start.data_ptr()
         elif T != self.batch:
             raise ValueError(f"one token a sequence ({self.batch}), or q_start")
         if rotary is not None:
@@ -515,13 +516,11 @@ class DecodeAttention:
             if pos is None:
                 raise ValueError("rotary needs pos")
             N.check_tensor(pos, "pos", (rotary.axes, T), torch.int32, dev)
+            pos_at, rot = pos.data_ptr(), rotary.c
         if T == 0:
             return
-        tokens = N.fastocr_tokens(q.data_ptr() if q is not None else None, k.data_ptr(), v.data_ptr(), qs, ks, vs,
-                                  out_q.data_ptr() if q is not None else None,
-                                  pos.data_ptr() if rotary is not None else None,
-                                  q_start.data_ptr() if q_start is not None else None, T)
-        N.fastocr_write_rows(self.handle, self.kv[l], tokens, rotary.c if rotary is not None else None, stream)
+        tokens = N.fastocr_tokens(q_at, k.data_ptr(), v.data_ptr(), qs, ks, vs, o_at, pos_at, start_at, T)
+        N.fastocr_write_rows(self.handle, self.kv[l], tokens, rot, stream)
 
     def read_layer(self, l, row_start, out_k, out_v, stream=None):
         """The last rows of every sequence of layer l as values: rows N_b - T_b .. N_b - 1 with

@@ -441,7 +441,7 @@ fastocr_status fastocr_cross_attend(fastocr_handle* h, const void* q, const fast
  * Overlap: everything is read after the preceding kernel completes. With start NULL only
  * rows N_b - 1 are written, as the attention calls expect of the kernel before them; with
  * start a second, empty kernel follows, so that any call may come next.
- * tokens * (H_q + 2 H_kv) * d < 2^34. Errors: NULL, INVALID (strides, rotary, tokens !=
+ * tokens * (H_q + 2 H_kv) * d < 2^33. Errors: NULL, INVALID (strides, rotary, tokens !=
  * B without start, another device current), UNSUPPORTED (rotary_dim), ALIGN, CUDA. */
 fastocr_status fastocr_write_rows(fastocr_handle* h, const fastocr_kv* kv, const fastocr_tokens* tokens,
                                   const fastocr_rotary* rotary, fastocr_stream stream);
