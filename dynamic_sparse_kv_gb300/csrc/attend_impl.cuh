@@ -417,6 +417,12 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
   using E = EpiSmem<D, kWarps>;
   constexpr bool kMma = Held<T>::kMma, kFp4 = Held<T>::kFp4;
   using TQ = typename Held<T>::Q;
+  // A cache in 4 bits and a list without a selection: no row list in shared memory, every
+  // warp looks up its own tiles' rows, one tile ahead of their copies. (The list is made
+  // in rounds with a barrier and an empty pipeline between them, which a tile of 8 KB
+  // bears, but one of 2.3 KB does not: 32 sequences x 8.4k, without any copy or
+  // product, spent 34 of 58 us on them.)
+  constexpr bool kDirect = kFp4 && MODE != kSparse;
   // These modes give the second product their probabilities in two bf16 parts, the
   // value cut off and its rounded remainder (together within 2^-15), against the same V
   // fragments: as close to 64 bits as fp32 probabilities (relative error 0.0016 to
@@ -558,9 +564,65 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
     doff[i] = kFp4 ? fp4_place<D>(r, ch_lane) : r * ROWB + ((ch_lane ^ (r & 7)) << 4);
   }
   const uint64_t pol_stream = l2_policy_evict_first();   // K/V rows are read once
+  // 4 bits: which of a stage's 16 rows exist, in shared memory (a word a stage of this
+  // warp), and the stages where all do
+  uint32_t whole = 0;
+  uint32_t* const exist = reinterpret_cast<uint32_t*>(smem + SM::kExist) + warp * ST;
+  const uint8_t* scale_lane = lane < kTile ? p.k_scale : p.v_scale;
+  // copies tile j of this warp, whose row `lane % 16` is `row` (-1: none). Codes: a 16-byte
+  // chunk of a K and a V row a lane and turn; scales: a K or a V row a lane.
+  auto issue_fp4 = [&](int j, int row) {
+    const int stage = j % ST;
+    const uint32_t sb = smem_u32(pipe + stage * SM::kStageBytes);
+    const uint32_t there = __ballot_sync(0xffffffffu, row >= 0);
+    auto copy = [&](bool all) {
+#pragma unroll
+      for (int i = 0; i < kIss; ++i) {
+        const int rr = __shfl_sync(0xffffffffu, row, i * kRowsPerInst + row_lane);
+        const bool ok = all || rr >= 0;
+        const size_t off = (size_t)(uint32_t)(ok ? rr : 0) * ROWB;
+        cp_async16(sb + doff[i], kg_lane + off, ok ? 16 : 0, pol_stream);
+        cp_async16(sb + doff[i] + kTile * ROWB, vg_lane + off, ok ? 16 : 0, pol_stream);
+      }
+      const bool ok = all || row >= 0;
+      if constexpr (kFp4)
+        cp_async_small<SM::kScaleBytes>(sb + 2 * kTile * ROWB + lane * SM::kScaleBytes,
+                                        scale_lane + (size_t)(uint32_t)(ok ? row : 0) * SM::kScaleBytes,
+                                        ok ? SM::kScaleBytes : 0, pol_stream);
+    };
+    if (there == 0xffffffffu) {
+      copy(true);
+      whole |= 1u << stage;
+    } else {
+      copy(false);
+      if (lane == 0) exist[stage] = there;
+      whole &= ~(1u << stage);
+    }
+  };
+  // direct: looks up entry `lane % 16` of tile j: its position (-1: no such entry) and page
+  auto look_up = [&](int j, int n_list, int& pos, int& page) {
+    const int u = (warp + j * kWarps) * kTile + (lane & (kTile - 1));
+    pos = u < n_list ? pos_of(u) : -1;
+    page = pos >= 0 ? __ldcg(bt + (pos >> p.log2_page)) : -1;
+  };
+  auto row_at = [&](int pos, int page) -> int {
+    const bool there = (uint32_t)page < (uint32_t)p.num_pages;
+    if (pos >= 0 && !there) bad |= kDevBadPage;
+    return there ? ((page * p.Hkv + hkv) << p.log2_page) | (pos & page_mask) : -1;
+  };
   auto issue = [&](int j, int n_round) {
     const int stage = j % ST;
     const int base = (warp + j * kWarps) * kTile;
+    if constexpr (kFp4) {
+      const int at = base + (lane & (kTile - 1));
+      int row = at < n_round ? srow[at] : -1;
+      if (row >= n_rows) {   // never true for a resolved row; guards the copy anyway
+        bad |= kDevInternal;
+        row = -1;
+      }
+      issue_fp4(j, row);
+      return;
+    }
     const uint32_t sb = smem_u32(pipe + stage * SM::kStageBytes);
     int rows[kIss];
 #pragma unroll
@@ -578,14 +640,6 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
       const int bytes = rows[i] >= 0 ? 16 : 0;
       cp_async16(sb + doff[i], kg_lane + off, bytes, pol_stream);
       cp_async16(sb + doff[i] + kTile * ROWB, vg_lane + off, bytes, pol_stream);
-    }
-    if constexpr (kFp4) {   // the scales of 16 K rows and 16 V rows, a row a lane
-      const int r = lane & (kTile - 1);
-      int row = base + r < n_round ? srow[base + r] : -1;
-      if (row >= n_rows) row = -1;
-      const uint8_t* src = (lane < kTile ? p.k_scale : p.v_scale) + (size_t)max(row, 0) * SM::kScaleBytes;
-      cp_async_small<SM::kScaleBytes>(sb + 2 * kTile * ROWB + lane * SM::kScaleBytes, src,
-                                      row >= 0 ? SM::kScaleBytes : 0, pol_stream);
     }
   };
   // pull a row's K and V into L2
@@ -631,8 +685,9 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
     for (int j = 0; j < kPer; ++j)
       if (n_txt_pad + tid + j * kThreads >= spec_u1) spec_raw[j] = -1;
   }
-  const int n_pre = min(kSliceMax, n_txt_pad + n_sel_pad);   // entries before the current token
-  {
+  // entries before the current token (of the first round)
+  const int n_pre = kDirect ? n_txt_pad : min(kSliceMax, n_txt_pad + n_sel_pad);
+  if constexpr (!kDirect) {
     const int u_staged = kWarps * ST * kTile;   // entries the pre-wait tiles can cover
     int tpos[kPer], tpage[kPer], sps[kPer], spage[kPer];
 #pragma unroll
@@ -705,9 +760,27 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
   if (tid == 0)
     prefetch_l2(static_cast<const TQ*>(p.q) + ((size_t)q_row * p.Hq + (size_t)hkv * p.g) * D,
                 p.g * D * (uint32_t)sizeof(TQ));
-  __syncthreads();
+  if constexpr (kDirect) {
+    int pos[ST], page[ST];
+#pragma unroll
+    for (int j = 0; j < ST; ++j) look_up(j, n_pre, pos[j], page[j]);
+    if (c.has_cur && warp == 0) {   // the current token's row, which is final; its K/V may not be
+      const int at = __ldcg(bt + (c.cur_pos >> p.log2_page));
+      if (lane == 0 && at >= 0 && at < p.num_pages)
+        prefetch_row(((at * p.Hkv + hkv) << p.log2_page) | (c.cur_pos & page_mask));
+    }
+#pragma unroll
+    for (int j = 0; j < ST; ++j)
+      if (pre_issued == j && (warp + j * kWarps + 1) * kTile <= n_pre) {
+        issue_fp4(j, row_at(pos[j], page[j]));
+        cp_async_commit();
+        ++pre_issued;
+      }
+  } else {
+    __syncthreads();
+  }
 #pragma unroll 1
-  for (int j = 0; j < ST; ++j) {
+  for (int j = 0; j < (kDirect ? 0 : ST); ++j) {
     const int end = (warp + j * kWarps + 1) * kTile;
     if (pre_issued == j && end <= n_pre) {
       issue(j, n_pre);
@@ -723,10 +796,15 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
   // selection, all in flight together. The tile follows the staged ones in
   // its warp's order (sparse: under the speculative layout, redone below if
   // the speculation fails).
-  if (c.has_cur && n_pre < kSliceMax && !sel_pending) {
+  if (c.has_cur && (kDirect || n_pre < kSliceMax) && !sel_pending) {
     const int t_cur = n_pre / kTile;   // n_pre is a multiple of kTile here
     if (warp == t_cur % kWarps && pre_issued == t_cur / kWarps && pre_issued < ST) {
-      issue(pre_issued, n_pre + 1);
+      if constexpr (kDirect) {
+        int pos, page;
+        look_up(pre_issued, n_pre + 1, pos, page);
+        issue_fp4(pre_issued, row_at(pos, page));
+      } else
+        issue(pre_issued, n_pre + 1);
       cp_async_commit();
       ++pre_issued;
     }
@@ -737,8 +815,7 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
   WarpStateMma<D> sm_;
   WarpStateF32<D> sf_;
   const int gid = lane >> 2, tig = lane & 3;
-  float sl0 = p.scale_log2, sl1 = p.scale_log2;   // logit scale of this lane's two heads
-  float v_gain = 1.f;
+  float sl0 = 0.f, sl1 = 0.f, v_gain = 1.f;   // 4 bits: logit scale of this lane's two heads
   if constexpr (kFp4) {
     v_gain = __ldg(p.v_gain + hkv);
     const float k_scale = p.scale_log2 * __ldg(p.k_gain + hkv);
@@ -875,9 +952,8 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
     float cc[kChains][4];
 #pragma unroll
     for (int q = 0; q < kChains; ++q) cc[q][0] = cc[q][1] = cc[q][2] = cc[q][3] = 0.f;
-    if constexpr (kFp4) fp4_keys<D, kChains>(kA, kA + 2 * kTile * ROWB, lane, sm_.qf, cc);
 #pragma unroll
-    for (int ks = 0; ks < (kFp4 ? 0 : D / 16); ++ks) {
+    for (int ks = 0; ks < D / 16; ++ks) {
       // chunk 2ks + (lane >> 4) of row `lane & 15`, swizzled: a lane
       // constant for ks % 4 plus 8 chunks per 4 ks
       uint32_t a[4];
@@ -896,13 +972,12 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
   // of work-list entries [tbase, tbase + 16) whose V rows start at vA.
   auto tile_rest = [&](const float cfr[4], uint32_t vA, int tbase, int n_round) {
     // cache positions of keys gid and gid+8 (-1: masked or past the end)
-    const int uA = tbase + (kFp4 ? fp4_key(gid) : gid);   // row gid of the fragments
-    const int posA = uA < n_round ? spos[uA] : -1;
-    const int posB = uA + 8 < n_round ? spos[uA + 8] : -1;
-    const float s0 = posA >= 0 ? cfr[0] * sl0 : kNegInf;
-    const float s1 = posA >= 0 ? cfr[1] * sl1 : kNegInf;
-    const float s2 = posB >= 0 ? cfr[2] * sl0 : kNegInf;
-    const float s3 = posB >= 0 ? cfr[3] * sl1 : kNegInf;
+    const int posA = tbase + gid < n_round ? spos[tbase + gid] : -1;
+    const int posB = tbase + gid + 8 < n_round ? spos[tbase + gid + 8] : -1;
+    const float s0 = posA >= 0 ? cfr[0] * p.scale_log2 : kNegInf;
+    const float s1 = posA >= 0 ? cfr[1] * p.scale_log2 : kNegInf;
+    const float s2 = posB >= 0 ? cfr[2] * p.scale_log2 : kNegInf;
+    const float s3 = posB >= 0 ? cfr[3] * p.scale_log2 : kNegInf;
     if (stores_logits(MODE)) {
       const int atA = logit_pos(posA), atB = logit_pos(posB);
       if (atA >= c.img_start && atA < c.img_start + c.n_img)
@@ -916,15 +991,11 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
     // max and the output scale are updated only when a score exceeds the
     // running max by more than kLazyMax, so most tiles need neither the
     // cross-lane max nor a rescale; probabilities stay below 2^kLazyMax.
-    // 4 bits: the running max is kept kHeadroom below the true one, so that the
-    // probabilities use fp16's range (up to 2^(kLazyMax + kHeadroom), and 2^-24 of
-    // the range below is 2^-31 of the largest).
-    constexpr float kHeadroom = kFp4 ? 7.f : 0.f, kLimit = kLazyMax + kHeadroom;
-    if (__any_sync(0xffffffffu, s0 > sm_.m[0] + kLimit || s2 > sm_.m[0] + kLimit ||
-                                    s1 > sm_.m[1] + kLimit || s3 > sm_.m[1] + kLimit)) {
+    if (__any_sync(0xffffffffu, s0 > sm_.m[0] + kLazyMax || s2 > sm_.m[0] + kLazyMax ||
+                                    s1 > sm_.m[1] + kLazyMax || s3 > sm_.m[1] + kLazyMax)) {
       const float mx0 = warp_max_gid(fmaxf(s0, s2));
       const float mx1 = warp_max_gid(fmaxf(s1, s3));
-      const float mn0 = fmaxf(sm_.m[0], mx0 - kHeadroom), mn1 = fmaxf(sm_.m[1], mx1 - kHeadroom);
+      const float mn0 = fmaxf(sm_.m[0], mx0), mn1 = fmaxf(sm_.m[1], mx1);
       const float al0 = fast_exp2(sm_.m[0] - (mn0 == kNegInf ? 0.f : mn0));
       const float al1 = fast_exp2(sm_.m[1] - (mn1 == kNegInf ? 0.f : mn1));
       sm_.l[0] *= al0;
@@ -959,9 +1030,6 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
     if constexpr (kTwoPart) {   // cut off, not rounded: the remainder is then positive
       pk01 = __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
       pk23 = __byte_perm(__float_as_uint(p2), __float_as_uint(p3), 0x7632);
-    } else if constexpr (kFp4) {   // fp16: within 2^-11, and V's values are whole in it
-      pk01 = pack_f16(p0, p1);
-      pk23 = pack_f16(p2, p3);
     } else {
       pk01 = pack_bf16(p0, p1);
       pk23 = pack_bf16(p2, p3);
@@ -975,10 +1043,6 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
         sm_.il[0] += (iA ? p0 : 0.f) + (iB ? p2 : 0.f);
         sm_.il[1] += (iA ? p1 : 0.f) + (iB ? p3 : 0.f);
       }
-    } else if constexpr (kFp4) {
-      const float2 r01 = unpack_f16(pk01), r23 = unpack_f16(pk23);
-      sm_.l[0] += r01.x + r23.x;
-      sm_.l[1] += r01.y + r23.y;
     } else {
       sm_.l[0] += __uint_as_float(pk01 << 16) + __uint_as_float(pk23 << 16);
       sm_.l[1] += __uint_as_float(pk01 & 0xffff0000u) + __uint_as_float(pk23 & 0xffff0000u);
@@ -993,9 +1057,8 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
       bl0 = movmatrix_trans(pack_bf16(rest(p0), rest(p1)));
       bl1 = movmatrix_trans(pack_bf16(rest(p2), rest(p3)));
     }
-    if constexpr (kFp4) fp4_values<D>(vA, vA + kTile * (ROWB + SM::kScaleBytes), lane, bb0, bb1, sm_.acc);
 #pragma unroll
-    for (int mt = 0; mt < (kFp4 ? 0 : D / 16); ++mt) {
+    for (int mt = 0; mt < D / 16; ++mt) {
       uint32_t a[4];
       ldmatrix_x4_trans(a, vA + voff[mt & 3] + (mt >> 2) * 128);
       // O^T[16 dims x 8 heads] += V^T[16 dims x 16 keys] . P^T[16 keys x 8 heads]
@@ -1004,8 +1067,150 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
     }
   };
 
+  // The tile body for a cache in 4 bits. What is left of a tile beside unpacking it counts here:
+  // the exponents e = s - max come from one multiply-add each, the running max is a finite
+  // number from the start (kUnset until a score arrives), and a tile whose rows all exist
+  // (`whole`, found when it was staged) needs no look at its positions unless the mode
+  // stores logits or sums the image's share. The running max is kept kHeadroom below the
+  // true one, so that the probabilities use fp16's range: up to 2^(kLazyMax + kHeadroom),
+  // and what is below 2^-24 is below 2^-31 of the largest. They are rounded to fp16
+  // (2^-11 each, at random) for the product only; V's values are whole in fp16.
+  constexpr float kHeadroom = 7.f, kLimit = kLazyMax + kHeadroom, kUnset = -1e30f;
+  float mb0 = kUnset, mb1 = kUnset;
+  Fp4Keys<D> key;        // of the next tile
+  Fp4Values<D> value;    // of this one
+  auto keys_fp4 = [&](float cfr[4]) {
+    float cc[2][4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) cc[0][e] = cc[1][e] = 0.f;
+    key.product(sm_.qf, cc);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) cfr[e] = cc[0][e] + cc[1][e];
+  };
+  // P^T of the tile as B fragments
+  auto probabilities_fp4 = [&](const float cfr[4], int it, int n_list, uint32_t& bb0, uint32_t& bb1) {
+    constexpr bool kPositions = stores_logits(MODE) || MODE == kProfile;
+    const bool whole_tile = whole >> (it % ST) & 1u;
+    // positions of rows gid and gid + 8 of the fragments, negative for a masked one (the modes
+    // that need more than that of them have no selection, so it is a matter of arithmetic)
+    int posA = 0, posB = 0;
+    if (kPositions || !whole_tile) {
+      const uint32_t there = whole_tile ? ~0u : exist[it % ST] >> fp4_key(gid);
+      if constexpr (kPositions) {
+        const int uA = (warp + it * kWarps) * kTile + fp4_key(gid);
+        posA = uA < n_list ? pos_of(uA) : -1;
+        posB = uA + 8 < n_list ? pos_of(uA + 8) : -1;
+      }
+      if (!(there & 1u)) posA = masked<MODE>(posA);
+      if (!(there & 0x100u)) posB = masked<MODE>(posB);
+    }
+    float e0 = fmaf(cfr[0], sl0, -mb0), e1 = fmaf(cfr[1], sl1, -mb1);
+    float e2 = fmaf(cfr[2], sl0, -mb0), e3 = fmaf(cfr[3], sl1, -mb1);
+    if (kPositions || !whole_tile) {
+      if (posA < 0) e0 = e1 = kNegInf;
+      if (posB < 0) e2 = e3 = kNegInf;
+    }
+    if (stores_logits(MODE)) {
+      const int atA = logit_pos(posA), atB = logit_pos(posB);
+      if (atA >= c.img_start && atA < c.img_start + c.n_img)
+        *reinterpret_cast<float2*>(logit_base + (size_t)(atA - c.img_start) * kSlots + 2 * tig) =
+            posA >= 0 ? make_float2(cfr[0] * sl0, cfr[1] * sl1) : make_float2(kNegInf, kNegInf);
+      if (atB >= c.img_start && atB < c.img_start + c.n_img)
+        *reinterpret_cast<float2*>(logit_base + (size_t)(atB - c.img_start) * kSlots + 2 * tig) =
+            posB >= 0 ? make_float2(cfr[2] * sl0, cfr[3] * sl1) : make_float2(kNegInf, kNegInf);
+    }
+    if (__any_sync(0xffffffffu, fmaxf(fmaxf(e0, e1), fmaxf(e2, e3)) > kLimit)) {
+      const float s0 = posA >= 0 ? cfr[0] * sl0 : kNegInf, s1 = posA >= 0 ? cfr[1] * sl1 : kNegInf;
+      const float s2 = posB >= 0 ? cfr[2] * sl0 : kNegInf, s3 = posB >= 0 ? cfr[3] * sl1 : kNegInf;
+      const float mn0 = fmaxf(mb0, warp_max_gid(fmaxf(s0, s2)) - kHeadroom);
+      const float mn1 = fmaxf(mb1, warp_max_gid(fmaxf(s1, s3)) - kHeadroom);
+      const float al0 = fast_exp2(mb0 - mn0), al1 = fast_exp2(mb1 - mn1);
+      mb0 = mn0;
+      mb1 = mn1;
+      sm_.l[0] *= al0;
+      sm_.l[1] *= al1;
+      if constexpr (MODE == kProfile) {
+        sm_.il[0] *= al0;
+        sm_.il[1] *= al1;
+      }
+#pragma unroll
+      for (int mt = 0; mt < D / 16; ++mt) {
+        sm_.acc[mt][0] *= al0;
+        sm_.acc[mt][1] *= al1;
+        sm_.acc[mt][2] *= al0;
+        sm_.acc[mt][3] *= al1;
+      }
+      e0 = s0 - mb0;
+      e1 = s1 - mb1;
+      e2 = s2 - mb0;
+      e3 = s3 - mb1;
+    }
+    const float p0 = fast_exp2(e0), p1 = fast_exp2(e1), p2 = fast_exp2(e2), p3 = fast_exp2(e3);
+    sm_.l[0] += p0 + p2;
+    sm_.l[1] += p1 + p3;
+    if constexpr (MODE == kProfile) {
+      const bool iA = posA >= c.img_start && posA < c.img_start + c.n_img;
+      const bool iB = posB >= c.img_start && posB < c.img_start + c.n_img;
+      sm_.il[0] += (iA ? p0 : 0.f) + (iB ? p2 : 0.f);
+      sm_.il[1] += (iA ? p1 : 0.f) + (iB ? p3 : 0.f);
+    }
+    bb0 = movmatrix_trans(pack_f16(p0, p1));
+    bb1 = movmatrix_trans(pack_f16(p2, p3));
+  };
+
+  // Tiles [0, my_tiles) of this warp, `first` of them staged already, through the pipeline,
+  // for a cache in 4 bits. Software pipelined like the deep variant below, in the order
+  // that hides most: the raw codes of the next tile's keys and of this tile's values are
+  // loaded first, this tile's probabilities (exponentials and a transposition to wait for)
+  // come before the next tile's first product, and its own second product last.
+  auto stream_fp4 = [&](int my_tiles, int first, int n_list, auto&& issue_tile) {
+    float cfr[4];
+    auto stage_of = [&](int it) { return smem_u32(pipe + (it % ST) * SM::kStageBytes); };
+    if (my_tiles > 0) {
+      cp_async_wait<ST - 2>();
+      __syncwarp();
+      key.load(stage_of(0), stage_of(0) + 2 * kTile * ROWB, lane);
+      keys_fp4(cfr);
+    }
+    for (int it = 0; it < my_tiles; ++it) {
+      const uint32_t here = stage_of(it), next = stage_of(it + 1);
+      const int jn = it + ST - 1;   // tiles below `first` were staged already
+      if (jn >= first && jn < my_tiles) issue_tile(jn);
+      cp_async_commit();
+      cp_async_wait<ST - 2>();
+      __syncwarp();
+      // past the last tile this reads a stage no copy is writing; unused
+      key.load(next, next + 2 * kTile * ROWB, lane);
+      value.load(here + kTile * ROWB, here + kTile * (2 * ROWB + SM::kScaleBytes), lane);
+      uint32_t bb0, bb1;
+      probabilities_fp4(cfr, it, n_list, bb0, bb1);
+      keys_fp4(cfr);
+      value.product(bb0, bb1, sm_.acc);
+      __syncwarp();
+    }
+  };
+  if constexpr (kDirect) {
+    const int n_tiles = (n_cta + kTile - 1) / kTile;
+    const int my_tiles = n_tiles > warp ? (n_tiles - warp + kWarps - 1) / kWarps : 0;
+    int pos, page;   // of the next tile to copy
+#pragma unroll 1
+    for (int j = pre_issued; j < ST - 1; ++j) {
+      if (j < my_tiles) {
+        look_up(j, n_cta, pos, page);
+        issue_fp4(j, row_at(pos, page));
+      }
+      cp_async_commit();
+    }
+    look_up(max(pre_issued, ST - 1), n_cta, pos, page);
+    stream_fp4(my_tiles, pre_issued, n_cta, [&](int jn) {
+      const int row = row_at(pos, page);
+      look_up(jn + 1, n_cta, pos, page);
+      issue_fp4(jn, row);
+    });
+  }
+
   // ---------------- stream the work list in rounds of kSliceMax entries
-  for (int rb = 0; rb < n_cta; rb += kSliceMax) {
+  for (int rb = 0; rb < (kDirect ? 0 : n_cta); rb += kSliceMax) {
     const int n_round = min(n_cta - rb, kSliceMax);
     int first = 0;            // tiles of this warp already staged for this round
     if (rb > 0) {
@@ -1022,7 +1227,9 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
       if (j < my_tiles) issue(j, n_round);
       cp_async_commit();
     }
-    if constexpr (kMma && ST >= 4) {
+    if constexpr (kFp4) {
+      stream_fp4(my_tiles, first, n_round, [&](int jn) { issue(jn, n_round); });
+    } else if constexpr (kMma && ST >= 4) {
       // Software pipelined (deep variant): the next tile's QK^T is issued
       // before this tile's softmax and PV, keeping ST-2 tiles in flight.
       // Tile j of this warp sits in stage j % ST and in commit group j, or
@@ -1217,6 +1424,10 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
   if constexpr (kMma) {
     const float l0 = warp_sum_gid(sm_.l[0]), l1 = warp_sum_gid(sm_.l[1]);
     const int h0 = warp * kSlots + 2 * tig, h1 = h0 + 1;
+    if constexpr (kFp4) {   // no score at all: as the other types have it
+      sm_.m[0] = mb0 == kUnset ? kNegInf : mb0;
+      sm_.m[1] = mb1 == kUnset ? kNegInf : mb1;
+    }
     if (gid == 0) {
       wm[h0] = sm_.m[0];
       wm[h1] = sm_.m[1];

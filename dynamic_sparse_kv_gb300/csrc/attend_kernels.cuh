@@ -351,7 +351,7 @@ __device__ __forceinline__ AttendList make_list(const Params& p, int b, int& bad
 
 // Work-list entries resolved to cache rows per round: a multiple of the CTA
 // size (every thread resolves the same number).
-__host__ __device__ constexpr int slice_for(int v) { return v == kGeneral ? 960 : 1024; }
+__host__ __device__ constexpr int slice_for(int v) { return v == kGeneral ? 960 : (v == kPacked ? 2048 : 1024); }
 
 template <typename T, int D, int V = Held<T>::kGeneralVariant>
 struct Smem {
@@ -373,7 +373,9 @@ struct Smem {
   static constexpr int kRecvAccFloats = 4 * (kSlots * D / 4 + kMaxSplits);
   // the CTA's one reading of k before the wait (sparse), shared by its threads
   static constexpr int kSpecK = kRecvAcc + kRecvAccFloats * 4;
-  static constexpr int kQOffset = kSpecK + 16;                       // f32 path: q[8][D]
+  // 4 bits: which rows of each stage exist
+  static constexpr int kExist = kSpecK + 16;
+  static constexpr int kQOffset = kExist + (Held<T>::kFp4 ? kWarps * ST * 4 : 0);   // f32 path: q[8][D]
   static constexpr int kMainBytes = kQOffset + (Held<T>::kMma ? 0 : kSlots * D * 4);
 };
 

@@ -171,8 +171,8 @@ __global__ void __launch_bounds__(kThreads, Held<T>::kFp4 ? 3 : 2) write_kernel(
   const CacheRows& c = p.c;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   // One token a sequence: only row N_b - 1 is written, which an attention call reads
-  // after its own wait, so it may start now. (A grid that writes older rows is launched
-  // without this, and followed by launch_fence.)
+  // after its own wait, so it may start now. A grid that writes older rows lets it start
+  // with its own end only, and makes its writes visible to the device before.
   if (p.single) asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 
   const uint32_t f = blockIdx.x * blockDim.x + threadIdx.x;   // below 2^31 (checked on the host)
@@ -320,6 +320,10 @@ __global__ void __launch_bounds__(kThreads, Held<T>::kFp4 ? 3 : 2) write_kernel(
     }
   }
   if (bad) atomicOr(c.status, bad);
+  if (!p.single) {   // one fence a CTA: the barrier hands it the other threads' writes
+    __syncthreads();
+    if (threadIdx.x == 0) __threadfence();
+  }
 }
 
 // A CTA takes p.tile tokens, whose rows its first threads look up together (the lookups are
@@ -414,8 +418,6 @@ __global__ void __launch_bounds__(kThreads, 6) read_kernel(const ReadParams p) {
   }
 }
 
-__global__ void fence_kernel() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
-
 // With programmatic dependent launch: every kernel here begins with its wait.
 template <typename... P, typename... A>
 cudaError_t launch_early(void (*kernel)(P...), long threads, cudaStream_t s, const A&... args) {
@@ -440,8 +442,7 @@ int slots_for(int tokens, int lanes, int heads, int num_sms) {
 
 template <typename T, int D>
 cudaError_t write_rows(const WriteParams& p, cudaStream_t s) {
-  const cudaError_t e = launch_early(write_kernel<T, D>, (long)p.c.tokens * p.slots * (D / 16), s, p);
-  return e != cudaSuccess || p.single ? e : launch_fence(s);
+  return launch_early(write_kernel<T, D>, (long)p.c.tokens * p.slots * (D / 16), s, p);
 }
 
 template <typename T, int D>
@@ -452,10 +453,6 @@ cudaError_t read_rows(const ReadParams& p, cudaStream_t s) {
 }
 
 }  // namespace
-
-cudaError_t launch_fence(cudaStream_t s) {
-  return launch_early(fence_kernel, 1, s);
-}
 
 cudaError_t launch_write_rows(int dtype, int head_dim, int num_sms, WriteParams p, cudaStream_t s) {
   p.slots = slots_for(p.c.tokens, head_dim / 16, (p.q ? p.Hq : 0) + p.c.Hkv, num_sms);

@@ -50,8 +50,5 @@ struct ReadParams {
 // dtype: FASTOCR_DTYPE_*; head_dim 64 or 128
 cudaError_t launch_write_rows(int dtype, int head_dim, int num_sms, WriteParams p, cudaStream_t s);
 cudaError_t launch_read_rows(int dtype, int head_dim, int num_sms, ReadParams p, cudaStream_t s);
-// An empty kernel that ends once everything before it on the stream is complete: the kernel
-// behind it may read, before its own wait, whatever was written before.
-cudaError_t launch_fence(cudaStream_t s);
 
 }  // namespace fastocr

@@ -91,94 +91,102 @@ __device__ __forceinline__ float fp4_query(const __nv_bfloat16* q, bool have, ui
   return __uint_as_float(e << 23);
 }
 
-// Partial S^T of a tile: K codes at shared address kA, their scales at sA.
-template <int D, int CHAINS>
-__device__ __forceinline__ void fp4_keys(uint32_t kA, uint32_t sA, int lane, const uint32_t (&qf)[D / 16][2],
-                                         float (&cc)[CHAINS][4]) {
-  const int gid = lane >> 2, tig = lane & 3;
-  const int r0 = fp4_key(gid);
-  constexpr int W = D / 32;   // 32-bit words of codes a row gives a lane
-  uint32_t w0[W], w1[W], s0[2], s1[2];
-  if constexpr (D == 128) {
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n"
-                 : "=r"(w0[0]), "=r"(w0[1]), "=r"(w0[2]), "=r"(w0[3]) : "r"(kA + fp4_place<D>(r0, tig)));
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n"
-                 : "=r"(w1[0]), "=r"(w1[1]), "=r"(w1[2]), "=r"(w1[3]) : "r"(kA + fp4_place<D>(r0 + 8, tig)));
-    uint16_t a, b;   // groups 2 tig and 2 tig + 1
-    asm volatile("ld.shared.u16 %0, [%1];\n" : "=h"(a) : "r"(sA + r0 * 8 + 2 * tig));
-    asm volatile("ld.shared.u16 %0, [%1];\n" : "=h"(b) : "r"(sA + (r0 + 8) * 8 + 2 * tig));
-    const uint32_t x = e4m3_pair(a), y = e4m3_pair(b);
-    s0[0] = __byte_perm(x, x, 0x1010);
-    s0[1] = __byte_perm(x, x, 0x3232);
-    s1[0] = __byte_perm(y, y, 0x1010);
-    s1[1] = __byte_perm(y, y, 0x3232);
-  } else {
-    const uint32_t half = (tig & 1) * 8;
-    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];\n"
-                 : "=r"(w0[0]), "=r"(w0[1]) : "r"(kA + fp4_place<D>(r0, tig >> 1) + half));
-    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];\n"
-                 : "=r"(w1[0]), "=r"(w1[1]) : "r"(kA + fp4_place<D>(r0 + 8, tig >> 1) + half));
-    uint16_t a, b;   // group tig
-    asm volatile("{\n .reg .b8 t;\n ld.shared.u8 t, [%1];\n cvt.u16.u8 %0, t;\n}\n" : "=h"(a) : "r"(sA + r0 * 4 + tig));
-    asm volatile("{\n .reg .b8 t;\n ld.shared.u8 t, [%1];\n cvt.u16.u8 %0, t;\n}\n" : "=h"(b) : "r"(sA + (r0 + 8) * 4 + tig));
-    s0[0] = s0[1] = e4m3_pair(a | (a << 8));
-    s1[0] = s1[1] = e4m3_pair(b | (b << 8));
-  }
-#pragma unroll
-  for (int i = 0; i < W; ++i) {
-    uint32_t h0[4], h1[4];
-    fp4_decode8(w0[i], h0);
-    fp4_decode8(w1[i], h1);
-    const int g = D == 128 ? i >> 1 : 0;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int ks = 2 * i + j;
-      const uint32_t a[4] = {mul_f16x2(h0[2 * j], s0[g]), mul_f16x2(h1[2 * j], s1[g]),
-                             mul_f16x2(h0[2 * j + 1], s0[g]), mul_f16x2(h1[2 * j + 1], s1[g])};
-      mma_f16(cc[ks % CHAINS], a, qf[ks][0], qf[ks][1]);
+// A lane's share of a tile's K as it lies: codes of rows fp4_key(gid) and 8 further, their
+// scales (two groups each at d = 128, one at 64). Loading and using are apart so that the
+// loads' latency passes under other work.
+template <int D>
+struct Fp4Keys {
+  static constexpr int W = D / 32;
+  uint32_t w0[W], w1[W];
+  uint32_t a, b;   // scales of either row
+
+  __device__ __forceinline__ void load(uint32_t kA, uint32_t sA, int lane) {
+    const int gid = lane >> 2, tig = lane & 3;
+    const int r0 = fp4_key(gid);
+    if constexpr (D == 128) {
+      asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n"
+                   : "=r"(w0[0]), "=r"(w0[1]), "=r"(w0[2]), "=r"(w0[3]) : "r"(kA + fp4_place<D>(r0, tig)));
+      asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n"
+                   : "=r"(w1[0]), "=r"(w1[1]), "=r"(w1[2]), "=r"(w1[3]) : "r"(kA + fp4_place<D>(r0 + 8, tig)));
+      asm volatile("ld.shared.u16 %0, [%1];\n" : "=r"(a) : "r"(sA + r0 * 8 + 2 * tig));
+      asm volatile("ld.shared.u16 %0, [%1];\n" : "=r"(b) : "r"(sA + (r0 + 8) * 8 + 2 * tig));
+    } else {
+      const uint32_t half = (tig & 1) * 8;
+      asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];\n"
+                   : "=r"(w0[0]), "=r"(w0[1]) : "r"(kA + fp4_place<D>(r0, tig >> 1) + half));
+      asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];\n"
+                   : "=r"(w1[0]), "=r"(w1[1]) : "r"(kA + fp4_place<D>(r0 + 8, tig >> 1) + half));
+      asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(a) : "r"(sA + r0 * 4 + tig));
+      asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(b) : "r"(sA + (r0 + 8) * 4 + tig));
     }
   }
-}
+  // S^T = K Q^T in CHAINS independent accumulations
+  template <int CHAINS>
+  __device__ __forceinline__ void product(const uint32_t (&qf)[D / 16][2], float (&cc)[CHAINS][4]) const {
+    const uint32_t x = e4m3_pair(a), y = e4m3_pair(b);
+    const uint32_t s0[2] = {__byte_perm(x, x, 0x1010), __byte_perm(x, x, 0x3232)};
+    const uint32_t s1[2] = {__byte_perm(y, y, 0x1010), __byte_perm(y, y, 0x3232)};
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      uint32_t h0[4], h1[4];
+      fp4_decode8(w0[i], h0);
+      fp4_decode8(w1[i], h1);
+      const int g = D == 128 ? i >> 1 : 0;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int ks = 2 * i + j;
+        const uint32_t f[4] = {mul_f16x2(h0[2 * j], s0[g]), mul_f16x2(h1[2 * j], s1[g]),
+                               mul_f16x2(h0[2 * j + 1], s0[g]), mul_f16x2(h1[2 * j + 1], s1[g])};
+        mma_f16(cc[ks % CHAINS], f, qf[ks][0], qf[ks][1]);
+      }
+    }
+  }
+};
 
-// O^T += V^T P^T of a tile: V codes at shared address vA, their scales at sA, the
-// probabilities' fragments in b0 (keys 2t, 2t + 1 of fp4_key's order) and b1 (8 further).
-// acc[mt]: dims D/8 gid + 2 mt (elements 0, 1) and the one after it (2, 3).
+// The same of V: codes of dims D/8 gid .. of keys tig, tig + 4, tig + 8, tig + 12, and their
+// scales.
 template <int D>
-__device__ __forceinline__ void fp4_values(uint32_t vA, uint32_t sA, int lane, uint32_t b0, uint32_t b1,
-                                           float (&acc)[D / 16][4]) {
-  const int gid = lane >> 2, tig = lane & 3;
-  constexpr int W = D / 64;   // words a key gives a lane: D / 8 codes
+struct Fp4Values {
+  static constexpr int W = D / 64;
   uint32_t w[4][W];
   uint32_t s[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int r = tig + 4 * j;
-    if constexpr (D == 128) {
-      asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];\n"
-                   : "=r"(w[j][0]), "=r"(w[j][1]) : "r"(vA + fp4_place<D>(r, gid >> 1) + (gid & 1) * 8));
-      asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(s[j]) : "r"(sA + r * 8 + gid));
-    } else {
-      asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(w[j][0]) : "r"(vA + fp4_place<D>(r, gid >> 2) + (gid & 3) * 4));
-      asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(s[j]) : "r"(sA + r * 4 + (gid >> 1)));
-    }
-  }
-  const uint32_t s01 = e4m3_pair(s[0] | (s[1] << 8)), s23 = e4m3_pair(s[2] | (s[3] << 8));
-#pragma unroll
-  for (int i = 0; i < W; ++i) {
-    // codes of the same dim of two keys side by side: even dims, then odd ones
-    constexpr uint32_t M = 0x0f0f0f0fu;
-    uint32_t e01[4], o01[4], e23[4], o23[4];
-    fp4_decode8((w[0][i] & M) | ((w[1][i] << 4) & ~M), e01);
-    fp4_decode8(((w[0][i] >> 4) & M) | (w[1][i] & ~M), o01);
-    fp4_decode8((w[2][i] & M) | ((w[3][i] << 4) & ~M), e23);
-    fp4_decode8(((w[2][i] >> 4) & M) | (w[3][i] & ~M), o23);
+
+  __device__ __forceinline__ void load(uint32_t vA, uint32_t sA, int lane) {
+    const int gid = lane >> 2, tig = lane & 3;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint32_t a[4] = {mul_f16x2(e01[j], s01), mul_f16x2(o01[j], s01), mul_f16x2(e23[j], s23),
-                             mul_f16x2(o23[j], s23)};
-      mma_f16(acc[4 * i + j], a, b0, b1);
+      const int r = tig + 4 * j;
+      if constexpr (D == 128) {
+        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];\n"
+                     : "=r"(w[j][0]), "=r"(w[j][1]) : "r"(vA + fp4_place<D>(r, gid >> 1) + (gid & 1) * 8));
+        asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(s[j]) : "r"(sA + r * 8 + gid));
+      } else {
+        asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(w[j][0]) : "r"(vA + fp4_place<D>(r, gid >> 2) + (gid & 3) * 4));
+        asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(s[j]) : "r"(sA + r * 4 + (gid >> 1)));
+      }
     }
   }
-}
+  // O^T += V^T P^T, the probabilities' fragments in b0 (keys 2t, 2t + 1 of fp4_key's order) and
+  // b1 (8 further). acc[mt]: dims D/8 gid + 2 mt (elements 0, 1) and the one after it (2, 3).
+  __device__ __forceinline__ void product(uint32_t b0, uint32_t b1, float (&acc)[D / 16][4]) const {
+    const uint32_t s01 = e4m3_pair(s[0] | (s[1] << 8)), s23 = e4m3_pair(s[2] | (s[3] << 8));
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      // codes of the same dim of two keys side by side: even dims, then odd ones
+      constexpr uint32_t M = 0x0f0f0f0fu;
+      uint32_t e01[4], o01[4], e23[4], o23[4];
+      fp4_decode8((w[0][i] & M) | ((w[1][i] << 4) & ~M), e01);
+      fp4_decode8(((w[0][i] >> 4) & M) | (w[1][i] & ~M), o01);
+      fp4_decode8((w[2][i] & M) | ((w[3][i] << 4) & ~M), e23);
+      fp4_decode8(((w[2][i] >> 4) & M) | (w[3][i] & ~M), o23);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t a[4] = {mul_f16x2(e01[j], s01), mul_f16x2(o01[j], s01), mul_f16x2(e23[j], s23),
+                               mul_f16x2(o23[j], s23)};
+        mma_f16(acc[4 * i + j], a, b0, b1);
+      }
+    }
+  }
+};
 
 }  // namespace fastocr

@@ -12,7 +12,6 @@
 #include <algorithm>
 
 #include "attend_kernels.cuh"
-#include "cache_rows.cuh"
 #include "pages.cuh"
 
 namespace fastocr {
@@ -25,6 +24,10 @@ constexpr int kPass = kPlan * kPer;
 constexpr int kPiece = 4096;         // bytes a warp copies at once
 
 __device__ __forceinline__ void pool_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+// The last kernel of a call lets its dependents start with its end only, and every thread
+// makes its writes visible to the device before: a kernel behind it may read the table, the
+// lengths and the rows before its own wait, as the attention kernels do.
+__device__ __forceinline__ void pool_publish() { __threadfence(); }
 __device__ __forceinline__ void pool_release_dependents() {
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 }
@@ -83,16 +86,18 @@ __device__ __forceinline__ int scan_warps(int x, int* s_warp, int& total) {
   return before;
 }
 
-// The references of one pass, 32 * kPer consecutive ones a warp: bit `lane` of free[i] is
-// whether page base + 32 i + lane exists and is free.
-__device__ __forceinline__ int free_masks(const PoolParams& p, long base, uint32_t free[kPer]) {
-  const int lane = threadIdx.x & 31;
-  int r[kPer], n = 0;
+// The references of one pass, 32 * kPer consecutive ones a warp; pages that do not exist
+// are in use.
+__device__ __forceinline__ void load_refs(const PoolParams& p, long base, int r[kPer]) {
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    const long page = base + 32 * i + lane;
+    const long page = base + 32 * i + (threadIdx.x & 31);
     r[i] = page < p.num_pages ? __ldcg(p.refs + page) : 1;
   }
+}
+// Bit `lane` of free[i]: whether page base + 32 i + lane is free. Returns how many are.
+__device__ __forceinline__ int free_masks(const int r[kPer], uint32_t free[kPer]) {
+  int n = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     free[i] = __ballot_sync(0xffffffffu, r[i] <= 0);
@@ -126,68 +131,104 @@ __device__ __forceinline__ Want want_of(const PoolParams& p, const int32_t* rows
 // move to a fresh page, the one being the first of them where every holder is here, and
 // none where somebody else keeps the page. A page that holds rows below the length is
 // copied. Fresh pages go out in order of sequence and column.
+//
+// The time of a steady call (a token more in every sequence, few pages or none) is that of
+// its dependent lookups, so each is made once: a warp keeps what it finds out about its
+// first sequence (all there are up to 32) in registers, the first pass over the references
+// is loaded before anything is known of the sequences, and counts and fresh pages pass
+// through shared memory while they fit (kPlan).
 __global__ void __launch_bounds__(kPlan) reserve_kernel(const PoolParams p, const int32_t* rows, int extra,
                                                         int32_t* missing) {
-  __shared__ int s_warp[32];
-  __shared__ int s_bad;
+  __shared__ int s_warp[32], s_count[kPlan], s_list[kPlan], s_old[kPlan];
+  __shared__ int s_bad, s_moves;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int bad = 0;
-  if (tid == 0) s_bad = 0;
+  if (tid == 0) s_bad = s_moves = 0;
   pool_wait();
   pool_release_dependents();   // the copy kernel waits for this grid
+  const long mine0 = (long)warp * 32 * kPer;
+  int refs0[kPer];
+  load_refs(p, mine0, refs0);
+
+  // column c of sequence b: the page it has and how many entries name that (none: 0)
+  struct Entry {
+    int page, refs;
+  };
+  auto look = [&](const Want& w, int b, int c) -> Entry {
+    Entry e = {-1, 0};
+    if (c < min(w.need, w.held)) {
+      const int page = __ldcg(p.table + (size_t)b * p.max_pages + c);
+      if (page >= 0 && page < p.num_pages)
+        e = {page, __ldcg(p.refs + page)};
+      else
+        bad |= kDevBadPage;
+    }
+    return e;
+  };
+  Want w0 = {0, 0, 0, 0};
+  Entry e0 = {-1, 0};
+  if (warp < p.B) {
+    w0 = want_of(p, rows, extra, warp, bad);
+    e0 = look(w0, warp, w0.first + lane);
+  }
+  // f(want, sequence, first column of 32, this lane's entry, whether it is the sequence's last 32)
+  auto each = [&](auto&& f) {
+    for (int b = warp; b < p.B; b += kWarps) {
+      const Want w = b == warp ? w0 : want_of(p, rows, extra, b, bad);
+      int c0 = w.first;
+      do {   // once at least
+        f(w, b, c0, b == warp && c0 == w.first ? e0 : look(w, b, c0 + lane), c0 + 32 >= w.need);
+        c0 += 32;
+      } while (c0 < w.need);
+    }
+  };
   // how many wanted columns refer to a shared page, and the first of them; only the
   // entries of pages looked at are cleared
-  auto each_shared = [&](auto&& f) {
-    for (int b = warp; b < p.B; b += kWarps) {
-      int ignored = 0;
-      const Want w = want_of(p, rows, extra, b, ignored);
-      const int32_t* row = p.table + (size_t)b * p.max_pages;
-      for (int c = w.first + lane; c < min(w.need, w.held); c += 32) {
-        const int page = __ldcg(row + c);
-        if (page >= 0 && page < p.num_pages && __ldcg(p.refs + page) > 1) f(page, b * p.max_pages + c);
+  bool shared = false;
+  each([&](const Want&, int, int, Entry e, bool) {
+    if (e.refs > 1) {
+      shared = true;
+      __stcg(p.want + e.page, 0);
+      __stcg(p.lead + e.page, 0x7fffffff);
+    }
+  });
+  if (__syncthreads_or(shared)) {
+    each([&](const Want&, int b, int c0, Entry e, bool) {
+      if (e.refs > 1) {
+        atomicAdd(p.want + e.page, 1);
+        atomicMin(p.lead + e.page, b * p.max_pages + c0 + lane);
       }
-    }
-  };
-  each_shared([&](int page, int) {
-    __stcg(p.want + page, 0);
-    __stcg(p.lead + page, 0x7fffffff);
-  });
-  __syncthreads();
-  each_shared([&](int page, int at) {
-    atomicAdd(p.want + page, 1);
-    atomicMin(p.lead + page, at);
-  });
-  __syncthreads();
-  // whether column c of sequence b gets a fresh page; old: the page it gives up, or -1
-  auto fresh = [&](const Want& w, int b, int c, int& old, int& bad) -> bool {
-    old = -1;
+    });
+    __syncthreads();
+  }
+  // whether column c of sequence b gets a fresh page
+  auto fresh = [&](const Want& w, int b, int c, Entry e) -> bool {
     if (c >= w.need) return false;
-    if (c >= w.held) return true;
-    const int page = __ldcg(p.table + (size_t)b * p.max_pages + c);
-    if (page < 0 || page >= p.num_pages) {
-      bad |= kDevBadPage;
-      return true;
-    }
-    const int refs = __ldcg(p.refs + page);
-    if (refs <= 1 || (__ldcg(p.want + page) == refs && __ldcg(p.lead + page) == b * p.max_pages + c)) return false;
-    old = page;
-    return true;
+    if (e.page < 0) return true;   // none, or one that is nowhere
+    if (e.refs <= 1) return false;
+    return !(__ldcg(p.want + e.page) == e.refs && __ldcg(p.lead + e.page) == b * p.max_pages + c);
   };
-  for (int b = warp; b < p.B; b += kWarps) {
-    const Want w = want_of(p, rows, extra, b, bad);
+  const bool few = p.B <= kPlan;
+  {
     int n = 0;
-    for (int c0 = w.first; c0 < w.need; c0 += 32) {
-      int old;
-      n += __popc(__ballot_sync(0xffffffffu, fresh(w, b, c0 + lane, old, bad)));
-    }
-    if (lane == 0) __stcg(p.count + b, n);
+    each([&](const Want& w, int b, int c0, Entry e, bool last) {
+      n += __popc(__ballot_sync(0xffffffffu, fresh(w, b, c0 + lane, e)));
+      if (!last) return;
+      if (lane == 0) {
+        if (few)
+          s_count[b] = n;
+        else
+          __stcg(p.count + b, n);
+      }
+      n = 0;
+    });
   }
   __syncthreads();
   // counts -> first indices, kPlan sequences a pass
   int total = 0;
   for (int b0 = 0; b0 < p.B; b0 += kPlan) {
     const int b = b0 + tid;
-    const int n = b < p.B ? __ldcg(p.count + b) : 0;
+    const int n = b >= p.B ? 0 : few ? s_count[b] : __ldcg(p.count + b);
     int incl = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -196,21 +237,33 @@ __global__ void __launch_bounds__(kPlan) reserve_kernel(const PoolParams p, cons
     }
     int sum;
     const int before = scan_warps(__shfl_sync(0xffffffffu, incl, 31), s_warp, sum);
-    if (b < p.B) __stcg(p.count + b, total + before + incl - n);
+    if (b < p.B) {
+      if (few)
+        s_count[b] = total + before + incl - n;
+      else
+        __stcg(p.count + b, total + before + incl - n);
+    }
     total += sum;
   }
   // the lowest `total` free pages
+  const bool small = total <= kPlan;
   int found = 0;
   for (long base = 0; base < p.num_pages && found < total; base += kPass) {
     uint32_t free[kPer];
-    const long mine = base + (long)warp * 32 * kPer;
-    const int n = free_masks(p, mine, free);
+    const long mine = base + mine0;
+    if (base > 0) load_refs(p, mine, refs0);
+    const int n = free_masks(refs0, free);
     int sum;
     int at = found + scan_warps(n, s_warp, sum);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int r = at + __popc(free[i] & ((1u << lane) - 1));
-      if ((free[i] >> lane & 1) && r < total) __stcg(p.list + r, (int)(mine + 32 * i + lane));
+      if ((free[i] >> lane & 1) && r < total) {
+        if (small)
+          s_list[r] = (int)(mine + 32 * i + lane);
+        else
+          __stcg(p.list + r, (int)(mine + 32 * i + lane));
+      }
       at += __popc(free[i]);
     }
     found += sum;
@@ -218,48 +271,46 @@ __global__ void __launch_bounds__(kPlan) reserve_kernel(const PoolParams p, cons
   if (bad) atomicOr(&s_bad, bad);
   __syncthreads();
   const int lacking = max(0, total - found);
+  if (lacking == 0) {   // all or nothing
+    // Hand them out; the references change once every sequence has looked at them.
+    int at = 0;
+    each([&](const Want& w, int b, int c0, Entry e, bool last) {
+      if (c0 == w.first) at = few ? s_count[b] : __ldcg(p.count + b);
+      const int c = c0 + lane;
+      const bool take = fresh(w, b, c, e);
+      const uint32_t mask = __ballot_sync(0xffffffffu, take);
+      if (take) {
+        const int r = at + __popc(mask & ((1u << lane) - 1));
+        const int page = small ? s_list[r] : __ldcg(p.list + r);
+        if (small)
+          s_old[r] = e.page;
+        else
+          __stcg(p.old + r, e.page);
+        __stcg(p.table + (size_t)b * p.max_pages + c, page);
+        if (e.page >= 0 && ((long)c << p.log2_page) < w.len) {   // the page that row `len` is in
+          const int m = atomicAdd(&s_moves, 1);                  // B moves at most, in any order
+          __stcg(p.src + m, e.page);
+          __stcg(p.dst + m, page);
+        }
+      }
+      at += __popc(mask);
+      if (last && lane == 0 && w.need > w.held) __stcg(p.held + b, w.need);
+    });
+    __syncthreads();
+    for (int r = tid; r < total; r += kPlan) {
+      __stcg(p.refs + (small ? s_list[r] : __ldcg(p.list + r)), 1);
+      const int old = small ? s_old[r] : __ldcg(p.old + r);
+      if (old >= 0) drop_ref(p, old, bad);
+    }
+    if (bad) atomicOr(&s_bad, bad);
+    __syncthreads();
+  }
   if (tid == 0) {
-    __stcg(p.head, lacking ? 0 : p.B);
+    __stcg(p.head, s_moves);
     __stcg(p.head + 1, 0);
     if (missing) __stcg(missing, lacking);
     if (s_bad || lacking) atomicOr(p.status, s_bad | (lacking ? kDevNoPages : 0));
   }
-  if (lacking) return;   // all or nothing
-  // Hand them out; the references change once every sequence has looked at them.
-  for (int b = warp; b < p.B; b += kWarps) {
-    int ignored = 0;
-    const Want w = want_of(p, rows, extra, b, ignored);
-    int at = __ldcg(p.count + b);
-    int32_t* row = p.table + (size_t)b * p.max_pages;
-    if (lane == 0) __stcg(p.src + b, -1);
-    __syncwarp();
-    for (int c0 = w.first; c0 < w.need; c0 += 32) {
-      const int c = c0 + lane;
-      int old;
-      const bool take = fresh(w, b, c, old, ignored);
-      const uint32_t mask = __ballot_sync(0xffffffffu, take);
-      if (take) {
-        const int r = at + __popc(mask & ((1u << lane) - 1));
-        const int page = __ldcg(p.list + r);
-        __stcg(p.old + r, old);
-        __stcg(row + c, page);
-        if (old >= 0 && ((long)c << p.log2_page) < w.len) {   // one column at most: that of row `len`
-          __stcg(p.src + b, old);
-          __stcg(p.dst + b, page);
-        }
-      }
-      at += __popc(mask);
-    }
-    if (lane == 0 && w.need > w.held) __stcg(p.held + b, w.need);
-  }
-  __syncthreads();
-  int late = 0;
-  for (int r = tid; r < total; r += kPlan) {
-    __stcg(p.refs + __ldcg(p.list + r), 1);
-    const int old = __ldcg(p.old + r);
-    if (old >= 0) drop_ref(p, old, late);
-  }
-  if (late) atomicOr(p.status, late);
 }
 
 // Fork: sequence dst[i] gets the pages of src[i] that hold rows, and its length. A pair out
@@ -267,7 +318,6 @@ __global__ void __launch_bounds__(kPlan) reserve_kernel(const PoolParams p, cons
 // other side of any pair is reported and left out.
 __global__ void __launch_bounds__(256) fork_kernel(const PoolParams p, const int32_t* src, const int32_t* dst, int n) {
   pool_wait();
-  pool_release_dependents();
   const int i = blockIdx.x, tid = threadIdx.x;
   const int from = __ldcg(src + i), to = __ldcg(dst + i);
   int bad = 0;
@@ -300,13 +350,13 @@ __global__ void __launch_bounds__(256) fork_kernel(const PoolParams p, const int
     __stcg(p.seq_len + to, len);
   }
   if (bad) atomicOr(p.status, bad);
+  pool_publish();
 }
 
 // Release: the pages of sequences seqs[i] (NULL: none of them, but of every sequence the
 // pages behind its rows). A sequence named twice is released once.
 __global__ void __launch_bounds__(256) release_kernel(const PoolParams p, const int32_t* seqs) {
   pool_wait();
-  pool_release_dependents();
   const int i = blockIdx.x, tid = threadIdx.x;
   int bad = 0;
   const int b = seqs ? __ldcg(seqs + i) : i;
@@ -328,6 +378,7 @@ __global__ void __launch_bounds__(256) release_kernel(const PoolParams p, const 
     if (seqs) __stcg(p.seq_len + b, 0);
   }
   if (bad) atomicOr(p.status, bad);
+  pool_publish();
 }
 
 // Compact: with U pages in use, the i-th used page at or behind U moves into the i-th free
@@ -339,12 +390,13 @@ __global__ void __launch_bounds__(kPlan) compact_kernel(const PoolParams p, int3
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pool_wait();
   pool_release_dependents();
+  int refs[kPer];
   int free_all = 0;
   for (long base = 0; base < p.num_pages; base += kPass) {
     uint32_t free[kPer];
-    const int n = free_masks(p, base + (long)warp * 32 * kPer, free);
+    load_refs(p, base + (long)warp * 32 * kPer, refs);
     int sum;
-    scan_warps(n, s_warp, sum);
+    scan_warps(free_masks(refs, free), s_warp, sum);
     free_all += sum;
   }
   const int border = p.num_pages - free_all;
@@ -352,7 +404,8 @@ __global__ void __launch_bounds__(kPlan) compact_kernel(const PoolParams p, int3
   for (long base = 0; base < p.num_pages; base += kPass) {
     uint32_t free[kPer];
     const long mine = base + (long)warp * 32 * kPer;
-    const int n = free_masks(p, mine, free);
+    if (p.num_pages > kPass) load_refs(p, mine, refs);   // one pass: still in registers
+    const int n = free_masks(refs, free);
     int sum;
     int at = before + scan_warps(n, s_warp, sum);
 #pragma unroll
@@ -427,9 +480,8 @@ __global__ void __launch_bounds__(256) copy_kernel(const PoolParams p, const int
   for (long it = me; it < items; it += warps) {
     const int m = (int)(it / per_move);
     const int from = __ldcg(src + first + m);
-    if (from < 0) continue;   // a sequence whose page stays
     const int to = __ldcg(dst + m);
-    if (from >= p.num_pages || to < 0 || to >= p.num_pages) {
+    if (from < 0 || from >= p.num_pages || to < 0 || to >= p.num_pages) {
       bad |= kDevBadPage;
       continue;
     }
@@ -471,6 +523,7 @@ __global__ void __launch_bounds__(256) copy_kernel(const PoolParams p, const int
     }
   }
   if (bad) atomicOr(p.status, bad);
+  pool_publish();
 }
 
 template <typename... P, typename... A>
@@ -487,11 +540,12 @@ cudaError_t launch_pool(void (*kernel)(P...), long grid, int block, cudaStream_t
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// CTAs of the copy kernel for up to n moves: pieces enough for a warp each, 8 CTAs an SM at most.
-long copy_grid(const PoolParams& p, long n) {
+// CTAs of the copy kernel for up to n moves: a piece for every warp, and `most` CTAs an SM at
+// most (two for reserve, whose steady calls move nothing: the launch of more costs them time).
+long copy_grid(const PoolParams& p, long n, long most) {
   long pieces = 0;
   for (int a = 0; a < p.arrays; ++a) pieces += (p.chunk[a] + kPiece - 1) / kPiece;
-  return std::max(1L, std::min(8L * p.num_sms, (n * pieces * p.layers + 7) / 8));
+  return std::max(1L, std::min(most * p.num_sms, (n * pieces * p.layers + 7) / 8));
 }
 
 }  // namespace
@@ -520,35 +574,31 @@ void place_pool_workspace(PoolParams& p, void* ws) {
 
 cudaError_t launch_reserve(const PoolParams& p, const int32_t* rows, int extra, int32_t* missing, cudaStream_t s) {
   cudaError_t e = launch_pool(reserve_kernel, 1, kPlan, s, p, rows, extra, missing);
-  if (e == cudaSuccess) e = launch_pool(copy_kernel, copy_grid(p, p.B), 256, s, p, p.src, p.dst, -1, 0);
-  return e == cudaSuccess ? launch_fence(s) : e;
+  if (e == cudaSuccess) e = launch_pool(copy_kernel, copy_grid(p, p.B, 2), 256, s, p, p.src, p.dst, -1, 0);
+  return e;
 }
 
 cudaError_t launch_fork(const PoolParams& p, const int32_t* src, const int32_t* dst, int n, cudaStream_t s) {
-  const cudaError_t e = launch_pool(fork_kernel, n, 256, s, p, src, dst, n);
-  return e == cudaSuccess ? launch_fence(s) : e;
+  return launch_pool(fork_kernel, n, 256, s, p, src, dst, n);
 }
 
 cudaError_t launch_release(const PoolParams& p, const int32_t* seqs, int n, cudaStream_t s) {
-  const cudaError_t e = launch_pool(release_kernel, n, 256, s, p, seqs);
-  return e == cudaSuccess ? launch_fence(s) : e;
+  return launch_pool(release_kernel, n, 256, s, p, seqs);
 }
 
 cudaError_t launch_trim(const PoolParams& p, cudaStream_t s) {
-  const cudaError_t e = launch_pool(release_kernel, p.B, 256, s, p, (const int32_t*)nullptr);
-  return e == cudaSuccess ? launch_fence(s) : e;
+  return launch_pool(release_kernel, p.B, 256, s, p, (const int32_t*)nullptr);
 }
 
 cudaError_t launch_compact(const PoolParams& p, int32_t* used, cudaStream_t s) {
   cudaError_t e = launch_pool(compact_kernel, 1, kPlan, s, p, used);
   if (e == cudaSuccess)
-    e = launch_pool(copy_kernel, copy_grid(p, std::max(p.num_pages / 2, p.B)), 256, s, p, p.src, p.list, -1, 1);
-  return e == cudaSuccess ? launch_fence(s) : e;
+    e = launch_pool(copy_kernel, copy_grid(p, std::max(p.num_pages / 2, p.B), 8), 256, s, p, p.src, p.list, -1, 1);
+  return e;
 }
 
 cudaError_t launch_copy_pages(const PoolParams& p, const int32_t* src, const int32_t* dst, int n, cudaStream_t s) {
-  const cudaError_t e = launch_pool(copy_kernel, copy_grid(p, n), 256, s, p, src, dst, n, 0);
-  return e == cudaSuccess ? launch_fence(s) : e;
+  return launch_pool(copy_kernel, copy_grid(p, n, 8), 256, s, p, src, dst, n, 0);
 }
 
 }  // namespace fastocr

@@ -17,7 +17,7 @@ struct PoolParams {
   int32_t* status;
   // workspace
   int32_t* head;       // [0] moves; compact: [1] index of the first source, [2] border
-  int32_t* src;        // pages to move, negative: none
+  int32_t* src;        // pages to move
   int32_t* dst;
   int32_t *list, *old, *want, *lead;   // [num_pages]
   int32_t* count;      // [B]
@@ -34,8 +34,8 @@ struct PoolParams {
 int64_t pool_workspace(int64_t pages, int64_t batch);
 void place_pool_workspace(PoolParams& p, void* ws);   // p.B and p.num_pages are set
 
-// Each ends with launch_fence: what follows may read the table, the lengths and the
-// cache before its own wait.
+// What follows may read the table, the lengths and the cache before its own wait (see
+// pool_publish).
 cudaError_t launch_reserve(const PoolParams& p, const int32_t* rows, int extra, int32_t* missing, cudaStream_t s);
 cudaError_t launch_fork(const PoolParams& p, const int32_t* src, const int32_t* dst, int n, cudaStream_t s);
 cudaError_t launch_release(const PoolParams& p, const int32_t* seqs, int n, cudaStream_t s);

@@ -440,7 +440,8 @@ fastocr_status fastocr_cross_attend(fastocr_handle* h, const void* q, const fast
  * fastocr_kv has them const.
  * Overlap: everything is read after the preceding kernel completes. With start NULL only
  * rows N_b - 1 are written, as the attention calls expect of the kernel before them; with
- * start a second, empty kernel follows, so that any call may come next.
+ * start the next kernel on the stream starts when this one has ended, so any call may come
+ * next. One kernel.
  * tokens * (H_q + 2 H_kv) * d < 2^33. Errors: NULL, INVALID (strides, rotary, tokens !=
  * B without start, another device current), UNSUPPORTED (rotary_dim), ALIGN, CUDA. */
 fastocr_status fastocr_write_rows(fastocr_handle* h, const fastocr_kv* kv, const fastocr_tokens* tokens,
@@ -458,8 +459,8 @@ fastocr_status fastocr_read_rows(fastocr_handle* h, const fastocr_kv* kv, const 
 /* Pages of a pool. Sequences hold pages of one pool, a page may be in several tables, and
  * refs counts how often. The calls keep table, lengths, pages held and references in step;
  * free pages go out lowest first, so the result is the same on every run. All of it happens
- * on the device, in order on `stream`; an empty kernel ends each call, so that any call may
- * follow. Calls on one pool must be ordered. State that does not fit (a page out of range, a
+ * on the device, in order on `stream`; the next kernel on it starts when a call's last has
+ * ended, so that any call may follow. Calls on one pool must be ordered. State that does not fit (a page out of range, a
  * reference too few) is reported as FASTOCR_DEV_BAD_PAGE or _BAD_POOL, and that entry left
  * out. Errors of all: NULL, INVALID (sizes, ws_bytes, another device current),
  * UNSUPPORTED (more than 2^31 rows or table entries), ALIGN, CUDA. */
@@ -473,7 +474,7 @@ int64_t fastocr_pool_workspace(const fastocr_handle* h, int64_t num_pages);
  * rows in it -- except the first of the sequences that want it, where every holder does.
  * seq_len stays. All or nothing: with too few free pages nothing changes and
  * FASTOCR_DEV_NO_PAGES is set. missing (device, may be NULL): how many too few. rows above
- * the capacity are clamped (FASTOCR_DEV_BAD_SEQLEN). Three kernels. */
+ * the capacity are clamped (FASTOCR_DEV_BAD_SEQLEN). Two kernels. */
 fastocr_status fastocr_pool_reserve(fastocr_handle* h, const fastocr_pool* pool, const int32_t* rows, int32_t extra,
                                     int32_t* missing, fastocr_stream stream);
 
@@ -481,28 +482,28 @@ fastocr_status fastocr_pool_reserve(fastocr_handle* h, const fastocr_pool* pool,
  * then shared (no rows move: fastocr_pool_reserve copies what one of them is about to
  * write); what dst[i] held is released. A pair out of range, a dst named again, and a
  * sequence that is both a src and a dst of different pairs are reported as
- * FASTOCR_DEV_BAD_GROUP and the pair left out. 0 <= n <= B. Two kernels. */
+ * FASTOCR_DEV_BAD_GROUP and the pair left out. 0 <= n <= B. One kernel. */
 fastocr_status fastocr_pool_fork(fastocr_handle* h, const fastocr_pool* pool, const int32_t* src, const int32_t* dst,
                                  int32_t n, fastocr_stream stream);
 
 /* Sequences seqs[i] (i < n; device) give up their pages and have no rows; one named twice
- * does so once. 0 <= n <= B. Two kernels. */
+ * does so once. 0 <= n <= B. One kernel. */
 fastocr_status fastocr_pool_release(fastocr_handle* h, const fastocr_pool* pool, const int32_t* seqs, int32_t n,
                                     fastocr_stream stream);
 
 /* Every sequence gives up the pages behind its rows (after an eviction, or when it was set
- * back). Two kernels. */
+ * back). One kernel. */
 fastocr_status fastocr_pool_trim(fastocr_handle* h, const fastocr_pool* pool, fastocr_stream stream);
 
 /* With U pages in use, the i-th page in use at or behind U moves, in every layer, into the
  * i-th free page before it, and the tables name it so: pages [U, num_pages) are then free.
- * used (device, may be NULL) = U. Three kernels. */
+ * used (device, may be NULL) = U. Two kernels. */
 fastocr_status fastocr_pool_compact(fastocr_handle* h, const fastocr_pool* pool, int32_t* used, fastocr_stream stream);
 
 /* Page src[i] is copied to dst[i] (i < n; device) in every layer; the tables stay. A pair
  * out of range is reported as FASTOCR_DEV_BAD_PAGE. No page may be dst of two pairs, or
  * src of one and dst of another (its rows are then unspecified). 0 <= n <= num_pages.
- * Two kernels. */
+ * One kernel. */
 fastocr_status fastocr_pool_copy(fastocr_handle* h, const fastocr_pool* pool, const int32_t* src, const int32_t* dst,
                                  int32_t n, fastocr_stream stream);
 
