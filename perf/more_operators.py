@@ -324,6 +324,8 @@ def _prepare_attend4(s, gen):
             cache.scales.copy_(s[x][1])
             caches.append(cache)
         kw = dict(rswa_prefix=c["prefix"], rswa_window=c["window"]) if c["kind"] == "rswa" else {}
+        if c["kind"] == "gather":
+            kw = dict(img_range=s["img"], max_img=c["image"])
         s["dec"] = DecodeAttention(*caches, s["table"], q_heads=hq, **kw)
         s["dec"].set_seq_len(max(_plan(c)[1]))
         s["dec"].set_seq_len(s["n"])
