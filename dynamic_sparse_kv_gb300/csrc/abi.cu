@@ -83,6 +83,8 @@ fastocr_status fastocr_create(const fastocr_dims* dims, fastocr_handle** out) {
     h->active[c] = d.dtype == FASTOCR_DTYPE_BF16 ? active_clusters_bf16(d.head_dim, c)
                    : d.dtype == FASTOCR_DTYPE_FP4 ? active_clusters_fp4(d.head_dim, c)
                                                   : active_clusters_f32(d.head_dim, c);
+  if (d.dtype == FASTOCR_DTYPE_FP4)
+    for (int c = 1; c <= h->max_splits; ++c) h->spread[c] = spread_clusters_fp4(d.head_dim, c);
   h->ws_bytes = off;
   if (cudaMalloc(&h->ws, off) != cudaSuccess) {
     free(h);

@@ -1079,16 +1079,18 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
   float mb0 = kUnset, mb1 = kUnset;
   Fp4Keys<D> key;        // of the next tile
   Fp4Values<D> value;    // of this one
-  auto keys_fp4 = [&](float cfr[4]) {
-    float cc[2][4];
+  float cc[2][4];   // S^T of the next tile in two accumulations, added where they are needed:
+                    // an addition here would hold the warp until the last product is done
+  auto keys_fp4 = [&]() {
 #pragma unroll
     for (int e = 0; e < 4; ++e) cc[0][e] = cc[1][e] = 0.f;
     key.product(sm_.qf, cc);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) cfr[e] = cc[0][e] + cc[1][e];
   };
   // P^T of the tile as B fragments
-  auto probabilities_fp4 = [&](const float cfr[4], int it, int n_list, uint32_t& bb0, uint32_t& bb1) {
+  auto probabilities_fp4 = [&](int it, int n_list, uint32_t& bb0, uint32_t& bb1) {
+    float cfr[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) cfr[e] = cc[0][e] + cc[1][e];
     constexpr bool kPositions = stores_logits(MODE) || MODE == kProfile;
     const bool whole_tile = whole >> (it % ST) & 1u;
     // positions of rows gid and gid + 8 of the fragments, negative for a masked one (the modes
@@ -1164,13 +1166,12 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
   // loaded first, this tile's probabilities (exponentials and a transposition to wait for)
   // come before the next tile's first product, and its own second product last.
   auto stream_fp4 = [&](int my_tiles, int first, int n_list, auto&& issue_tile) {
-    float cfr[4];
     auto stage_of = [&](int it) { return smem_u32(pipe + (it % ST) * SM::kStageBytes); };
     if (my_tiles > 0) {
       cp_async_wait<ST - 2>();
       __syncwarp();
       key.load(stage_of(0), stage_of(0) + 2 * kTile * ROWB, lane);
-      keys_fp4(cfr);
+      keys_fp4();
     }
     for (int it = 0; it < my_tiles; ++it) {
       const uint32_t here = stage_of(it), next = stage_of(it + 1);
@@ -1183,8 +1184,8 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
       key.load(next, next + 2 * kTile * ROWB, lane);
       value.load(here + kTile * ROWB, here + kTile * (2 * ROWB + SM::kScaleBytes), lane);
       uint32_t bb0, bb1;
-      probabilities_fp4(cfr, it, n_list, bb0, bb1);
-      keys_fp4(cfr);
+      probabilities_fp4(it, n_list, bb0, bb1);
+      keys_fp4();
       value.product(bb0, bb1, sm_.acc);
       __syncwarp();
     }
@@ -1832,7 +1833,8 @@ cudaError_t prepare_attend(Kern k, int bytes) {
 
 template <typename T, int D, int V>
 cudaError_t prepare_modes() {
-  const int bytes = attend_smem_bytes<T, D, V>();
+  // 4 bits: a limit, which spread_clusters_fp4's occupancy question needs at its highest
+  const int bytes = Held<T>::kFp4 ? 227 * 1024 : attend_smem_bytes<T, D, V>();
   cudaError_t e;
   if ((e = prepare_attend(attend_kernel<T, D, kFull, V>, bytes))) return e;
   if ((e = prepare_attend(attend_kernel<T, D, kFocal, V>, bytes))) return e;
@@ -1864,11 +1866,11 @@ cudaError_t prepare_all_modes() {
 // How many clusters of `c` CTAs of the general variant the device holds at
 // once (0 if a cluster of that size cannot be scheduled).
 template <typename T, int D>
-int active_clusters(int c) {
+int active_clusters(int c, int smem = attend_smem_bytes<T, D>()) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(c, 1, 1);
   cfg.blockDim = dim3(32 * warps_for(Held<T>::kGeneralVariant), 1, 1);
-  cfg.dynamicSmemBytes = attend_smem_bytes<T, D>();
+  cfg.dynamicSmemBytes = smem;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = c;

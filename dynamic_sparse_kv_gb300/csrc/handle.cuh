@@ -24,6 +24,7 @@ int max_cluster_fp4(int head_dim, int variant);
 int active_clusters_bf16(int head_dim, int cluster);
 int active_clusters_f32(int head_dim, int cluster);
 int active_clusters_fp4(int head_dim, int cluster);
+int spread_clusters_fp4(int head_dim, int cluster);
 }  // namespace fastocr
 
 struct fastocr_handle {
@@ -36,6 +37,7 @@ struct fastocr_handle {
   int max_splits;   // largest thread-block cluster the device co-schedules (<= 16)
   int max_splits_v[fastocr::kNumVariants];   // same per variant (0: the variant does not exist)
   int active[fastocr::kMaxSplits + 1];   // clusters of each size the device holds at once
+  int spread[fastocr::kMaxSplits + 1];   // 4 bits: clusters at one CTA an SM
   long len_hint;    // caller's N_t of the coming calls (0: unknown), split choice only
   void* ws;
   size_t ws_bytes;
@@ -68,7 +70,9 @@ inline void plan_launch(const fastocr_handle* h, int mode, long len, Params& p) 
   if (len < 1) len = 1;
   int v = h->variant_override[slot] - 1;   // -1: automatic
   int s = h->split_override[slot];         // 0: automatic
-  if (s == 0) s = choose_splits(units, len, h->max_splits, h->active, h->num_sms);
+  if (s == 0)
+    s = h->dims.dtype == FASTOCR_DTYPE_FP4 ? choose_splits_fp4(units, len, h->max_splits, h->active, h->spread)
+                                           : choose_splits(units, len, h->max_splits, h->active, h->num_sms);
   // grids that leave room for the next kernel's CTAs at one CTA per SM take
   // the deeper pipeline (more of each CTA's tiles staged before the wait)
   if (v < 0)

@@ -24,4 +24,10 @@ int active_clusters_fp4(int head_dim, int cluster) {
   return head_dim == 64 ? active_clusters<Fp4, 64>(cluster) : active_clusters<Fp4, 128>(cluster);
 }
 
+// the same with shared memory for one CTA an SM
+int spread_clusters_fp4(int head_dim, int cluster) {
+  constexpr int kMost = 227 * 1024;
+  return head_dim == 64 ? active_clusters<Fp4, 64>(cluster, kMost) : active_clusters<Fp4, 128>(cluster, kMost);
+}
+
 }  // namespace fastocr
