@@ -1122,7 +1122,7 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
   // true one, so that the probabilities use fp16's range: up to 2^(kLazyMax + kHeadroom),
   // and what is below 2^-24 is below 2^-31 of the largest. They are rounded to fp16
   // (2^-11 each, at random) for the product only; V's values are whole in fp16.
-  constexpr float kHeadroom = 7.f, kLimit = kLazyMax + kHeadroom, kUnset = -1e30f;
+  constexpr float kHeadroom = 7.f, kLimit = kLazyMax + kHeadroom, kUnset = -3e38f;
   float mb0 = kUnset, mb1 = kUnset;
   Fp4Keys<D> key;        // of the next tile
   Fp4Values<D> value;    // of this one

@@ -20,6 +20,9 @@ class PagePool:
     with dec's table and seq_len, if given. Otherwise the pool starts empty: every page
     free, every table entry -1, every length 0.
 
+    A sequence may be empty: attention gives it zeros (and reports DEV_BAD_SEQLEN for it).
+    Tokens go behind the length (write_layer) once reserve has given them their pages.
+
     Sequences are given as a list or a tensor; lists are checked on the host, int32 tensors
     on the device are checked there (dec.device_status). Calls are asynchronous on `stream`
     and have to be ordered among themselves and with what uses the table.

@@ -169,6 +169,42 @@ def test_pages_out_of_range_are_masked_and_reported():
     assert dec.device_status() == N.DEV_BAD_PAGE
 
 
+def test_a_cache_past_4_gib():
+    from dynamic_sparse_kv_gb300 import DecodeAttention, Fp4Cache
+    hq, hkv, d, page, pages = 8, 8, 128, 256, 33000
+    c = Fp4Paged([300], hkv, d, page, 23)
+    caches = [Fp4Cache(1, pages, hkv, page, d, device="cuda", gain=torch.from_numpy(g)[None]) for g in c.gain]
+    assert caches[0].codes.numel() > 2 ** 32
+    table = torch.tensor([[0, pages - 1]], dtype=torch.int32)
+    for w, x in enumerate(caches):
+        for i, at in enumerate(c.table[0].tolist()):
+            x.codes[0, table[0, i]].copy_(torch.from_numpy(c.codes[w][at]))
+            x.scales.view(torch.uint8)[0, table[0, i]].copy_(torch.from_numpy(c.scales[w][at]))
+    dec = DecodeAttention(*caches, table.cuda(), q_heads=hq)
+    q = queries(1, hq, d, 24)
+    out = torch.full_like(q, float("nan"))
+    idx, k = torch.tensor([[299, 3, 260, 17]], dtype=torch.int32, device="cuda"), torch.full((1,), 4, dtype=torch.int32, device="cuda")
+    img = torch.tensor([[0, 300]], dtype=torch.int32, device="cuda")
+    dec.set_seq_len(300)
+    dec.dense_step(q[None], out[None])
+    check(c, q, out)
+    from dynamic_sparse_kv_gb300 import fastocr_sparse_attend
+    fastocr_sparse_attend(dec.handle, q, dec.kv[0], img, idx, 4, k, out)
+    check(c, q, out, lambda b: idx[0].tolist())
+
+
+def test_logits_of_any_size():
+    """Logits far below any that a first running maximum could be taken for."""
+    hq, hkv, d = 4, 2, 64
+    c = Fp4Paged([40], hkv, d, 16, 25, kv=lambda b, w, m: torch.full((m, hkv, d), 2.0) if w == 0
+                 else torch.arange(m * hkv * d).view(m, hkv, d) % 7 - 3.0)
+    q = torch.full((1, hq, d), -2.0 ** 110).to(BF).cuda()      # every logit near -2^114: one value, no spread
+    out = torch.full_like(q, float("nan"))
+    c.decoder(hq).dense_step(q[None], out[None])
+    want = c.rows[0][1].mean(0).repeat(hq // hkv, 0)
+    assert np.abs(np64(out[0]) - want).max() <= (2.0 ** -8 + 2.0 ** -10) * 3
+
+
 def test_captured_steps_replay_on_other_lengths_and_codes():
     from dynamic_sparse_kv_gb300 import CapturedStep
     hq, hkv, d = 28, 4, 128

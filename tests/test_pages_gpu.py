@@ -223,3 +223,24 @@ def test_captured_and_replayed():
         assert t.m.reserve([n + 1 for n in t.m.len]) == 0
         t.m.len = [n + 1 for n in t.m.len]
     t.check()
+
+
+def test_pages_freed_by_an_eviction():
+    from dynamic_sparse_kv_gb300 import DecodeAttention, PagePool
+    g = torch.Generator().manual_seed(9)
+    k, v = (torch.randn(1, 40, 2, 16, 64, generator=g).to(BF).cuda() for _ in range(2))
+    dec = DecodeAttention(k, v, torch.zeros(3, 10, dtype=torch.int32, device="cuda"), q_heads=4)
+    pool = PagePool(dec)
+    rows = [150, 70, 33]
+    pool.reserve(rows)
+    dec.seq_len.copy_(torch.tensor(rows, dtype=torch.int32))
+    dec.track_weights(160, 10)
+    q = torch.randn(1, 3, 4, 64, generator=g).to(BF).cuda()
+    dec.weighed_step(q, torch.empty_like(q))
+    dec.evict_step(40, recent=8)
+    pool.trim()
+    assert dec.seq_len.tolist() == [50, 50, 33] and pool.held.tolist() == [4, 4, 3]
+    table = dec.block_table.cpu()
+    assert int((table >= 0).sum()) == 11 and int(pool.refs.sum()) == 11 and int(pool.refs.max()) == 1
+    pool.reserve(extra=40)
+    assert pool.held.tolist() == [6, 6, 5] and dec.device_status() == 0
