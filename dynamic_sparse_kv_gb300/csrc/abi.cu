@@ -6,6 +6,7 @@
 #include <algorithm>
 #include <vector>
 
+#include "cache_rows.cuh"
 #include "evict.cuh"
 #include "handle.cuh"
 #include "rows.cuh"
@@ -52,7 +53,7 @@ fastocr_status fastocr_create(const fastocr_dims* dims, fastocr_handle** out) {
   if (prop.major != 10 || prop.minor != 3) return FASTOCR_ERR_NO_DEVICE;
   if (prepare_bf16() != cudaSuccess || prepare_f32() != cudaSuccess || prepare_fp4() != cudaSuccess ||
       prepare_rows_f32() != cudaSuccess || prepare_rows_bf16() != cudaSuccess ||
-      prepare_evict() != cudaSuccess)
+      prepare_evict() != cudaSuccess || prepare_write_rows() != cudaSuccess)
     return FASTOCR_ERR_CUDA;
 
   const size_t units = (size_t)d.batch * d.num_kv_heads;

@@ -107,10 +107,15 @@ __device__ __forceinline__ void store8(char* at, const float x[8], const float*)
   reinterpret_cast<float4*>(at)[1] = make_float4(x[4], x[5], x[6], x[7]);
 }
 
-// a / b rounded to nearest, r = 1 / b rounded to nearest (Markstein: a quotient within an ulp
-// of a / b plus its remainder times r rounds correctly), where no product leaves the normal
-// range: b in [2^-30, 2^30], |a| below 2^60. A quotient below 2^-60 may be off by its last
-// bit, far below the smallest scale.
+// 1 / b and a / b, rounded to nearest, for b in [2^-30, 2^30] and |a| below 2^60, where no
+// product leaves the normal range (Markstein's theorems: a Newton step from an approximation
+// within an ulp, and a quotient's remainder times the reciprocal added to it). A quotient
+// below 2^-60 may be off by its last bit, far below the smallest scale.
+__device__ __forceinline__ float reciprocal(float b) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(b));
+  return __fmaf_rn(__fmaf_rn(-b, r, 1.f), r, r);
+}
 __device__ __forceinline__ float quotient(float a, float b, float r) {
   const float q = __fmul_rn(a, r);
   return __fmaf_rn(__fmaf_rn(-q, b, a), r, q);
@@ -119,45 +124,123 @@ __device__ __forceinline__ float quotient(float a, float b, float r) {
 // 8 dims of a group of 16 whose other 8 the neighbouring lane holds, as codes; *scale is
 // the group's. Every lane of the warp takes part.
 __device__ __forceinline__ uint32_t pack_codes(const float x[8], float gain, uint32_t* scale) {
-  float y[8], most = 0.f, poison = 0.f;   // poison: NaN if an element is not finite
+  float most = 0.f, poison = 0.f;   // poison: NaN if an element is not finite
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     most = fmaxf(most, fabsf(x[i]));
     poison = __fmaf_rn(x[i], 0.f, poison);
   }
-  if (most < 0x1p60f && gain >= 0x1p-30f && gain <= 0x1p30f) {
-    const float r = __frcp_rn(gain);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = quotient(x[i], gain, r);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(x[i], gain);
-  }
-  float top = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(y[i]));
-  top = poison == 0.f ? top : CUDART_INF_F;
-  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  most = poison == 0.f ? most : CUDART_INF_F;
+  most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+  // the quotients' largest is the largest's quotient: rounding keeps order
+  const bool plain = most < 0x1p30f && gain >= 0x1p-30f && gain <= 0x1p30f;
+  const float r = reciprocal(plain ? gain : 1.f);
+  const float top = plain ? quotient(most, gain, r) : __fdiv_rn(most, gain);
   uint32_t s;
   asm("{\n .reg .b16 t;\n cvt.rn.satfinite.e4m3x2.f32 t, 0f00000000, %1;\n cvt.u32.u16 %0, t;\n}\n"
       : "=r"(s)
-      : "f"(__fdiv_rn(top, 6.f)));
+      : "f"(plain ? quotient(top, 6.f, 1.f / 6.f) : __fdiv_rn(top, 6.f)));
   const float sf = unpack_f16(e4m3_pair(s)).x;
-  if (top < 0x1p60f) {
-    const float rs = __frcp_rn(sf);
+  float y[8];
+  if (plain) {   // the same for the group
+    const float rs = reciprocal(fmaxf(sf, 0x1p-9f));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = quotient(y[i], sf, rs);   // a scale of 0: any value, see below
+    for (int i = 0; i < 8; ++i) y[i] = quotient(quotient(x[i], gain, r), sf, rs);   // scale 0: see below
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(y[i], sf);
+    for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(__fdiv_rn(x[i], gain), sf);
   }
   uint32_t code;
   asm("{\n .reg .b8 a, b, c, d;\n cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
       " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n mov.b32 %0, {a, b, c, d};\n}\n"
       : "=r"(code)
       : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
-  *scale = top <= FLT_MAX ? s : 0x7fu;   // a NaN or an infinity makes the group NaN
-  return top <= FLT_MAX && sf > 0.f ? code : 0u;
+  const bool finite = top <= FLT_MAX;
+  *scale = finite ? s : 0x7fu;   // a NaN or an infinity makes the group NaN
+  return finite && s != 0 ? code : 0u;
+}
+
+// The dims of thread j of a head's D / 16: 8 from `lo` and 8 from `hi`, and whether they turn.
+template <int D>
+struct Dims {
+  int lo, hi;
+  bool turns;
+  __device__ __forceinline__ Dims(const WriteParams& p, int j) {
+    const int turning = p.rotary / 16;
+    turns = j < turning;
+    lo = turns ? 8 * j : p.rotary + 8 * (j - turning);
+    hi = lo + (turns ? p.rotary / 2 : (D - p.rotary) / 2);
+  }
+};
+
+// Cosines and sines of a token's pairs in those dims: rotate-halves takes dim lo + i with
+// hi + i (pair lo + i), the adjacent layout neighbouring dims (pairs lo / 2 .. and hi / 2 ..).
+struct Angles {
+  float co[8], si[8];
+  template <int D>
+  __device__ __forceinline__ void load(const WriteParams& p, const Dims<D>& d, int token, int& bad) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int pair = p.adjacent ? (i < 4 ? d.lo / 2 + i : d.hi / 2 + i - 4) : d.lo + i;
+      const int a = min(max((int)__ldg(p.axis + pair), 0), p.axes - 1);
+      int at = p.pos[(size_t)a * p.c.tokens + token];
+      if (at < 0 || at >= p.positions) {
+        bad |= kDevBadPosition;
+        at = at < 0 ? 0 : p.positions - 1;
+      }
+      const float2 cs = __ldg(reinterpret_cast<const float2*>(p.cos_sin) + (size_t)at * (p.rotary / 2) + pair);
+      co[i] = cs.x;
+      si[i] = cs.y;
+    }
+  }
+  __device__ __forceinline__ void turn(float x[8], float y[8], int adjacent) const {
+    if (adjacent) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float a0 = x[2 * i], a1 = x[2 * i + 1], b0 = y[2 * i], b1 = y[2 * i + 1];
+        x[2 * i] = __fsub_rn(__fmul_rn(a0, co[i]), __fmul_rn(a1, si[i]));
+        x[2 * i + 1] = __fadd_rn(__fmul_rn(a1, co[i]), __fmul_rn(a0, si[i]));
+        y[2 * i] = __fsub_rn(__fmul_rn(b0, co[4 + i]), __fmul_rn(b1, si[4 + i]));
+        y[2 * i + 1] = __fadd_rn(__fmul_rn(b1, co[4 + i]), __fmul_rn(b0, si[4 + i]));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float a = x[i], e = y[i];
+        x[i] = __fsub_rn(__fmul_rn(a, co[i]), __fmul_rn(e, si[i]));
+        y[i] = __fadd_rn(__fmul_rn(e, co[i]), __fmul_rn(a, si[i]));
+      }
+    }
+  }
+};
+
+// 8 + 8 dims of head i of the keys (which = 0) or values to their row; the warp's lanes all
+// take part, `on` or not.
+template <typename T, int D>
+__device__ __forceinline__ void put_row(const CacheRows& c, const Dims<D>& d, long row, int i, int which, bool on,
+                                        const float x[8], const float y[8]) {
+  using Q = typename Held<T>::Q;
+  constexpr int E = sizeof(Q);
+  const long at = row + ((long)i << c.log2_page);
+  if constexpr (Held<T>::kFp4) {
+    const float gain = on ? __ldg((which ? c.v_gain : c.k_gain) + i) : 1.f;
+    uint32_t sx, sy;
+    const uint32_t cx = pack_codes(x, gain, &sx), cy = pack_codes(y, gain, &sy);
+    if (on) {
+      char* codes = (which ? c.v : c.k) + at * (D / 2);
+      uint8_t* scales = (which ? c.v_scale : c.k_scale) + at * (D / 16);
+      *reinterpret_cast<uint32_t*>(codes + d.lo / 2) = cx;
+      *reinterpret_cast<uint32_t*>(codes + d.hi / 2) = cy;
+      if ((d.lo & 15) == 0) {
+        scales[d.lo / 16] = (uint8_t)sx;
+        scales[d.hi / 16] = (uint8_t)sy;
+      }
+    }
+  } else if (on) {
+    char* dst = (which ? c.v : c.k) + at * (D * E);
+    store8(dst + d.lo * E, x, static_cast<const Q*>(nullptr));
+    store8(dst + d.hi * E, y, static_cast<const Q*>(nullptr));
+  }
 }
 
 template <typename T, int D>
@@ -183,18 +266,13 @@ __global__ void __launch_bounds__(kThreads, Held<T>::kFp4 ? 3 : 2) write_kernel(
   int first = 0, end = 0, bad = 0;
   const int b = token < c.tokens ? sequence_of(c, token, first, end) : -1;
 
-  // this thread's dims: 8 from `lo`, 8 from `hi`
-  const int turning = p.rotary / 16;   // threads whose dims turn
-  const bool turns = j < turning;
-  const int rest = D - p.rotary;
-  const int lo = turns ? 8 * j : p.rotary + 8 * (j - turning);
-  const int hi = lo + (turns ? p.rotary / 2 : rest / 2);
+  const Dims<D> d(p, j);
 
   // Heads slot, slot + slots, ... of the queries, then of keys and values. The loads of the
   // first ones go out before the chain of lookups that their angles and rows hang on.
   const int Hq = p.q ? p.Hq : 0;
-  const char* q_lo = p.q + token * p.q_stride + lo * E;
-  const int to_hi = (hi - lo) * E;
+  const char* q_lo = p.q + token * p.q_stride + d.lo * E;
+  const int to_hi = (d.hi - d.lo) * E;
   Raw8<Q> x0[U], x1[U];
   auto load_q = [&](int h) {
 #pragma unroll
@@ -209,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, Held<T>::kFp4 ? 3 : 2) write_kernel(
   Raw8<Q> k0, k1, v0, v1;
   auto load_kv = [&](int i) {
     if (b >= 0 && i < c.Hkv) {
-      const long at = ((long)i * D + lo) * E;
+      const long at = ((long)i * D + d.lo) * E;
       k0.load(p.k + token * p.k_stride + at);
       k1.load(p.k + token * p.k_stride + at + to_hi);
       v0.load(p.v + token * p.v_stride + at);
@@ -222,47 +300,8 @@ __global__ void __launch_bounds__(kThreads, Held<T>::kFp4 ? 3 : 2) write_kernel(
   if (few) load_kv(kv_first);
 
   const long row = b >= 0 ? row_of(c, b, token, first, end, bad) : -1;
-  // the pairs: rotate-halves takes dim lo + i with hi + i (pair lo + i), the adjacent
-  // layout neighbouring dims (pairs lo / 2 .. and hi / 2 ..)
-  float co[8], si[8];
-  if (turns && b >= 0) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int pair = p.adjacent ? (i < 4 ? lo / 2 + i : hi / 2 + i - 4) : lo + i;
-      const int a = min(max((int)__ldg(p.axis + pair), 0), p.axes - 1);
-      int at = p.pos[(size_t)a * c.tokens + token];
-      if (at < 0 || at >= p.positions) {
-        bad |= kDevBadPosition;
-        at = at < 0 ? 0 : p.positions - 1;
-      }
-      const float2 cs = __ldg(reinterpret_cast<const float2*>(p.cos_sin) + (size_t)at * (p.rotary / 2) + pair);
-      co[i] = cs.x;
-      si[i] = cs.y;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) co[i] = 1.f, si[i] = 0.f;
-  }
-  auto turn = [&](float x[8], float y[8]) {
-    if (!turns) return;
-    if (p.adjacent) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float a0 = x[2 * i], a1 = x[2 * i + 1], b0 = y[2 * i], b1 = y[2 * i + 1];
-        x[2 * i] = __fsub_rn(__fmul_rn(a0, co[i]), __fmul_rn(a1, si[i]));
-        x[2 * i + 1] = __fadd_rn(__fmul_rn(a1, co[i]), __fmul_rn(a0, si[i]));
-        y[2 * i] = __fsub_rn(__fmul_rn(b0, co[4 + i]), __fmul_rn(b1, si[4 + i]));
-        y[2 * i + 1] = __fadd_rn(__fmul_rn(b1, co[4 + i]), __fmul_rn(b0, si[4 + i]));
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float a = x[i], e = y[i];
-        x[i] = __fsub_rn(__fmul_rn(a, co[i]), __fmul_rn(e, si[i]));
-        y[i] = __fadd_rn(__fmul_rn(e, co[i]), __fmul_rn(a, si[i]));
-      }
-    }
-  };
+  Angles angles;
+  if (d.turns && b >= 0) angles.load(p, d, token, bad);
 
   for (int h = slot; h < Hq; h += U * p.slots) {
     if (h != slot) load_q(h);
@@ -272,51 +311,31 @@ __global__ void __launch_bounds__(kThreads, Held<T>::kFp4 ? 3 : 2) write_kernel(
         float x[8], y[8];
         x0[u].get(x);
         x1[u].get(y);
-        turn(x, y);
-        char* dst = p.q_out + ((long)token * p.Hq + h + u * p.slots) * (D * E) + lo * E;
+        if (d.turns) angles.turn(x, y, p.adjacent);
+        char* dst = p.q_out + ((long)token * p.Hq + h + u * p.slots) * (D * E) + d.lo * E;
         store8(dst, x, static_cast<const Q*>(nullptr));
         store8(dst + to_hi, y, static_cast<const Q*>(nullptr));
       }
   }
 
-  const int page = 1 << c.log2_page;
 #pragma unroll 1
   for (int i0 = 0; i0 < c.Hkv; i0 += p.slots) {   // the same number of turns for every thread
     const int i = i0 + kv_first;
     const bool on = row >= 0 && i < c.Hkv;
     if (i0 > 0 || !few) load_kv(i);
-    const long at = row + (long)i * page;
+    if (!__any_sync(0xffffffffu, on)) continue;
 #pragma unroll
     for (int which = 0; which < 2; ++which) {   // keys, then values
       float x[8], y[8];
       if (on) {
         (which ? v0 : k0).get(x);
         (which ? v1 : k1).get(y);
-        if (!which) turn(x, y);
+        if (!which && d.turns) angles.turn(x, y, p.adjacent);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = y[e] = 0.f;
       }
-      if constexpr (Held<T>::kFp4) {
-        if (!__any_sync(0xffffffffu, on)) continue;   // the lanes of a group agree; the shuffles need all
-        const float gain = on ? __ldg((which ? c.v_gain : c.k_gain) + i) : 1.f;
-        uint32_t sx, sy;
-        const uint32_t cx = pack_codes(x, gain, &sx), cy = pack_codes(y, gain, &sy);
-        if (on) {
-          char* codes = (which ? c.v : c.k) + at * (D / 2);
-          uint8_t* scales = (which ? c.v_scale : c.k_scale) + at * (D / 16);
-          *reinterpret_cast<uint32_t*>(codes + lo / 2) = cx;
-          *reinterpret_cast<uint32_t*>(codes + hi / 2) = cy;
-          if ((lo & 15) == 0) {
-            scales[lo / 16] = (uint8_t)sx;
-            scales[hi / 16] = (uint8_t)sy;
-          }
-        }
-      } else if (on) {
-        char* dst = (which ? c.v : c.k) + at * (D * E) + lo * E;
-        store8(dst, x, static_cast<const Q*>(nullptr));
-        store8(dst + to_hi, y, static_cast<const Q*>(nullptr));
-      }
+      put_row<T, D>(c, d, row, i, which, on, x, y);
     }
   }
   if (bad) atomicOr(c.status, bad);
@@ -324,6 +343,153 @@ __global__ void __launch_bounds__(kThreads, Held<T>::kFp4 ? 3 : 2) write_kernel(
     __syncthreads();
     if (threadIdx.x == 0) __threadfence();
   }
+}
+
+// Many tokens: one CTA an SM, whose warps take tokens each and have the next ones' rows of the
+// projection under way into a ring of their own in shared memory (bulk copies; a token is
+// 9 KB at 28 + 2 x 4 heads of 128), so that no register waits for memory: 147 KB are in
+// flight an SM where the kernel above has 64. A warp takes 32 / (D / 16) heads at once.
+struct Ring {
+  int warps, slots, slot_bytes;   // 0 warps: it does not fit
+};
+constexpr int kRingTokens = 500, kRingSlot = 4096;   // fewer tokens or bytes a token: the other kernel
+constexpr int kRingPacked = 8192, kRingMany = 10000;  // 4 bits: bytes a token from so many tokens on
+constexpr int kRingBytes = 221 * 1024, kRingWarps = 16, kRingSlots = 6;
+
+__device__ __forceinline__ bool ring_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok;
+}
+// Waits for a phase, about two seconds at most; then (a library bug) `dead` is set, every later
+// wait gives up at once, and the call ends with an error status instead of hanging.
+__device__ __forceinline__ bool ring_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
+  if (ring_try(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!*dead) {
+    if (ring_try(bar, parity)) return true;
+    if (clock64() - t0 > 4000000000LL) *dead = 1;
+  }
+  return false;
+}
+__device__ __forceinline__ void ring_copy(uint32_t dst, const char* src, int bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(32 * kRingWarps, 1) write_stream_kernel(const WriteParams p, const Ring ring) {
+  using Q = typename Held<T>::Q;
+  constexpr int L = D / 16, H = 32 / L;   // lanes a head, heads a warp
+  constexpr int E = sizeof(Q), HB = D * E;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ __align__(8) unsigned long long s_bar[kRingWarps * kRingSlots];
+  __shared__ int s_dead;
+  const CacheRows& c = p.c;
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int Hq = p.q ? p.Hq : 0;
+  const int first_token = blockIdx.x * ring.warps + warp, step = gridDim.x * ring.warps;
+  const int n = first_token < c.tokens ? (c.tokens - first_token + step - 1) / step : 0;
+  const uint32_t bars = smem_u32(s_bar + warp * kRingSlots);
+  const unsigned char* mine = smem + (size_t)warp * ring.slots * ring.slot_bytes;
+  if (threadIdx.x == 0) s_dead = 0;
+  if (lane < ring.slots) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;\n" ::"r"(bars + lane * 8) : "memory");
+  asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  __syncthreads();
+  volatile int* dead = &s_dead;
+
+  // token i of this warp into its slot: queries, keys, values
+  auto load = [&](int i) {
+    const long token = first_token + (long)i * step;
+    const int slot = i % ring.slots;
+    const uint32_t bar = bars + slot * 8, dst = smem_u32(mine + slot * ring.slot_bytes);
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"((Hq + 2 * c.Hkv) * HB)
+                 : "memory");
+    if (Hq) ring_copy(dst, p.q + token * p.q_stride, Hq * HB, bar);
+    ring_copy(dst + Hq * HB, p.k + token * p.k_stride, c.Hkv * HB, bar);
+    ring_copy(dst + (Hq + c.Hkv) * HB, p.v + token * p.v_stride, c.Hkv * HB, bar);
+  };
+  if (lane == 0)
+    for (int i = 0; i < min(n, ring.slots); ++i) load(i);
+
+  const Dims<D> d(p, lane % L);
+  int bad = 0;
+  long rows = -2;   // of token 32 k + lane of this warp; -1: no row, -2: behind the last sequence
+  auto look_up = [&](int i) {
+    int first = 0, end = 0;
+    rows = -2;
+    if (i < n) {
+      const int token = first_token + i * step, b = sequence_of(c, token, first, end);
+      if (b >= 0) rows = row_of(c, b, token, first, end, bad);
+    }
+  };
+  look_up(lane);
+  Angles angles, next;
+  // a token behind the last sequence has no position to be wrong
+  auto load_angles = [&](int token) {
+    int ignored = 0;
+    next.load(p, d, token, token < c.start[c.B] ? bad : ignored);
+  };
+  if (d.turns && n > 0) load_angles(first_token);
+  for (int i = 0; i < n; ++i) {
+    if (i > 0 && (i & 31) == 0) look_up(i + lane);
+    const long row = __shfl_sync(0xffffffffu, rows, i & 31);
+    const int token = first_token + i * step, slot = i % ring.slots;
+    angles = next;
+    if (d.turns && i + 1 < n) load_angles(token + step);
+    if (!__all_sync(0xffffffffu, ring_wait(bars + slot * 8, (i / ring.slots) & 1, dead))) {
+      bad |= kDevInternal;
+      break;
+    }
+    const char* src = reinterpret_cast<const char*>(mine) + slot * ring.slot_bytes;
+    auto get = [&](const char* at, float x[8]) {
+      Raw8<Q> w;
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) w.w[e] = reinterpret_cast<const uint4*>(at)[e];
+      w.get(x);
+    };
+    if (row >= -1) {
+#pragma unroll 2
+      for (int h0 = 0; h0 < Hq; h0 += H) {
+        const int h = h0 + lane / L;
+        if (h < Hq) {
+          float x[8], y[8];
+          get(src + h * HB + d.lo * E, x);
+          get(src + h * HB + d.hi * E, y);
+          if (d.turns) angles.turn(x, y, p.adjacent);
+          char* dst = p.q_out + ((long)token * Hq + h) * HB;
+          store8(dst + d.lo * E, x, static_cast<const Q*>(nullptr));
+          store8(dst + d.hi * E, y, static_cast<const Q*>(nullptr));
+        }
+      }
+    }
+    if (row >= 0) {   // the same for the whole warp
+      for (int h0 = 0; h0 < c.Hkv; h0 += H) {
+        const int h = h0 + lane / L;
+        const bool on = h < c.Hkv;
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+          float x[8], y[8];
+          const char* at = src + (Hq + which * c.Hkv + (on ? h : 0)) * HB;
+          get(at + d.lo * E, x);
+          get(at + d.hi * E, y);
+          if (!which && d.turns) angles.turn(x, y, p.adjacent);
+          put_row<T, D>(c, d, row, h, which, on, x, y);
+        }
+      }
+    }
+    __syncwarp();   // every lane has read the slot
+    if (lane == 0 && i + ring.slots < n) load(i + ring.slots);
+  }
+  if (bad) atomicOr(c.status, bad);
+  __syncthreads();
+  if (threadIdx.x == 0) __threadfence();
 }
 
 // A CTA takes p.tile tokens, whose rows its first threads look up together (the lookups are
@@ -440,8 +606,40 @@ int slots_for(int tokens, int lanes, int heads, int num_sms) {
   return (int)(slots < 1 ? 1 : slots > heads ? heads : slots);
 }
 
+// Warps and slots of a ring kernel. In 4 bits packing bounds it, so it gets as many warps as
+// there are slots (33 280 tokens of 28 + 2 x 4 heads of 128: 16 warps of 1 slot 98 us, 12 of 2
+// 118, 8 of 3 142); otherwise two slots a warp (bf16: 106, 105, 107). The other kernel takes
+// 115 and 109 us for them, 28 and 23 us for 4000 tokens (17 and 15). It is faster for few
+// tokens (300: 7 us and 10, bf16 6 and 8), for small ones (2 KB each, 33 280 of them: 38 us
+// and 46) and, packing, for many of medium size (33 280 of 16 + 2 x 2 heads 69 us and 75; 4000
+// 20 and 14).
+Ring ring_for(const WriteParams& p, int row_bytes, bool fp4) {
+  Ring r = {0, 0, ((p.q ? p.Hq : 0) + 2 * p.c.Hkv) * row_bytes};
+  const int w = std::min(fp4 ? kRingWarps : 12, kRingBytes / ((fp4 ? 1 : 2) * r.slot_bytes));
+  if (p.single || w < 4 || p.c.tokens < kRingTokens || r.slot_bytes < kRingSlot) return r;
+  if (fp4 && r.slot_bytes < kRingPacked && p.c.tokens >= kRingMany) return r;
+  r.warps = w;
+  r.slots = std::min(kRingSlots, kRingBytes / (w * r.slot_bytes));
+  return r;
+}
+
 template <typename T, int D>
-cudaError_t write_rows(const WriteParams& p, cudaStream_t s) {
+cudaError_t write_rows(const WriteParams& p, int num_sms, cudaStream_t s) {
+  const Ring ring = ring_for(p, D * (int)sizeof(typename Held<T>::Q), Held<T>::kFp4);
+  if (ring.warps) {
+    const int smem = ring.warps * ring.slots * ring.slot_bytes;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(num_sms);
+    cfg.blockDim = dim3(32 * ring.warps);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, write_stream_kernel<T, D>, p, ring);
+  }
   return launch_early(write_kernel<T, D>, (long)p.c.tokens * p.slots * (D / 16), s, p);
 }
 
@@ -454,14 +652,28 @@ cudaError_t read_rows(const ReadParams& p, cudaStream_t s) {
 
 }  // namespace
 
+cudaError_t prepare_write_rows() {
+  cudaError_t e = cudaSuccess;
+  auto limit = [&](auto kernel) {
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+  };
+  limit(write_stream_kernel<__nv_bfloat16, 64>);
+  limit(write_stream_kernel<__nv_bfloat16, 128>);
+  limit(write_stream_kernel<float, 64>);
+  limit(write_stream_kernel<float, 128>);
+  limit(write_stream_kernel<Fp4, 64>);
+  limit(write_stream_kernel<Fp4, 128>);
+  return e;
+}
+
 cudaError_t launch_write_rows(int dtype, int head_dim, int num_sms, WriteParams p, cudaStream_t s) {
   p.slots = slots_for(p.c.tokens, head_dim / 16, (p.q ? p.Hq : 0) + p.c.Hkv, num_sms);
   switch (dtype) {
     case FASTOCR_DTYPE_BF16:
-      return head_dim == 64 ? write_rows<__nv_bfloat16, 64>(p, s) : write_rows<__nv_bfloat16, 128>(p, s);
-    case FASTOCR_DTYPE_F32: return head_dim == 64 ? write_rows<float, 64>(p, s) : write_rows<float, 128>(p, s);
+      return head_dim == 64 ? write_rows<__nv_bfloat16, 64>(p, num_sms, s) : write_rows<__nv_bfloat16, 128>(p, num_sms, s);
+    case FASTOCR_DTYPE_F32: return head_dim == 64 ? write_rows<float, 64>(p, num_sms, s) : write_rows<float, 128>(p, num_sms, s);
   }
-  return head_dim == 64 ? write_rows<Fp4, 64>(p, s) : write_rows<Fp4, 128>(p, s);
+  return head_dim == 64 ? write_rows<Fp4, 64>(p, num_sms, s) : write_rows<Fp4, 128>(p, num_sms, s);
 }
 
 cudaError_t launch_read_rows(int dtype, int head_dim, int num_sms, ReadParams p, cudaStream_t s) {

@@ -47,6 +47,7 @@ struct ReadParams {
   int tile, share;         // tokens a CTA takes; groups of lanes that split a token's heads
 };
 
+cudaError_t prepare_write_rows();   // once per device, outside any capture
 // dtype: FASTOCR_DTYPE_*; head_dim 64 or 128
 cudaError_t launch_write_rows(int dtype, int head_dim, int num_sms, WriteParams p, cudaStream_t s);
 cudaError_t launch_read_rows(int dtype, int head_dim, int num_sms, ReadParams p, cudaStream_t s);

@@ -59,7 +59,7 @@ class Case:
         i = 0
         for b, (t, n) in enumerate(zip(self.tokens, self.rows)):
             for r in range(n - t, n):
-                yield i, int(self.table[b, r // self.page]), r % self.page
+                yield i, int(self.table[b, max(r, 0) // self.page]), r % self.page
                 i += 1
 
     def check(self, before, k, v, skip=()):
@@ -145,6 +145,58 @@ def test_write_and_read(kind, heads, adjacent, page, tokens, rows, single):
             assert torch.equal(back[w][:c.t].cpu() + 0.0, want.to(dt) + 0.0)
             assert bool((back[w][c.t:] == 3.0).all())      # rows behind the last sequence
     assert c.dec.device_status() == 0
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("heads,tokens,adjacent", [((28, 4, 128), [700, 0, 333, 1], False), ((28, 4, 128), [499, 1], True),
+                                                   ((20, 20, 64), [801], False), ((10, 10, 128), [5000, 3], True),
+                                                   ((64, 8, 128), [600, 40], False), ((16, 16, 128), [5000], False)])
+def test_many_tokens(kind, heads, tokens, adjacent):
+    """Prompts, some of whose rows no sequence has: the last 8 tokens are behind the last sequence."""
+    from dynamic_sparse_kv_gb300 import Rotary
+    c = Case(kind, heads, 16, tokens, [t + 5 for t in tokens], 11)
+    wide = torch.cat([c.qkv, c.qkv[:8]])
+    c.t += 8
+    a, b = c.hq * c.d, (c.hq + c.hkv) * c.d
+    q, k, v = (x.unflatten(1, (-1, c.d)) for x in (wide[:, :a], wide[:, a:b], wide[:, b:b + c.hkv * c.d]))
+    rot = Rotary(c.d, (c.d // 8, 3 * c.d // 8), positions=6000, adjacent=adjacent, device="cuda")
+    cos, sin = (rot.cos_sin[..., i].cpu().numpy() for i in range(2))
+    pos = c.positions(2, 6000)
+    pos[:, -8:] = 10 ** 6                   # nobody's
+    before = c.before()
+    out_q = torch.full((c.t, c.hq, c.d), 5.0, dtype=c.dt, device="cuda")
+    c.dec.write_layer(0, k, v, q=q, out_q=out_q, rotary=rot, pos=pos.cuda(), q_start=c.start)
+    axis = [0] * (c.d // 8) + [1] * (3 * c.d // 8)
+    n = c.t - 8
+    turn = lambda x: rotate(f32(x[:n]), pos.numpy()[:, :n], axis, cos, sin, adjacent)
+    assert torch.equal(out_q[:n].cpu(), torch.from_numpy(turn(q)).to(c.dt)) and bool((out_q[n:] == 5.0).all())
+    c.check(before, turn(k), f32(v[:n]))
+    # and in place
+    same = q.contiguous()
+    c.dec.write_layer(0, k, v, q=same, out_q=same, rotary=rot, pos=pos.cuda(), q_start=c.start)
+    assert torch.equal(same[:n], out_q[:n]) and torch.equal(same[n:], q[n:])
+    assert c.dec.device_status() == 0
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_many_tokens_without_rows_are_reported(kind):
+    from dynamic_sparse_kv_gb300 import Rotary
+    from dynamic_sparse_kv_gb300 import _native as N
+    c = Case(kind, (28, 4, 128), 16, [600, 300], [600, 300], 12)
+    rot = Rotary(128, (64,), positions=100, device="cuda")
+    cos, sin = (rot.cos_sin[..., i].cpu().numpy() for i in range(2))
+    pos = c.positions(1, 100)
+    pos[0, 64] = -1
+    c.dec.seq_len[0] = 590                  # ten tokens have no row
+    c.dec.block_table[1, 3] = -1            # nor have rows 48 .. 63 of sequence 1
+    before = c.before()
+    c.rows[0] = 590
+    out_q = torch.empty(c.t, c.hq, c.d, dtype=c.dt, device="cuda")
+    c.dec.write_layer(0, c.k, c.v, q=c.q, out_q=out_q, rotary=rot, pos=pos.cuda(), q_start=c.start)
+    assert c.dec.device_status() == N.DEV_BAD_GROUP | N.DEV_BAD_PAGE | N.DEV_BAD_POSITION
+    turn = lambda x: rotate(f32(x), pos.numpy(), [0] * 64, cos, sin, False)
+    assert torch.equal(out_q.cpu(), torch.from_numpy(turn(c.q)).to(c.dt))
+    c.check(before, turn(c.k), f32(c.v), skip=[*range(10), *range(648, 664)])
 
 
 @pytest.mark.parametrize("kind", KINDS)
