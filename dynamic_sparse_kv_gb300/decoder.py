@@ -101,6 +101,22 @@ class _Weights(dict):
     """What track_weights made; a dict that can be held weakly."""
 
 
+class _Layers:
+    """x[l] of a tensor x [L, ...] as the address that the library takes: a step's calls each
+    made two views of a layer otherwise, 3 us apiece next to a launch of 3.5."""
+    __slots__ = ("at", "step")
+
+    def __init__(self, x):
+        self.at, self.step = x.data_ptr(), x.stride(0) * x.element_size()
+
+    def __getitem__(self, l):
+        return self.at + l * self.step
+
+
+def _layers(x):
+    return _Layers(x) if isinstance(x, torch.Tensor) else x
+
+
 class DecodeAttention:
     """Decode attention of a stack of layers over a paged KV cache.
 
@@ -288,6 +304,7 @@ class DecodeAttention:
         kernel a layer, no logits, scores or top-k), and finish_warmup(q=...)
         then selects on the deepest chosen layer alone; select=True also keeps
         every layer's selection, for finish_warmup to take F_last from."""
+        q, out = _layers(q), _layers(out)
         for l in range(self.layers):
             if hook:
                 hook(l, True)
@@ -427,6 +444,7 @@ class DecodeAttention:
         flags (per-kind timing). hook(l, before): called on the host right
         before and right after layer l's calls are issued (CapturedStep uses
         it to order per-layer host copies against the layers)."""
+        q, out = _layers(q), _layers(out)
         cur = self.sel[max(self.focal)] if self.has_f_last else None
         flags = 0   # first layer: stage F_last early, check it after the wait
         for l in range(self.layers):
@@ -453,6 +471,7 @@ class DecodeAttention:
             self.has_f_last = True
 
     def dense_step(self, q, out, stream=None, hook=None):
+        q, out = _layers(q), _layers(out)
         for l in range(self.layers):
             if hook:
                 hook(l, True)
@@ -461,6 +480,7 @@ class DecodeAttention:
                 hook(l, False)
 
     def rswa_step(self, q, out, stream=None, hook=None):
+        q, out = _layers(q), _layers(out)
         for l in range(self.layers):
             if hook:
                 hook(l, True)
