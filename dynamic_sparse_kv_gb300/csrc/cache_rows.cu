@@ -30,7 +30,7 @@ constexpr int kPerSm = 2048;
 constexpr int kReadTile = 8;   // tokens a CTA reads at most
 
 // What many threads look up at the same address (offsets, lengths, gains) is loaded through
-// L1: past it, one L2 slice would answer every warp of the grid in turn (reading 27 820
+// L1: past it, one L2 slice would answer every warp of the grid in turn (reading 32 250
 // tokens from 4 bits back as fp32 took 62 us that way, 33 with it).
 //
 // Sequence of a packed token (the last that starts at or before it), or -1: none has it.
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, Held<T>::kFp4 ? 3 : 2) write_kernel(
   using Q = typename Held<T>::Q;
   constexpr int L = D / 16;   // threads a head
   constexpr int E = sizeof(Q);
-  // Query heads in flight. 27 820 tokens: bf16 100 us with 4 (a third CTA an SM and 2: 102),
+  // Query heads in flight. 32 250 tokens: bf16 100 us with 4 (a third CTA an SM and 2: 102),
   // 4 bits, whose packing wants warps more, 108 with 2 and three CTAs (4 and two: 112).
   constexpr int U = Held<T>::kFp4 ? 2 : 8 / E;
   const CacheRows& c = p.c;
