@@ -16,7 +16,8 @@ class PagePool:
     """Who holds the pages of dec's caches.
 
     held [B] and refs [num_pages] int32, on the caches' device: how many leading entries of
-    a sequence's table row are pages, and how many entries name a page; taken as they are,
+    a sequence's table row are pages, and how many entries name a page (a page that something
+    else holds would be moved by compact without its knowledge); taken as they are,
     with dec's table and seq_len, if given. Otherwise the pool starts empty: every page
     free, every table entry -1, every length 0.
 
@@ -24,8 +25,9 @@ class PagePool:
     Tokens go behind the length (write_layer) once reserve has given them their pages.
 
     Sequences are given as a list or a tensor; lists are checked on the host, int32 tensors
-    on the device are checked there (dec.device_status). Calls are asynchronous on `stream`
-    and have to be ordered among themselves and with what uses the table.
+    on the device are checked there (dec.device_status) and are what a captured step needs.
+    Calls are asynchronous on `stream` and have to be ordered among themselves and with what
+    uses the table.
     """
 
     def __init__(self, dec, *, held=None, refs=None):
@@ -52,6 +54,14 @@ class PagePool:
         pad = [None] * (4 - len(arrays)), [0] * (4 - len(arrays))
         self.c = N.fastocr_pool(dec.block_table.data_ptr(), dec.seq_len.data_ptr(), held.data_ptr(), refs.data_ptr(),
                                 dec.num_pages, *arrays, *pad[0], *steps, *pad[1], self.ws.data_ptr(), n)
+
+    def _on(self, stream):
+        """Makes `stream` (a torch stream, a raw one, None: the current one) the current stream, so
+        that what a call copies or fills for the library comes before it and is not reused under it."""
+        if isinstance(stream, int):   # 0 is the default stream, which ExternalStream does not know
+            dev = self.dec.k_cache.device
+            stream = torch.cuda.ExternalStream(stream, dev) if stream else torch.cuda.default_stream(dev)
+        return torch.cuda.stream(stream)
 
     def _indices(self, x, name, bound):
         """[n] int32 on the device, and the host's copy if x was there."""
@@ -90,22 +100,27 @@ class PagePool:
         if rows is None:
             if extra < 0:
                 raise ValueError("extra must not be negative")
-        else:
+            N.fastocr_pool_reserve(self.dec.handle, self.c, None, extra, self.missing, stream)
+            return
+        with self._on(stream):
             rows = self.dec._per_sequence(rows, "rows")
-        N.fastocr_pool_reserve(self.dec.handle, self.c, rows, extra or 0, self.missing, stream)
+            N.fastocr_pool_reserve(self.dec.handle, self.c, rows, 0, self.missing, stream)
 
     def fork(self, src, dst, stream=None):
         """Sequences dst[i] become copies of src[i] that share its pages; what they held is
-        released. reserve copies a shared page before one of them writes to it."""
-        a, b = self._pairs(src, dst, self.dec.batch)
-        if a.numel():
-            N.fastocr_pool_fork(self.dec.handle, self.c, a, b, a.numel(), stream)
+        released. reserve copies a shared page before one of them writes to it; evict_step moves
+        rows in place, so what is shared has to lie in its protected rows."""
+        with self._on(stream):
+            a, b = self._pairs(src, dst, self.dec.batch)
+            if a.numel():
+                N.fastocr_pool_fork(self.dec.handle, self.c, a, b, a.numel(), stream)
 
     def release(self, seqs, stream=None):
         """Sequences give up their pages; their length is 0."""
-        s, _ = self._indices(seqs, "seqs", self.dec.batch)
-        if s.numel():
-            N.fastocr_pool_release(self.dec.handle, self.c, s, s.numel(), stream)
+        with self._on(stream):
+            s, _ = self._indices(seqs, "seqs", self.dec.batch)
+            if s.numel():
+                N.fastocr_pool_release(self.dec.handle, self.c, s, s.numel(), stream)
 
     def trim(self, stream=None):
         """Every sequence gives up the pages behind its rows."""
@@ -118,6 +133,7 @@ class PagePool:
 
     def copy_pages(self, src, dst, stream=None):
         """Page src[i] to dst[i] in every layer; tables and references stay."""
-        a, b = self._pairs(src, dst, self.dec.num_pages)
-        if a.numel():
-            N.fastocr_pool_copy(self.dec.handle, self.c, a, b, a.numel(), stream)
+        with self._on(stream):
+            a, b = self._pairs(src, dst, self.dec.num_pages)
+            if a.numel():
+                N.fastocr_pool_copy(self.dec.handle, self.c, a, b, a.numel(), stream)

@@ -435,8 +435,9 @@ fastocr_status fastocr_cross_attend(fastocr_handle* h, const void* q, const fast
  * that has a NaN or an infinity becomes NaN. rotary NULL: nothing turns, q is copied.
  * Tokens behind start[B], and their q_out, are left alone. A token of a sequence with fewer
  * rows than tokens (FASTOCR_DEV_BAD_GROUP), a length out of range or a bad page gets no row;
- * a position outside the table is clamped to it (FASTOCR_DEV_BAD_POSITION). A page must not
- * be written through two sequences' tables at once. K and V are written although
+ * a position outside the table is clamped to it (FASTOCR_DEV_BAD_POSITION). A row must not
+ * be written twice by one call (a page in two sequences' tables, or a ring of pages shorter
+ * than the tokens): which token it then holds is unspecified. K and V are written although
  * fastocr_kv has them const.
  * Overlap: everything is read after the preceding kernel completes. With start NULL only
  * rows N_b - 1 are written, as the attention calls expect of the kernel before them; with

@@ -84,6 +84,53 @@ def test_gather(heads, flags):
     assert dec.device_status() == 0
 
 
+@pytest.mark.parametrize("splits", [0, 1])
+def test_gather_of_a_list_in_several_rounds(splits):
+    from dynamic_sparse_kv_gb300 import _native as N
+    hq, hkv, d, n, kept = 8, 1, 64, 6100, 4600
+    c = Fp4Paged([n], hkv, d, 16, 26)
+    dec = c.decoder(hq, img_range=torch.tensor([[700, 5000]]), max_img=5000, splits={1: splits})
+    idx = 700 + torch.randperm(5000, generator=torch.Generator().manual_seed(27))[:kept].to(torch.int32)
+    q = queries(1, hq, d, 28)
+    out = torch.full_like(q, float("nan"))
+    N.fastocr_sparse_attend(dec.handle, q, dec.kv[0], dec.img_range, idx.cuda()[None], kept,
+                            torch.full((1,), kept, dtype=torch.int32, device="cuda"), out)
+    check(c, q, out, lambda b: [*range(700), *idx.tolist(), *range(5700, n)])
+    assert dec.device_status() == 0
+
+
+def test_steps_of_a_stack_hand_the_selection_on():
+    """Three layers, the middle one focal: the last gathers its selection, the first the one of
+    the step before (staged early, and found to be another when it is)."""
+    from dynamic_sparse_kv_gb300 import DecodeAttention, Fp4Cache
+    hq, hkv, d, n, start, n_img, tau = 28, 4, 128, 700, 30, 512, 0.1
+    c = Fp4Paged([n, n], hkv, d, 16, 29)
+    caches = []
+    for w in range(2):
+        p = c.codes[w].shape[0]
+        x = Fp4Cache(3, p, hkv, 16, d, gain=torch.from_numpy(c.gain[w]).expand(3, -1), device="cuda")
+        x.codes.copy_(torch.from_numpy(c.codes[w]).expand(3, -1, -1, -1, -1))
+        x.scales.view(torch.uint8).copy_(torch.from_numpy(c.scales[w]).expand(3, -1, -1, -1, -1))
+        caches.append(x)
+    dec = DecodeAttention(*caches, c.table.cuda(), q_heads=hq, img_range=torch.tensor([[start, n_img]] * 2),
+                          max_img=n_img, tau=tau)
+    dec.set_focal_layers([1])
+    last = None
+    for t in range(4):
+        dec.set_seq_len(n - 3 + t)
+        q = torch.stack([queries(2, hq, d, 30 + 3 * t + l) for l in range(3)])
+        out = torch.full_like(q, float("nan"))
+        dec.step(q, out)
+        sel = [dec.sel[1][0][b, :int(dec.sel[1][1][b])].tolist() for b in range(2)]
+        text = [*range(start), *range(start + n_img, n - 3 + t)]
+        every = list(range(n - 3 + t))
+        check(c, q[0], out[0], lambda b: every if last is None else text + last[b])
+        check(c, q[1], out[1], lambda b: every)
+        check(c, q[2], out[2], lambda b: text + sel[b])
+        last = sel
+    assert dec.device_status() == 0
+
+
 @pytest.mark.parametrize("heads", HEADS)
 @pytest.mark.parametrize("splits", [0, 1, 5])
 def test_focal_selection_scores_and_profile(heads, splits):

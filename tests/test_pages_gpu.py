@@ -244,3 +244,31 @@ def test_pages_freed_by_an_eviction():
     assert int((table >= 0).sum()) == 11 and int(pool.refs.sum()) == 11 and int(pool.refs.max()) == 1
     pool.reserve(extra=40)
     assert pool.held.tolist() == [6, 6, 5] and dec.device_status() == 0
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_lists_and_numbers_on_another_stream(raw):
+    """What a call makes of its arguments is made on the stream that it runs on."""
+    t = Both(4, 60)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    given = s.cuda_stream if raw else s
+    busy = torch.zeros(64 << 20, device="cuda")
+    for rows in (40, 90, 100):
+        for _ in range(20):
+            busy.add_(1)                       # the current stream is late
+        t.pool.reserve(rows, stream=given)
+        t.pool.reserve(torch.tensor([rows, 0, rows, 1]), stream=given)
+        t.m.reserve([rows] * 4)
+    t.pool.release([1], stream=given)
+    t.m.release([1])
+    with torch.cuda.stream(s):
+        t.set_len([100, 0, 77, 100])
+    t.pool.fork([2], [1], stream=given)
+    t.m.fork([2], [1])
+    t.pool.trim(stream=given)
+    t.m.trim()
+    t.pool.compact(stream=given)
+    t.m.compact()
+    s.synchronize()
+    t.check()
