@@ -1220,6 +1220,8 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
       key.load(stage_of(0), stage_of(0) + 2 * kTile * ROWB, lane);
       keys_fp4();
     }
+    // in turns of ST tiles, whose stages are then constants (64 sequences x 8.4k 70 -> 66 us)
+#pragma unroll 4
     for (int it = 0; it < my_tiles; ++it) {
       const uint32_t here = stage_of(it), next = stage_of(it + 1);
       const int jn = it + ST - 1;   // tiles below `first` were staged already

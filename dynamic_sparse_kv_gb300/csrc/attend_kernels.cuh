@@ -452,13 +452,13 @@ inline int choose_splits(long units, long len, int max_splits, const int* active
 }
 
 // The same for a cache in 4 bits, whose CTAs (8 warps) are bound by their own instructions:
-// a turn of 8 tiles (128 tokens) takes ~0.66 us where a CTA has its SM to itself and
-// ~1.0 us where two share one. spread[s] = clusters of s CTAs that the device holds at
+// a turn of 8 tiles (128 tokens) takes ~0.56 us where a CTA has its SM to itself and
+// ~0.95 us where two share one. spread[s] = clusters of s CTAs that the device holds at
 // one CTA an SM; what fits in those also lets the next kernel's CTAs begin (the ~2 us
 // between the fixed costs). Fitted to forced split counts in chains of layers (4 to 512
 // units of 600 to 16.5k tokens, groups of 7 and of 1): on 15 shapes the choice is the
-// fastest or within 2 % (4 % on one). CTAs of half the size, up to four an SM, fill the SMs more
-// evenly but do less in each: 160 units of 2752 tokens 22.6 us instead of 25.5, 400 of 2700
+// fastest or within 2 %. CTAs of half the size, up to four an SM, fill the SMs more evenly
+// but do less in each: 160 units of 2752 tokens took 22.6 us instead of 25.5, 400 of 2700
 // 43.8 instead of 40.0, 16 of 8.4k 13.2 instead of 10.8, so there is one size.
 inline int choose_splits_fp4(long units, long len, int max_splits, const int* active, const int* spread) {
   int best = 1;
@@ -468,7 +468,7 @@ inline int choose_splits_fp4(long units, long len, int max_splits, const int* ac
     if (act < 1) continue;
     const double turns = (double)(((len + s - 1) / s + 127) / 128);
     auto wave_us = [&](long clusters) {
-      return clusters <= spread[s] ? 3.5 + 0.66 * turns : 5.5 + 1.0 * turns;
+      return clusters <= spread[s] ? 3.5 + 0.56 * turns : 5.5 + 0.95 * turns;
     };
     const long full = units / act, rest = units % act;
     const double cost = full * wave_us(act) + (rest ? wave_us(rest) : 0.0) + 0.25 * log2((double)s);

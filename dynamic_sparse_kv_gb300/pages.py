@@ -7,6 +7,8 @@ are fine.
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import _native as N
@@ -58,6 +60,8 @@ class PagePool:
     def _on(self, stream):
         """Makes `stream` (a torch stream, a raw one, None: the current one) the current stream, so
         that what a call copies or fills for the library comes before it and is not reused under it."""
+        if stream is None:
+            return contextlib.nullcontext()
         if isinstance(stream, int):   # 0 is the default stream, which ExternalStream does not know
             dev = self.dec.k_cache.device
             stream = torch.cuda.ExternalStream(stream, dev) if stream else torch.cuda.default_stream(dev)
