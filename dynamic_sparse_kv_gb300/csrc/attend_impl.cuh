@@ -624,7 +624,20 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
                    : -1;
     fetch_tiles(k + 1);
   };
-  const int code_at = lane * 16, scale_at = (lane & (kTile - 1)) * SM::kScaleBytes;
+  // What a lane adds to a tile's first row and to a stage, formed once and kept: a tile's copies
+  // and loads are then one addition each, or none (formed in every tile 32 sequences x 8.4k
+  // took 37.6 us instead of 36.2)
+  unsigned long long k_at = (unsigned long long)(kg + lane * 16), v_at = (unsigned long long)(vg + lane * 16);
+  unsigned long long scale_at = (unsigned long long)(scale_lane + (lane & (kTile - 1)) * SM::kScaleBytes);
+  uint32_t code_to = smem_u32(pipe) + lane * 16;
+  uint32_t scale_to = smem_u32(pipe) + 2 * kTile * ROWB + lane * SM::kScaleBytes;
+  if constexpr (kDirect) {
+    keep(k_at);
+    keep(v_at);
+    keep(scale_at);
+    keep(code_to);
+    keep(scale_to);
+  }
   // copies tile j of a list of n_list entries: rows that lie together (every lane's addresses
   // are one row's plus a constant), or others one by one (entry `lane % 16` is looked up by
   // this lane). Bulk copies of the former, four a tile and a barrier for them, measured
@@ -633,18 +646,19 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
     const int stage = j % ST;
     const int row0 = __shfl_sync(0xffffffffu, tile_row, j & 31);
     if (row0 >= 0) {
-      const uint32_t sb = smem_u32(pipe + stage * SM::kStageBytes);
-      const size_t row = (uint32_t)row0;
-      const char* k = kg + code_at + row * ROWB;
-      const char* v = vg + code_at + row * ROWB;
+      const unsigned long long row = (uint32_t)row0;
+      const char* k = reinterpret_cast<const char*>(k_at + row * ROWB);
+      const char* v = reinterpret_cast<const char*>(v_at + row * ROWB);
+      const uint32_t to = code_to + stage * SM::kStageBytes;
 #pragma unroll
       for (int i = 0; i < kIss; ++i) {
-        cp_async16(sb + doff[i], k + i * 512, 16, pol_stream);
-        cp_async16(sb + doff[i] + kTile * ROWB, v + i * 512, 16, pol_stream);
+        cp_async16(to + i * 512, k + i * 512, 16, pol_stream);
+        cp_async16(to + i * 512 + kTile * ROWB, v + i * 512, 16, pol_stream);
       }
       if constexpr (kFp4)
-        cp_async_small<SM::kScaleBytes>(sb + 2 * kTile * ROWB + lane * SM::kScaleBytes,
-                                        scale_lane + scale_at + row * SM::kScaleBytes, SM::kScaleBytes, pol_stream);
+        cp_async_small<SM::kScaleBytes>(scale_to + stage * SM::kStageBytes,
+                                        reinterpret_cast<const uint8_t*>(scale_at + row * SM::kScaleBytes),
+                                        SM::kScaleBytes, pol_stream);
       whole |= 1u << stage;
       return;
     }
@@ -708,6 +722,9 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
   // all their page lookups in one round. Then every whole tile of this warp
   // that the pipeline holds, up to but excluding the current token's.
   const int n_txt0 = min(n_txt_pad, kSliceMax);
+  // 4 bits: all but one stage, as in the loop, which then need not ask whether a tile is staged
+  // already (32 sequences x 8.4k 36.0 us and 35.2)
+  constexpr int kAhead = kFp4 ? ST - 1 : ST;
   int pre_issued = 0;   // leading tiles of this warp already staged
   int spec_u1 = n_txt_pad;   // selection entries read before the wait: [n_txt_pad, spec_u1)
   if (MODE == kSparse && !sel_pending) {
@@ -819,7 +836,7 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
     }
     take_tiles(0);
 #pragma unroll 1
-    for (int j = 0; j < ST; ++j)
+    for (int j = 0; j < kAhead; ++j)
       if (pre_issued == j && (warp + j * kWarps + 1) * kTile <= n_pre) {
         stage_tile(j, n_pre);
         cp_async_commit();
@@ -829,7 +846,7 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
     __syncthreads();
   }
 #pragma unroll 1
-  for (int j = 0; j < (kDirect ? 0 : ST); ++j) {
+  for (int j = 0; j < (kDirect ? 0 : kAhead); ++j) {
     const int end = (warp + j * kWarps + 1) * kTile;
     if (pre_issued == j && end <= n_pre) {
       issue(j, n_pre);
@@ -847,7 +864,7 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
   // the speculation fails).
   if (c.has_cur && (kDirect || n_pre < kSliceMax) && !sel_pending) {
     const int t_cur = n_pre / kTile;   // n_pre is a multiple of kTile here
-    if (warp == t_cur % kWarps && pre_issued == t_cur / kWarps && pre_issued < ST) {
+    if (warp == t_cur % kWarps && pre_issued == t_cur / kWarps && pre_issued < kAhead) {
       if constexpr (kDirect)
         stage_tile(pre_issued, n_pre + 1);
       else
@@ -1126,18 +1143,17 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
   float mb0 = kUnset, mb1 = kUnset;
   Fp4Keys<D> key;        // of the next tile
   Fp4Values<D> value;    // of this one
-  float cc[2][4];   // S^T of the next tile in two accumulations, added where they are needed:
-                    // an addition here would hold the warp until the last product is done
+  float cc[4];           // S^T of the next tile
   auto keys_fp4 = [&]() {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) cc[0][e] = cc[1][e] = 0.f;
+    for (int e = 0; e < 4; ++e) cc[e] = 0.f;
     key.product(sm_.qf, cc);
   };
   // P^T of the tile as B fragments
   auto probabilities_fp4 = [&](int it, int n_list, uint32_t& bb0, uint32_t& bb1) {
     float cfr[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) cfr[e] = cc[0][e] + cc[1][e];
+    for (int e = 0; e < 4; ++e) cfr[e] = cc[e];
     constexpr bool kPositions = stores_logits(MODE) || MODE == kProfile;
     const bool whole_tile = whole >> (it % ST) & 1u;
     // positions of rows gid and gid + 8 of the fragments, negative for a masked one (the modes
@@ -1207,33 +1223,34 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
     bb1 = movmatrix_trans(pack_f16(p2, p3));
   };
 
-  // Tiles [0, my_tiles) of this warp, `first` of them staged already, through the pipeline,
+  // Tiles [0, my_tiles) of this warp, the first ST - 1 of them staged already, through the pipeline,
   // for a cache in 4 bits. Software pipelined like the deep variant below, in the order
-  // that hides most: the raw codes of the next tile's keys and of this tile's values are
-  // loaded first, this tile's probabilities (exponentials and a transposition to wait for)
+  // that hides most: the raw codes of the next tile's keys are loaded first, this tile's
+  // probabilities (exponentials and a transposition to wait for) and the loads of its values
   // come before the next tile's first product, and its own second product last.
-  auto stream_fp4 = [&](int my_tiles, int first, int n_list, auto&& issue_tile) {
-    auto stage_of = [&](int it) { return smem_u32(pipe + (it % ST) * SM::kStageBytes); };
+  auto stream_fp4 = [&](int my_tiles, int n_list, auto&& issue_tile) {
+    Fp4Places<D> at(smem_u32(pipe), smem_u32(pipe) + 2 * kTile * ROWB, lane);
+    auto stage_of = [&](int it) { return (uint32_t)((it % ST) * SM::kStageBytes); };
     if (my_tiles > 0) {
       cp_async_wait<ST - 2>();
       __syncwarp();
-      key.load(stage_of(0), stage_of(0) + 2 * kTile * ROWB, lane);
+      key.load(at, stage_of(0));
       keys_fp4();
     }
-    // in turns of ST tiles, whose stages are then constants (64 sequences x 8.4k 70 -> 66 us)
+    // in turns of ST tiles, whose stages are then constants (64 sequences x 8.4k took 66.2 us
+    // instead of 70.3, and 60.3 with places that are kept)
 #pragma unroll 4
     for (int it = 0; it < my_tiles; ++it) {
-      const uint32_t here = stage_of(it), next = stage_of(it + 1);
-      const int jn = it + ST - 1;   // tiles below `first` were staged already
-      if (jn >= first && jn < my_tiles) issue_tile(jn);
+      const int jn = it + ST - 1;
+      if (jn < my_tiles) issue_tile(jn);
       cp_async_commit();
       cp_async_wait<ST - 2>();
       __syncwarp();
       // past the last tile this reads a stage no copy is writing; unused
-      key.load(next, next + 2 * kTile * ROWB, lane);
-      value.load(here + kTile * ROWB, here + kTile * (2 * ROWB + SM::kScaleBytes), lane);
+      key.load(at, stage_of(it + 1));
       uint32_t bb0, bb1;
       probabilities_fp4(it, n_list, bb0, bb1);
+      value.load(at, stage_of(it));
       keys_fp4();
       value.product(bb0, bb1, sm_.acc);
       __syncwarp();
@@ -1247,7 +1264,7 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
       if (j < my_tiles) stage_tile(j, n_cta);
       cp_async_commit();
     }
-    stream_fp4(my_tiles, pre_issued, n_cta, [&](int jn) {
+    stream_fp4(my_tiles, n_cta, [&](int jn) {
       if ((jn & 31) == 0) take_tiles(jn / 32);
       stage_tile(jn, n_cta);
     });
@@ -1272,7 +1289,7 @@ __global__ void __launch_bounds__(32 * warps_for(V), ctas_per_sm(V)) attend_kern
       cp_async_commit();
     }
     if constexpr (kFp4) {
-      stream_fp4(my_tiles, first, n_round, [&](int jn) { issue(jn, n_round); });
+      stream_fp4(my_tiles, n_round, [&](int jn) { issue(jn, n_round); });
     } else if constexpr (kMma && ST >= 4) {
       // Software pipelined (deep variant): the next tile's QK^T is issued
       // before this tile's softmax and PV, keeping ST-2 tiles in flight.

@@ -169,6 +169,9 @@ struct Params {
 
 // ---------------------------------------------------------------- PTX helpers
 
+// Keeps x in a register: the compiler does not form it again where it is used.
+__device__ __forceinline__ void keep(uint32_t& x) { asm volatile("" : "+r"(x)); }
+__device__ __forceinline__ void keep(unsigned long long& x) { asm volatile("" : "+l"(x)); }
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }

@@ -140,7 +140,7 @@ __device__ __forceinline__ uint32_t pack_codes(const float x[8], float gain, uin
   asm("{\n .reg .b16 t;\n cvt.rn.satfinite.e4m3x2.f32 t, 0f00000000, %1;\n cvt.u32.u16 %0, t;\n}\n"
       : "=r"(s)
       : "f"(plain ? quotient(top, 6.f, 1.f / 6.f) : __fdiv_rn(top, 6.f)));
-  const float sf = unpack_f16(e4m3_pair(s)).x;
+  const float sf = __low2float(e4m3_pair(s));
   float y[8];
   if (plain) {   // the same for the group
     const float rs = reciprocal(fmaxf(sf, 0x1p-9f));
@@ -564,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 6) read_kernel(const ReadParams p) {
         if (i >= 2 * c.Hkv) break;
         const bool is_v = i >= c.Hkv;
         if constexpr (Held<T>::kFp4) {
-          const float s = unpack_f16(e4m3_pair(scale[u])).x;
+          const float s = __low2float(e4m3_pair(scale[u]));
           uint32_t v[4];
           fp4_decode8(code[u], v);
 #pragma unroll

@@ -39,8 +39,8 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 __device__ __forceinline__ float2 unpack_f16(uint32_t x) {
   return __half22float2(*reinterpret_cast<const __half2*>(&x));
 }
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, __half2 b) {
+  const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&a), b);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
@@ -52,10 +52,10 @@ __device__ __forceinline__ void fp4_decode8(uint32_t w, uint32_t h[4]) {
       : "r"(w));
 }
 // Two e4m3 in the low 16 bits as a pair of fp16.
-__device__ __forceinline__ uint32_t e4m3_pair(uint32_t x) {
+__device__ __forceinline__ __half2 e4m3_pair(uint32_t x) {
   uint32_t h;
   asm("{\n .reg .b16 a;\n cvt.u16.u32 a, %1;\n cvt.rn.f16x2.e4m3x2 %0, a;\n}\n" : "=r"(h) : "r"(x));
-  return h;
+  return *reinterpret_cast<const __half2*>(&h);
 }
 
 // This lane's share of query row q (head gid) as fp16 fragments, divided by a power of
@@ -90,41 +90,62 @@ __device__ __forceinline__ float fp4_query(const __nv_bfloat16* q, bool have, ui
   return __uint_as_float(e << 23);
 }
 
-// A lane's share of a tile's K as it lies: codes of rows fp4_key(gid) and 8 further, their
-// scales (two groups each at d = 128, one at 64). Loading and using are apart so that the
-// loads' latency passes under other work.
+// Where a lane finds its share of a tile in stage 0, formed once and kept. K: codes of row
+// fp4_key(gid) and its scales (8 rows further: a constant further); V: codes of dims D/8 gid ..
+// of keys fp4_key(2 tig), fp4_key(2 tig + 1), and their scales.
+template <int D>
+struct Fp4Places {
+  uint32_t key, key_scale, value[2], value_scale[2];
+
+  __device__ __forceinline__ Fp4Places(uint32_t codes, uint32_t scales, int lane) {
+    const int gid = lane >> 2, tig = lane & 3;
+    const int r = fp4_key(gid);
+    key = codes + fp4_place<D>(r, 0) + tig * (D / 8);
+    key_scale = scales + r * (D / 16) + tig * (D / 64);
+    keep(key);
+    keep(key_scale);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int n = 16 + fp4_key(2 * tig + j);   // V lies behind the 16 rows of K
+      value[j] = codes + fp4_place<D>(n, 0) + gid * (D / 16);
+      value_scale[j] = scales + n * (D / 16) + gid * (D / 64) / 2;
+      keep(value[j]);
+      keep(value_scale[j]);
+    }
+  }
+};
+
+// A lane's share of a tile's K as it lies, from the stage `stage` bytes further. Loading and
+// using are apart so that the loads' latency passes under other work.
 template <int D>
 struct Fp4Keys {
   static constexpr int W = D / 32;
   uint32_t w0[W], w1[W];
-  uint32_t a, b;   // scales of either row
+  uint32_t a, b;   // scales of either row (two groups each at d = 128, one at 64)
 
-  __device__ __forceinline__ void load(uint32_t kA, uint32_t sA, int lane) {
-    const int gid = lane >> 2, tig = lane & 3;
-    const int r0 = fp4_key(gid);
+  __device__ __forceinline__ void load(const Fp4Places<D>& at, uint32_t stage) {
+    const uint32_t c = at.key + stage, s = at.key_scale + stage;
     if constexpr (D == 128) {
       asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n"
-                   : "=r"(w0[0]), "=r"(w0[1]), "=r"(w0[2]), "=r"(w0[3]) : "r"(kA + fp4_place<D>(r0, tig)));
+                   : "=r"(w0[0]), "=r"(w0[1]), "=r"(w0[2]), "=r"(w0[3]) : "r"(c));
       asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n"
-                   : "=r"(w1[0]), "=r"(w1[1]), "=r"(w1[2]), "=r"(w1[3]) : "r"(kA + fp4_place<D>(r0 + 8, tig)));
-      asm volatile("ld.shared.u16 %0, [%1];\n" : "=r"(a) : "r"(sA + r0 * 8 + 2 * tig));
-      asm volatile("ld.shared.u16 %0, [%1];\n" : "=r"(b) : "r"(sA + (r0 + 8) * 8 + 2 * tig));
+                   : "=r"(w1[0]), "=r"(w1[1]), "=r"(w1[2]), "=r"(w1[3]) : "r"(c + 8 * (D / 2)));
+      asm volatile("ld.shared.u16 %0, [%1];\n" : "=r"(a) : "r"(s));
+      asm volatile("ld.shared.u16 %0, [%1];\n" : "=r"(b) : "r"(s + 8 * (D / 16)));
     } else {
-      const uint32_t half = (tig & 1) * 8;
-      asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];\n"
-                   : "=r"(w0[0]), "=r"(w0[1]) : "r"(kA + fp4_place<D>(r0, tig >> 1) + half));
-      asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];\n"
-                   : "=r"(w1[0]), "=r"(w1[1]) : "r"(kA + fp4_place<D>(r0 + 8, tig >> 1) + half));
-      asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(a) : "r"(sA + r0 * 4 + tig));
-      asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(b) : "r"(sA + (r0 + 8) * 4 + tig));
+      asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];\n" : "=r"(w0[0]), "=r"(w0[1]) : "r"(c));
+      asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];\n" : "=r"(w1[0]), "=r"(w1[1]) : "r"(c + 8 * (D / 2)));
+      asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(a) : "r"(s));
+      asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(b) : "r"(s + 8 * (D / 16)));
     }
   }
-  // S^T = K Q^T in CHAINS independent accumulations
-  template <int CHAINS>
-  __device__ __forceinline__ void product(const uint32_t (&qf)[D / 16][2], float (&cc)[CHAINS][4]) const {
-    const uint32_t x = e4m3_pair(a), y = e4m3_pair(b);
-    const uint32_t s0[2] = {__byte_perm(x, x, 0x1010), __byte_perm(x, x, 0x3232)};
-    const uint32_t s1[2] = {__byte_perm(y, y, 0x1010), __byte_perm(y, y, 0x3232)};
+  // S^T += K Q^T, in one accumulation: two side by side (and their sum) cost more than the
+  // latency they hide (32 sequences x 8.4k 36.3 us instead of 35.5)
+  __device__ __forceinline__ void product(const uint32_t (&qf)[D / 16][2], float (&cc)[4]) const {
+    // a product takes either half twice by itself; copies of the halves (four permutations a
+    // tile) cost 32 sequences x 8.4k 38.6 us instead of 37.4
+    const __half2 x = e4m3_pair(a), y = e4m3_pair(b);
+    const __half2 s0[2] = {__low2half2(x), __high2half2(x)}, s1[2] = {__low2half2(y), __high2half2(y)};
 #pragma unroll
     for (int i = 0; i < W; ++i) {
       uint32_t h0[4], h1[4];
@@ -136,39 +157,35 @@ struct Fp4Keys {
         const int ks = 2 * i + j;
         const uint32_t f[4] = {mul_f16x2(h0[2 * j], s0[g]), mul_f16x2(h1[2 * j], s1[g]),
                                mul_f16x2(h0[2 * j + 1], s0[g]), mul_f16x2(h1[2 * j + 1], s1[g])};
-        mma_f16(cc[ks % CHAINS], f, qf[ks][0], qf[ks][1]);
+        mma_f16(cc, f, qf[ks][0], qf[ks][1]);
       }
     }
   }
 };
 
-// The same of V: codes of dims D/8 gid .. of keys fp4_key(2 tig), fp4_key(2 tig + 1) and 8
-// further, and their scales.
+// The same of V: four keys (0, 1 and 8 further), 16 dims at d = 128, 8 at 64.
 template <int D>
 struct Fp4Values {
   static constexpr int W = D / 64;
   uint32_t w[4][W];
   uint32_t s[4];
 
-  __device__ __forceinline__ void load(uint32_t vA, uint32_t sA, int lane) {
-    const int gid = lane >> 2, tig = lane & 3;
+  __device__ __forceinline__ void load(const Fp4Places<D>& at, uint32_t stage) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int r = fp4_key(2 * tig + (j & 1)) + 8 * (j >> 1);
-      if constexpr (D == 128) {
-        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];\n"
-                     : "=r"(w[j][0]), "=r"(w[j][1]) : "r"(vA + fp4_place<D>(r, gid >> 1) + (gid & 1) * 8));
-        asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(s[j]) : "r"(sA + r * 8 + gid));
-      } else {
-        asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(w[j][0]) : "r"(vA + fp4_place<D>(r, gid >> 2) + (gid & 3) * 4));
-        asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(s[j]) : "r"(sA + r * 4 + (gid >> 1)));
-      }
+      const uint32_t c = at.value[j & 1] + stage + (j >> 1) * 8 * (D / 2);
+      const uint32_t e = at.value_scale[j & 1] + stage + (j >> 1) * 8 * (D / 16);
+      if constexpr (D == 128)
+        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];\n" : "=r"(w[j][0]), "=r"(w[j][1]) : "r"(c));
+      else
+        asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(w[j][0]) : "r"(c));
+      asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(s[j]) : "r"(e));
     }
   }
   // O^T += V^T P^T, the probabilities' fragments in b0 (keys 2t, 2t + 1 of fp4_key's order) and
   // b1 (8 further). acc[mt]: dims D/8 gid + 2 mt (elements 0, 1) and the one after it (2, 3).
   __device__ __forceinline__ void product(uint32_t b0, uint32_t b1, float (&acc)[D / 16][4]) const {
-    const uint32_t s01 = e4m3_pair(s[0] | (s[1] << 8)), s23 = e4m3_pair(s[2] | (s[3] << 8));
+    const __half2 s01 = e4m3_pair(__byte_perm(s[0], s[1], 0x0040)), s23 = e4m3_pair(__byte_perm(s[2], s[3], 0x0040));
 #pragma unroll
     for (int i = 0; i < W; ++i) {
       // codes of the same dim of two keys side by side: even dims, then odd ones
