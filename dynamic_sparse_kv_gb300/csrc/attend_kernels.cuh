@@ -455,8 +455,8 @@ inline int choose_splits(long units, long len, int max_splits, const int* active
 }
 
 // The same for a cache in 4 bits, whose CTAs (8 warps) are bound by their own instructions:
-// a turn of 8 tiles (128 tokens) takes ~0.56 us where a CTA has its SM to itself and
-// ~0.95 us where two share one. spread[s] = clusters of s CTAs that the device holds at
+// a turn of 8 tiles (128 tokens) takes ~0.47 us where a CTA has its SM to itself and
+// ~0.77 us where two share one. spread[s] = clusters of s CTAs that the device holds at
 // one CTA an SM; what fits in those also lets the next kernel's CTAs begin (the ~2 us
 // between the fixed costs). Fitted to forced split counts in chains of layers (4 to 512
 // units of 600 to 16.5k tokens, groups of 7 and of 1): on 15 shapes the choice is the
@@ -471,7 +471,7 @@ inline int choose_splits_fp4(long units, long len, int max_splits, const int* ac
     if (act < 1) continue;
     const double turns = (double)(((len + s - 1) / s + 127) / 128);
     auto wave_us = [&](long clusters) {
-      return clusters <= spread[s] ? 3.5 + 0.56 * turns : 5.5 + 0.95 * turns;
+      return clusters <= spread[s] ? 5.0 + 0.47 * turns : 7.0 + 0.77 * turns;
     };
     const long full = units / act, rest = units % act;
     const double cost = full * wave_us(act) + (rest ? wave_us(rest) : 0.0) + 0.25 * log2((double)s);
