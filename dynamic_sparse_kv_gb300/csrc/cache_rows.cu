@@ -437,7 +437,8 @@ __global__ void __launch_bounds__(32 * kRingWarps, 1) write_stream_kernel(const 
     next.load(p, d, token, token < c.start[c.B] ? bad : ignored);
   };
   if (d.turns && n > 0) load_angles(first_token);
-  for (int i = 0; i < n; ++i) {
+  int i = 0;
+  for (; i < n; ++i) {
     if (i > 0 && (i & 31) == 0) look_up(i + lane);
     const long row = __shfl_sync(0xffffffffu, rows, i & 31);
     const int token = first_token + i * step, slot = i % ring.slots;
@@ -486,6 +487,11 @@ __global__ void __launch_bounds__(32 * kRingWarps, 1) write_stream_kernel(const 
     }
     __syncwarp();   // every lane has read the slot
     if (lane == 0 && i + ring.slots < n) load(i + ring.slots);
+  }
+  for (int end = min(n, i + ring.slots); i < end; ++i) {   // given up: copies under way land first, if they do
+    const long long t0 = clock64();
+    while (!ring_try(bars + i % ring.slots * 8, (i / ring.slots) & 1) && clock64() - t0 < 4000000000LL) {
+    }
   }
   if (bad) atomicOr(c.status, bad);
   __syncthreads();
@@ -564,14 +570,15 @@ __global__ void __launch_bounds__(kThreads, 6) read_kernel(const ReadParams p) {
         if (i >= 2 * c.Hkv) break;
         const bool is_v = i >= c.Hkv;
         if constexpr (Held<T>::kFp4) {
-          const float s = __low2float(e4m3_pair(scale[u]));
-          uint32_t v[4];
-          fp4_decode8(code[u], v);
+          const __half2 s = __low2half2(e4m3_pair(scale[u]));
+          uint32_t v[N / 2];
+          if constexpr (N == 8) fp4_decode8(code[u], v);
+          else fp4_decode4(code[u], v);
 #pragma unroll
           for (int e = 0; e < N / 2; ++e) {
-            const float2 y = unpack_f16(v[e]);
-            x[u][2 * e] = __fmul_rn(__fmul_rn(y.x, s), gain[u]);
-            x[u][2 * e + 1] = __fmul_rn(__fmul_rn(y.y, s), gain[u]);
+            const float2 y = unpack_f16(mul_f16x2(v[e], s));   // whole in fp16
+            x[u][2 * e] = __fmul_rn(y.x, gain[u]);
+            x[u][2 * e + 1] = __fmul_rn(y.y, gain[u]);
           }
         }
         O* dst = reinterpret_cast<O*>(is_v ? p.v_out : p.k_out) + ((long)token * c.Hkv + i - (is_v ? c.Hkv : 0)) * D + dim;

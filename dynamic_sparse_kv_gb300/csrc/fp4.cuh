@@ -51,6 +51,13 @@ __device__ __forceinline__ void fp4_decode8(uint32_t w, uint32_t h[4]) {
       : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
       : "r"(w));
 }
+// The two low ones.
+__device__ __forceinline__ void fp4_decode4(uint32_t w, uint32_t h[2]) {
+  asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %2;\n cvt.rn.f16x2.e2m1x2 %0, a;\n"
+      " cvt.rn.f16x2.e2m1x2 %1, b;\n}\n"
+      : "=r"(h[0]), "=r"(h[1])
+      : "r"(w));
+}
 // Two e4m3 in the low 16 bits as a pair of fp16.
 __device__ __forceinline__ __half2 e4m3_pair(uint32_t x) {
   uint32_t h;
