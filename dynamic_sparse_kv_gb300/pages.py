@@ -102,8 +102,8 @@ class PagePool:
         if (rows is None) == (extra is None):
             raise ValueError("give rows or extra")
         if rows is None:
-            if extra < 0:
-                raise ValueError("extra must not be negative")
+            if not 0 <= extra < 2**31:   # more would be cut to 32 bits on its way
+                raise ValueError("extra must lie in [0, 2^31)")
             N.fastocr_pool_reserve(self.dec.handle, self.c, None, extra, self.missing, stream)
             return
         with self._on(stream):

@@ -149,7 +149,7 @@ def test_pools_refuse_what_they_would_read_wrongly(calls):
     pool.reserve(5)
     pool.reserve(torch.tensor([1, 2, 3]))
     pool.reserve(extra=0)
-    for args, kw in (((), {}), ((5,), dict(extra=1)), ((), dict(extra=-1)), ((torch.zeros(2),), {})):
+    for args, kw in (((), {}), ((5,), dict(extra=1)), ((), dict(extra=-1)), ((), dict(extra=2**31)), ((torch.zeros(2),), {})):
         with pytest.raises(ValueError):
             pool.reserve(*args, **kw)
     pool.fork([0], [1])
